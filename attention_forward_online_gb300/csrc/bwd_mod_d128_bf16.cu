@@ -1,0 +1,11 @@
+// The modified-score backward at d = 128 in bf16, compiled on its own so
+// that the variants build in parallel.
+#include "bwd_mod_tcgen05.cuh"
+
+namespace osattn {
+namespace bwdmod {
+template cudaError_t prepare<128, false>();
+template cudaError_t launch<128, false>(const ModArgs&, const CUtensorMap&, const CUtensorMap&,
+                                    const CUtensorMap&, const CUtensorMap&);
+}  // namespace bwdmod
+}  // namespace osattn

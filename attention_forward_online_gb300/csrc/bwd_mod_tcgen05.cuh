@@ -1,0 +1,1151 @@
+// bwd_mod_tcgen05.cuh - gradients of the modified-score attention forward
+// (fwd_mod_tcgen05.cuh) on the tcgen05 tensor cores.  Built for sm_103a; bf16
+// or fp16, d = 64 or 128.
+//
+// With P = e^{y - LSE} on the keys a row sees, dP = dO V^T, D = rowsum(dO O):
+//   dY = P (dP - D)               (gradient of the modified score)
+//   dS = dY (1 - tanh^2)          (capped scores; dS = dY otherwise)
+//   dQ = scale dS K,  dK = scale sum dS^T Q,  dV = sum P^T dO,
+// the sums of dK and dV running over the query heads that share the key head,
+// and dTable[k][h] = sum of dY over the pairs whose distance has bucket k.
+//
+// Launches, in order on one stream:
+//   dq_kernel    one CTA per 128-row query tile; K and V tiles stream.  Also
+//                writes D, and with a learned bias the sums of dY by distance.
+//   dkdv_kernel  one CTA per 128-key tile of a key head; the query tiles of
+//                every head of its group that can see those keys stream, so
+//                the sums over heads stay in tensor memory and nothing is
+//                added by atomics: results do not depend on the order of CTAs.
+//   rel_reduce   folds the partial sums by distance into the table's buckets.
+// P and dS are rounded to 16 bits as MMA operands, everything summed in fp32.
+//
+// CTA layout (320 threads): warps 0-7 elementwise in two warpgroups, group g
+// taking columns 64g .. 64g + 63 of every score tile, one tile row a thread;
+// warp 8 TMA producer; warp 9 issues the MMAs.  Tensor memory, dkdv:
+// [0, 128) S^T, [128, 256) dP^T, then dV and dK; dq: two S buffers, dP, dQ.
+//
+// Masked places hold anything: their P and dY are selected to 0, never
+// multiplied, and rows of K (dq) or of Q and dO (dkdv) that take part in no
+// pair are zeroed in shared memory before they enter a product.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mod_common.cuh"
+#include "mod_internal.h"
+#include "sm100_ptx.cuh"
+#include "tc_attn_mma.cuh"
+
+namespace osattn {
+namespace bwdmod {
+
+constexpr int kT = 128;
+constexpr int kThreads = 320;
+constexpr int kProdWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kCols = 512;
+
+enum : uint32_t { kSiteLoad = 61, kSiteMma = 62, kSiteElem = 63, kSiteEpi = 64, kSiteSync = 65 };
+
+template <int HD, int MODE>
+struct Cfg {
+  static constexpr int kTileBytes = kT * HD * 2;
+  static constexpr int kRelBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16 : 0;
+  // dkdv: K, V, kStages stages of (Q_i, dO_i), then per stage LSE, D, lo, hi
+  static constexpr int kStages = HD == 128 ? 2 : 4;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kDkdvRows = 2 * kTileBytes + kStages * kStageBytes;
+  static constexpr int kDkdvRel = kDkdvRows + kStages * kT * 16;
+  static constexpr int kDkdvRegion = kDkdvRel + kRelBytes;
+  // dq: Q, dO, kKSlots K tiles, kVSlots V tiles (K_j is read until dQ_j, V_j
+  // until dP_j); with a learned bias the table, its sums by distance and the
+  // warps' diagonal strips take the place of the third K tile at d = 128.
+  static constexpr int kKSlots = HD == 128 ? (mode_rel(MODE) ? 2 : 3) : 4;
+  static constexpr int kVSlots = HD == 128 ? 2 : 4;
+  static constexpr int kDqRel = (2 + kKSlots + kVSlots) * kTileBytes;
+  static constexpr int kStripBytes = mode_rel(MODE) ? 2 * 8 * 96 * 4 : 0;
+  static constexpr int kDqRegion = kDqRel + 2 * kRelBytes + kStripBytes;
+  static constexpr uint32_t kColAcc0 = 256;       // dV
+  static constexpr uint32_t kColAcc1 = 256 + HD;  // dK
+};
+
+struct __align__(16) Bars {
+  uint64_t fixed_full;
+  uint64_t full[4];
+  uint64_t empty[4];
+  uint64_t empty2[4];
+  uint64_t s_full[2];
+  uint64_t dp_full;
+  uint64_t p_full;
+  uint64_t ds_full;
+  uint64_t acc_full;
+  uint64_t mma_drain;
+  uint64_t d_full;
+  uint64_t elem;
+  uint32_t tmem_base;
+  int abort_flag;
+  int it_lo, it_hi;
+  float d_part[2][kT];
+  float far_part[2][8];
+};
+
+template <int HD, int MODE>
+constexpr int dkdv_smem_bytes() {
+  return Cfg<HD, MODE>::kDkdvRegion + static_cast<int>(sizeof(Bars)) + 1024;
+}
+template <int HD, int MODE>
+constexpr int dq_smem_bytes() {
+  return Cfg<HD, MODE>::kDqRegion + static_cast<int>(sizeof(Bars)) + 1024;
+}
+
+struct Params {
+  uint16_t* dQ;
+  uint16_t* dK;
+  uint16_t* dV;
+  long long dq_s[3], dk_s[3], dv_s[3];
+  const float* LSE;
+  float* D;
+  const uint16_t* O;
+  long long o_s[3];
+  PlanView plan;
+  int H, Hkv, group, Nq, Nkv;
+  int q_tiles;      // 128-row query tiles per (b, h)
+  int num_tiles;    // this kernel's tiles per head
+  int BH;           // this kernel's heads: B * H (dq) or B * Hkv (dkdv)
+  int group_heads;  // heads per last-tile-first (dq) or first-tile-first (dkdv) group of CTAs
+  float scale;
+  float scale_log2;
+  float cap_c1, cap2;
+  const float* slopes;
+  RelArgs rel;
+  float* rel_part;
+  int q_offset;
+  unsigned int* status;
+  uint64_t wait_limit_ns;
+};
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kF16) return pack_f16x2(lo, hi);
+  else return pack_bf16x2(lo, hi);
+}
+
+template <bool kF16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if constexpr (kF16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) return;
+  }
+}
+
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t tx_bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(tx_bytes)
+               : "memory");
+}
+
+// Barrier over the 256 elementwise threads, bounded like every other wait
+// (a warp that gave up elsewhere must not leave the rest waiting).  phase
+// counts the barrier's uses; false: give up.
+__device__ __forceinline__ bool elem_sync(Bars* bars, uint32_t& phase, const WaitCtl& wc) {
+  mbar_arrive(&bars->elem);
+  const bool ok = mbar_wait(&bars->elem, phase & 1u, wc, kSiteSync);
+  ++phase;
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The head and the rank by length (0 = longest under a causal mask) of this
+// CTA's tile: heads in groups whose streamed tiles fit in L2 together.
+__device__ __forceinline__ void unit_of(const Params& p, int& bh, int& rank) {
+  const int nt = p.num_tiles, G = p.group_heads;
+  const int g0 = (static_cast<int>(blockIdx.x) / (G * nt)) * G;
+  const int gsize = min(G, p.BH - g0);
+  const int r = static_cast<int>(blockIdx.x) - g0 * nt;
+  bh = g0 + r % gsize;
+  rank = r / gsize;
+}
+
+template <int NC, bool kF16>
+__device__ __forceinline__ void write_row(uint16_t* dst, uint32_t taddr, bool has_acc, bool store,
+                                          float mul) {
+#pragma unroll
+  for (int ch = 0; ch < NC / 32; ++ch) {
+    uint32_t r[32];
+    if (has_acc) {
+      tmem_ld_32x32b_x32(taddr + ch * 32, r);
+      tmem_ld_wait();
+      reg_fence32(r);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) r[e] = 0u;
+    }
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      pk[e] = pack2<kF16>(__uint_as_float(r[2 * e]) * mul, __uint_as_float(r[2 * e + 1]) * mul);
+    if (store) {
+      uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+    }
+  }
+}
+
+// Zeroes row `row` of a 128-row tile in shared memory, column block cb only.
+__device__ __forceinline__ void zero_row(uint8_t* tile, int cb, int row) {
+  uint4* r = reinterpret_cast<uint4*>(tile + cb * kT * 128 + row * 128);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) r[x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// P part over the 64 columns of this thread's group at tile column c0:
+// P = 2^(x - LSE log2 e) with x the modified score; kMask selects 0 where
+// vis(column) is false.  nl2of4(column): -LSE log2 e of 4 columns.
+// dist(column) = key position less query position of that entry (slopes),
+// bias(column) = the learned bias in base-2 units.  kWriteP writes the 16-bit
+// P over columns c0 .. c0 + 31.  On return pr holds what dS is made of:
+// P, times 1 - tanh^2 = 4 r (1 - r) where scores are capped.
+template <bool kF16, int MODE, bool kWriteP, bool kMask, typename Vis, typename L2of4, typename Dist,
+          typename Bias>
+__device__ __forceinline__ void p_part(uint32_t s_addr, int c0, const Params& p, float slope2, Vis&& vis,
+                                       L2of4&& nl2of4, Dist&& dist, Bias&& bias, float (&pr)[64]) {
+  uint32_t sa[32], sb[32];
+  tmem_ld_32x32b_x32(s_addr + c0, sa);
+  tmem_ld_wait();
+  reg_fence32(sa);
+  tmem_ld_32x32b_x32(s_addr + c0 + 32, sb);
+  auto half = [&](const uint32_t(&sv)[32], int h) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const float4 L = nl2of4(c0 + 32 * h + 4 * g);
+      const float nl[4] = {L.x, L.y, L.z, L.w};
+      float e[4], f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int col = c0 + 32 * h + 4 * g + u;
+        const float s = __uint_as_float(sv[4 * g + u]);
+        float x = nl[u];
+        if constexpr (mode_slopes(MODE)) x = fmaf(-slope2, fabsf(dist(col)), x);
+        if constexpr (mode_rel(MODE)) x += bias(col);
+        if constexpr (mode_cap(MODE)) {
+          const float r = cap_r(s, p.cap_c1);
+          x += fmaf(r, -2.f * p.cap2, p.cap2);
+          f[u] = 4.f * r * (1.f - r);
+        } else {
+          x = fmaf(s, p.scale_log2, x);
+        }
+        e[u] = ex2_approx(x);
+        if constexpr (kMask) e[u] = vis(col) ? e[u] : 0.f;
+      }
+      if constexpr (kWriteP) {
+        pk[2 * g] = pack2<kF16>(e[0], e[1]);
+        pk[2 * g + 1] = pack2<kF16>(e[2], e[3]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float v = e[u];
+        if constexpr (mode_cap(MODE)) {
+          v = e[u] * f[u];
+          if constexpr (kMask) v = e[u] == 0.f ? 0.f : v;  // a masked score may be NaN
+        }
+        pr[32 * h + 4 * g + u] = v;
+      }
+    }
+    if constexpr (kWriteP) tmem_st_32x32b_x16(s_addr + c0 + 16 * h, pk);
+  };
+  half(sa, 0);
+  tmem_ld_wait();
+  reg_fence32(sb);
+  half(sb, 1);
+}
+
+// dS part over the same 64 columns of the dP tile: dS = pr (dP - D), in 16
+// bits over columns c0 .. c0 + 31; ndof4(column): -D of 4 columns.  kMask: a
+// masked place (pr = 0) gives 0 whatever dP and D are.  kKeep: pr returns dS.
+template <bool kF16, bool kMask, bool kKeep, typename Dof4>
+__device__ __forceinline__ void ds_part(uint32_t dp_addr, int c0, Dof4&& ndof4, float (&pr)[64]) {
+  uint32_t dva[32], dvb[32];
+  tmem_ld_32x32b_x32(dp_addr + c0, dva);
+  tmem_ld_wait();
+  reg_fence32(dva);
+  tmem_ld_32x32b_x32(dp_addr + c0 + 32, dvb);
+  auto chunk = [&](const uint32_t(&dv)[32], int ch) {
+    uint32_t gk[16];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const float4 D = ndof4(c0 + 32 * ch + 4 * g);
+      const int x = 32 * ch + 4 * g;
+      const uint64_t d01 = f2_add(
+          f2_pack(__uint_as_float(dv[4 * g]), __uint_as_float(dv[4 * g + 1])), f2_pack(D.x, D.y));
+      const uint64_t d23 = f2_add(
+          f2_pack(__uint_as_float(dv[4 * g + 2]), __uint_as_float(dv[4 * g + 3])), f2_pack(D.z, D.w));
+      float gr[4];
+      f2_unpack(f2_mul(f2_pack(pr[x], pr[x + 1]), d01), gr[0], gr[1]);
+      f2_unpack(f2_mul(f2_pack(pr[x + 2], pr[x + 3]), d23), gr[2], gr[3]);
+      if constexpr (kMask) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) gr[u] = pr[x + u] == 0.f ? 0.f : gr[u];
+      }
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pr[x + u] = gr[u];
+      }
+      gk[2 * g] = pack2<kF16>(gr[0], gr[1]);
+      gk[2 * g + 1] = pack2<kF16>(gr[2], gr[3]);
+    }
+    tmem_st_32x32b_x16(dp_addr + c0 + 16 * ch, gk);
+  };
+  chunk(dva, 0);
+  tmem_ld_wait();
+  reg_fence32(dvb);
+  chunk(dvb, 1);
+}
+
+// D (128 x N fp32) (+)= A B over 128 inner elements, A the 16-bit operand the
+// two warpgroups wrote (elements 0-63 in columns 0-31 of a_tmem, 64-127 in
+// 64-95), B an MN-major tile.
+template <int N, bool kF16>
+__device__ __forceinline__ void mma_groups(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           bool accumulate) {
+  constexpr uint32_t id = idesc_f16_f32(128, N, 1, kF16);
+  mma_bf16_ts<true>(d_tmem, a_tmem, b_desc, id, accumulate ? 1u : 0u);
+#pragma unroll
+  for (int kk = 1; kk < 8; ++kk)
+    mma_ts_k<1, true>(d_tmem, a_tmem + (kk / 4) * 64 + (kk % 4) * 8,
+                      sdesc_add(b_desc, static_cast<uint32_t>((kk * 2048) >> 4)), id);
+}
+
+// Whether a learned bias is one value over a tile of keys k0 .. k0 + 127 and
+// queries at positions p0 .. p0 + 127: -1 (all at or below -R), 1 (at or above R), 0.
+__device__ __forceinline__ int far_side(int k0, int p0, int R) {
+  const int first = k0 - p0;
+  if (first + kT - 1 <= -R) return -1;
+  if (first - (kT - 1) >= R) return 1;
+  return 0;
+}
+
+// ------------------------------------------------------------------ dK, dV
+template <int HD, bool kF16, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                const Params p) {
+  using C = Cfg<HD, MODE>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + C::kTileBytes;
+  uint8_t* ring = smem + 2 * C::kTileBytes;  // stage s: Q_i at +0, dO_i at +kTileBytes
+  float* lse2 = reinterpret_cast<float*>(smem + C::kDkdvRows);  // [stage][query]: -LSE log2 e
+  float* dsum = lse2 + C::kStages * kT;                         //   -D
+  int* slo = reinterpret_cast<int*>(dsum + C::kStages * kT);    //   lo, hi of the query
+  int* shi = slo + C::kStages * kT;
+  float* bias_all = reinterpret_cast<float*>(smem + C::kDkdvRel);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kDkdvRegion);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  int bhk, kt;
+  unit_of(p, bhk, kt);
+  const int b = bhk / p.Hkv, hk = bhk % p.Hkv;
+  const int k0 = kt * kT;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->fixed_full, 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&bars->full[s], 2);  // the dO load's expect-tx, then the Q load's arrival
+      mbar_init(&bars->empty[s], 1);
+      mbar_init(&bars->empty2[s], 1);
+    }
+    mbar_init(&bars->s_full[0], 1);
+    mbar_init(&bars->dp_full, 1);
+    mbar_init(&bars->p_full, 256);
+    mbar_init(&bars->ds_full, 256);
+    mbar_init(&bars->acc_full, 1);
+    mbar_init(&bars->mma_drain, 1);
+    mbar_init(&bars->elem, 256);
+    bars->abort_flag = 0;
+    bars->it_lo = p.q_tiles;
+    bars->it_hi = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, kCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  // Query tiles [it_lo, it_hi) hold every row that sees one of these keys.
+  for (int q = threadIdx.x; q < p.q_tiles; q += kThreads) {
+    const int4 pt = plan_tile(p.plan, b, p.q_tiles, q, p.Nkv);
+    if (pt.x < k0 + kT && pt.y > k0) {
+      atomicMin(&bars->it_lo, q);
+      atomicMax(&bars->it_hi, q + 1);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const int it_lo = bars->it_lo;
+  const int cnt = max(0, bars->it_hi - it_lo);  // query tiles per head
+  const int n_it = cnt * p.group;
+  const uint32_t tmem = bars->tmem_base;
+  const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
+
+  if (warp == kProdWarp) {
+    int issued = 0;
+    if (n_it > 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars->fixed_full, 2 * C::kTileBytes);
+#pragma unroll
+        for (int cb = 0; cb < HD / 64; ++cb) {
+          tma_load_4d(sK + cb * kT * 128, &tmK, &bars->fixed_full, cb * 64, k0, hk, b);
+          tma_load_4d(sV + cb * kT * 128, &tmV, &bars->fixed_full, cb * 64, k0, hk, b);
+        }
+      }
+      for (int it = 0; it < n_it; ++it) {
+        const int s = it % C::kStages;
+        const int h = hk * p.group + it / cnt;
+        const int q0 = (it_lo + it % cnt) * kT;
+        const long long rowbase = (static_cast<long long>(b) * p.H + h) * p.Nq;
+        // per-query values, read before the wait for the stage
+        float l2[kT / 32], dd[kT / 32];
+        int2 see[kT / 32];
+#pragma unroll
+        for (int r = 0; r < kT / 32; ++r) {
+          const int q = q0 + lane + 32 * r;
+          l2[r] = -INFINITY;
+          dd[r] = 0.f;
+          see[r] = plan_row(p.plan, b, p.Nq, q, p.Nkv);
+          if (q < p.Nq && see[r].x < see[r].y) {
+            const float L = p.LSE[rowbase + q];
+            l2[r] = (L == -INFINITY) ? -INFINITY : -(L * kModLog2e);
+            dd[r] = -p.D[rowbase + q];
+          }
+        }
+        uint8_t* st = ring + s * C::kStageBytes;
+        bool ok = true;
+        if (it >= C::kStages)
+          ok = mbar_wait(&bars->empty2[s], static_cast<uint32_t>(it / C::kStages - 1) & 1u, wc, kSiteLoad);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->full[s], 2 * C::kTileBytes);
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb)
+            tma_load_4d(st + C::kTileBytes + cb * kT * 128, &tmdO, &bars->full[s], cb * 64, q0, h, b);
+        }
+        issued = it + 1;
+        if (it >= C::kStages)
+          ok = mbar_wait(&bars->empty[s], static_cast<uint32_t>(it / C::kStages - 1) & 1u, wc, kSiteLoad);
+        if (!__all_sync(0xffffffffu, ok)) {
+          // Q_i will not be loaded: count its bytes and arrival as done
+          if (lane == 0) {
+            mbar_complete_tx(&bars->full[s], C::kTileBytes);
+            mbar_arrive(&bars->full[s]);
+          }
+          break;
+        }
+#pragma unroll
+        for (int r = 0; r < kT / 32; ++r) {
+          const int x = s * kT + lane + 32 * r;
+          lse2[x] = l2[r];
+          dsum[x] = dd[r];
+          slo[x] = see[r].x;
+          shi[x] = see[r].y;
+        }
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb)
+            tma_load_4d(st + cb * kT * 128, &tmQ, &bars->full[s], cb * 64, q0, h, b);
+          mbar_arrive(&bars->full[s]);  // releases the per-query values above
+        }
+      }
+      if (lane == 0) {
+        drain(&bars->fixed_full, 0, wc.limit_ns);
+        for (int it = (issued > C::kStages ? issued - C::kStages : 0); it < issued; ++it)
+          drain(&bars->full[it % C::kStages], static_cast<uint32_t>(it / C::kStages) & 1u, wc.limit_ns);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // Order: S^T_0, dP^T_0; then per query tile dV += P^T dO, the next S^T,
+    // dK += dS^T Q, the next dP^T.  The tensor core runs them in issue order.
+    if (n_it > 0) {
+      const uint64_t kA = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t vA = sdesc_sw128(smem_u32(sV), 16, 1024);
+      bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);
+      if (ok) ok = warp_wait(&bars->full[0], 0, wc, kSiteMma);
+      if (ok) {
+        tc_fence_after_sync();
+        const uint32_t sq = smem_u32(ring), sdo = sq + C::kTileBytes;
+        mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(sq, 16, 1024));
+        mma_commit<true>(&bars->s_full[0]);
+        mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(sdo, 16, 1024));
+        mma_commit<true>(&bars->dp_full);
+      }
+      for (int it = 0; ok && it < n_it; ++it) {
+        const int s = it % C::kStages, s1 = (it + 1) % C::kStages;
+        const uint32_t sq = smem_u32(ring + s * C::kStageBytes), sdo = sq + C::kTileBytes;
+        const uint32_t nq = smem_u32(ring + s1 * C::kStageBytes), ndo = nq + C::kTileBytes;
+        const bool more = it + 1 < n_it;
+        ok = warp_wait(&bars->p_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
+        if (!ok) break;
+        tc_fence_after_sync();
+        mma_groups<HD, kF16>(tmem + C::kColAcc0, tmem, sdesc_sw128(sdo, kT * 128, 1024), it > 0);
+        mma_commit<true>(&bars->empty2[s]);
+        if (more) {
+          ok = warp_wait(&bars->full[s1], static_cast<uint32_t>((it + 1) / C::kStages) & 1u, wc, kSiteMma);
+          if (!ok) break;
+          tc_fence_after_sync();
+          mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(nq, 16, 1024));
+          mma_commit<true>(&bars->s_full[0]);
+        }
+        ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
+        if (!ok) break;
+        tc_fence_after_sync();
+        mma_groups<HD, kF16>(tmem + C::kColAcc1, tmem + 128, sdesc_sw128(sq, kT * 128, 1024), it > 0);
+        mma_commit<true>(&bars->empty[s]);
+        if (more) {
+          mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(ndo, 16, 1024));
+          mma_commit<true>(&bars->dp_full);
+        }
+      }
+      if (ok) mma_commit<true>(&bars->acc_full);
+      mma_commit<true>(&bars->mma_drain);
+      drain(&bars->mma_drain, 0, wc.limit_ns);
+      __syncwarp();
+    }
+  } else {
+    const int c0 = 64 * (warp >> 2);         // this warpgroup's columns (queries)
+    const int row = (warp & 3) * 32 + lane;  // key row of the tile = tensor-memory lane
+    const int kabs = k0 + row;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    bool ok = true;
+    int h_of = -1;
+    [[maybe_unused]] uint32_t sync_phase = 0;
+    float slope2 = 0.f;
+    for (int it = 0; ok && it < n_it; ++it) {
+      const int s = it % C::kStages;
+      const int h = hk * p.group + it / cnt;
+      const int qt = it_lo + it % cnt;
+      const int p0 = qt * kT + p.q_offset;  // position of the tile's first query
+      if (h != h_of) {  // uniform over the elementwise warps
+        if constexpr (mode_slopes(MODE)) slope2 = p.slopes[h] * kModLog2e;
+        if constexpr (mode_rel(MODE)) {
+          // everyone is done with the last head's table
+          if (h_of >= 0 && !(ok = elem_sync(bars, sync_phase, wc))) break;
+          for (int x = threadIdx.x; x < rel_entries(p.rel.range); x += 256) {
+            const int bucket = __ldg(p.rel.map + min(max(x - kRelPad, 0), 2 * p.rel.range));
+            float v = 0.f;
+            if (bucket >= 0 && bucket < p.rel.num)
+              v = load_16<kF16>(static_cast<const uint16_t*>(p.rel.table) +
+                                static_cast<long long>(bucket) * p.H + h);
+            bias_all[x] = v * kModLog2e;
+          }
+          if (!(ok = elem_sync(bars, sync_phase, wc))) break;
+        }
+        h_of = h;
+      }
+      const int4 pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
+      ok = mbar_wait(&bars->s_full[0], static_cast<uint32_t>(it) & 1u, wc, kSiteElem);
+      if (ok) ok = mbar_wait(&bars->full[s], static_cast<uint32_t>(it / C::kStages) & 1u, wc, kSiteElem);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const float4* l2 = reinterpret_cast<const float4*>(lse2 + s * kT);
+      const float4* dd = reinterpret_cast<const float4*>(dsum + s * kT);
+      const int* lo = slo + s * kT;
+      const int* hi = shi + s * kT;
+      const int d0 = kabs - p0;  // distance to the tile's first query
+      auto vis = [&](int col) { return lo[col] <= kabs && kabs < hi[col]; };
+      auto l2of4 = [&](int col) { return l2[col >> 2]; };
+      auto dist = [&](int col) { return static_cast<float>(d0 - col); };
+      const float* bt = nullptr;
+      float far = 0.f;
+      int side = 0;
+      if constexpr (mode_rel(MODE)) {
+        side = far_side(k0, p0, p.rel.range);
+        far = side < 0 ? bias_all[0] : bias_all[rel_entries(p.rel.range) - 1];
+        bt = bias_all + (d0 + p.rel.range + kRelPad);
+      }
+      float pr[64];
+      // Every key of the tile visible to every query: no per-entry mask.
+      // (Uniform over the CTA.)
+      const bool full = pt.z <= k0 && pt.w >= k0 + kT;
+      auto part = [&](auto mask) {
+        constexpr bool kMask = decltype(mask)::value;
+        if constexpr (mode_rel(MODE)) {
+          if (side != 0) {
+            p_part<kF16, MODE, true, kMask>(lane_base, c0, p, slope2, vis, l2of4, dist,
+                                            [&](int) { return far; }, pr);
+            return;
+          }
+        }
+        p_part<kF16, MODE, true, kMask>(lane_base, c0, p, slope2, vis, l2of4, dist,
+                                        [&](int col) { return bt[-col]; }, pr);
+      };
+      bool waited = false;
+      if (full) {
+        part(std::false_type{});
+      } else {
+        part(std::true_type{});
+        if (pt.w == 0) {
+          // Queries of this tile that see nothing: their rows of Q and dO
+          // must not reach the sums (0 * NaN is NaN).  dP^T, the last other
+          // reader of dO, is awaited first.
+          ok = mbar_wait(&bars->dp_full, static_cast<uint32_t>(it) & 1u, wc, kSiteElem);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          waited = true;
+          uint8_t* st = ring + s * C::kStageBytes;
+          if (lo[row] >= hi[row]) {
+            // warpgroup 0 clears Q, warpgroup 1 dO
+#pragma unroll
+            for (int cb = 0; cb < HD / 64; ++cb) zero_row(st + (c0 ? C::kTileBytes : 0), cb, row);
+          }
+          fence_proxy_async();
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&bars->p_full);
+      if (!waited) {
+        ok = mbar_wait(&bars->dp_full, static_cast<uint32_t>(it) & 1u, wc, kSiteElem);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      tc_fence_after_sync();
+      auto dof4 = [&](int col) { return dd[col >> 2]; };
+      if (full)
+        ds_part<kF16, false, false>(lane_base + 128, c0, dof4, pr);
+      else
+        ds_part<kF16, true, false>(lane_base + 128, c0, dof4, pr);
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&bars->ds_full);
+    }
+    // epilogue: warpgroup 0 writes dV, warpgroup 1 dK
+    bool has_acc = false;
+    if (ok && n_it > 0) {
+      ok = mbar_wait(&bars->acc_full, 0, wc, kSiteEpi);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) tc_fence_after_sync();
+      has_acc = ok;
+    }
+    if (ok) {
+      const bool store = kabs < p.Nkv;
+      if (c0 == 0)
+        write_row<HD, kF16>(p.dV + b * p.dv_s[0] + hk * p.dv_s[1] + kabs * p.dv_s[2],
+                            lane_base + C::kColAcc0, has_acc, store, 1.f);
+      else
+        write_row<HD, kF16>(p.dK + b * p.dk_s[0] + hk * p.dk_s[1] + kabs * p.dk_s[2],
+                            lane_base + C::kColAcc1, has_acc, store, p.scale);
+    }
+  }
+
+  __syncwarp();
+  tmem_st_wait();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// ------------------------------------------------------------------ dQ
+constexpr uint32_t kDqColDP = 256, kDqColAcc = 384;
+
+template <int HD, bool kF16, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+              const Params p) {
+  using C = Cfg<HD, MODE>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sdO = smem + C::kTileBytes;
+  uint8_t* kring = smem + 2 * C::kTileBytes;
+  uint8_t* vring = kring + C::kKSlots * C::kTileBytes;
+  float* bias = reinterpret_cast<float*>(smem + C::kDqRel);
+  float* dsum = reinterpret_cast<float*>(smem + C::kDqRel + C::kRelBytes);  // sums of dY by distance
+  float* strips = reinterpret_cast<float*>(smem + C::kDqRel + 2 * C::kRelBytes);  // [2][8][96]
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kDqRegion);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  int bh, rank;
+  unit_of(p, bh, rank);
+  const int qt = p.num_tiles - 1 - rank;
+  const int b = bh / p.H, h = bh % p.H, hk = h / p.group;
+  const int q0 = qt * kT;
+  const int4 pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
+  const int kt0 = pt.x / kT;
+  const int n_kt = pt.x < pt.y ? (pt.y + kT - 1) / kT - kt0 : 0;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->fixed_full, 1);
+    for (int s = 0; s < C::kKSlots; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int s = 0; s < C::kVSlots; ++s) mbar_init(&bars->empty2[s], 1);
+    mbar_init(&bars->s_full[0], 1);
+    mbar_init(&bars->s_full[1], 1);
+    mbar_init(&bars->dp_full, 1);
+    mbar_init(&bars->ds_full, 256);
+    mbar_init(&bars->acc_full, 1);
+    mbar_init(&bars->mma_drain, 1);
+    mbar_init(&bars->d_full, 256);
+    mbar_init(&bars->elem, 256);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, kCols);
+    tmem_relinquish();
+  }
+  if constexpr (mode_rel(MODE)) {
+    rel_fill<kF16>(bias, p.rel, p.H, h);
+    for (int x = threadIdx.x; x < rel_entries(p.rel.range); x += kThreads) dsum[x] = 0.f;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
+
+  if (warp == kProdWarp) {
+    if (lane == 0 && n_kt > 0) {
+      mbar_arrive_expect_tx(&bars->fixed_full, 2 * C::kTileBytes);
+#pragma unroll
+      for (int cb = 0; cb < HD / 64; ++cb) {
+        tma_load_4d(sQ + cb * kT * 128, &tmQ, &bars->fixed_full, cb * 64, q0, h, b);
+        tma_load_4d(sdO + cb * kT * 128, &tmdO, &bars->fixed_full, cb * 64, q0, h, b);
+      }
+      int issued = 0;
+      for (int j = 0; j < n_kt; ++j) {
+        const int a = j % C::kKSlots, v = j % C::kVSlots;
+        if (j >= C::kKSlots &&
+            !mbar_wait(&bars->empty[a], static_cast<uint32_t>(j / C::kKSlots - 1) & 1u, wc, kSiteLoad))
+          break;
+        if (j >= C::kVSlots &&
+            !mbar_wait(&bars->empty2[v], static_cast<uint32_t>(j / C::kVSlots - 1) & 1u, wc, kSiteLoad))
+          break;
+        mbar_arrive_expect_tx(&bars->full[a], 2 * C::kTileBytes);
+#pragma unroll
+        for (int cb = 0; cb < HD / 64; ++cb) {
+          tma_load_4d(kring + a * C::kTileBytes + cb * kT * 128, &tmK, &bars->full[a], cb * 64,
+                      (kt0 + j) * kT, hk, b);
+          tma_load_4d(vring + v * C::kTileBytes + cb * kT * 128, &tmV, &bars->full[a], cb * 64,
+                      (kt0 + j) * kT, hk, b);
+        }
+        issued = j + 1;
+      }
+      drain(&bars->fixed_full, 0, wc.limit_ns);
+      for (int j = (issued > C::kKSlots ? issued - C::kKSlots : 0); j < issued; ++j)
+        drain(&bars->full[j % C::kKSlots], static_cast<uint32_t>(j / C::kKSlots) & 1u, wc.limit_ns);
+    }
+  } else if (warp == kMmaWarp) {
+    // Order: S_0, dP_0; then per key tile j: S_{j+1}, dQ += dS_j K_j, dP_{j+1}.
+    if (n_kt > 0) {
+      const uint64_t qA = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dA = sdesc_sw128(smem_u32(sdO), 16, 1024);
+      bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);
+      if (ok) ok = warp_wait(&bars->full[0], 0, wc, kSiteMma);
+      if (ok) {
+        tc_fence_after_sync();
+        mma_abt<128, HD, kF16, true>(tmem, qA, sdesc_sw128(smem_u32(kring), 16, 1024));
+        mma_commit<true>(&bars->s_full[0]);
+        mma_abt<128, HD, kF16, true>(tmem + kDqColDP, dA, sdesc_sw128(smem_u32(vring), 16, 1024));
+        mma_commit<true>(&bars->dp_full);
+        mma_commit<true>(&bars->empty2[0]);
+      }
+      for (int j = 0; ok && j < n_kt; ++j) {
+        const int a = j % C::kKSlots, a1 = (j + 1) % C::kKSlots, v1 = (j + 1) % C::kVSlots;
+        const uint32_t sk = smem_u32(kring + a * C::kTileBytes);
+        const uint32_t nk = smem_u32(kring + a1 * C::kTileBytes);
+        const uint32_t nv = smem_u32(vring + v1 * C::kTileBytes);
+        const bool more = j + 1 < n_kt;
+        if (more) {
+          ok = warp_wait(&bars->full[a1], static_cast<uint32_t>((j + 1) / C::kKSlots) & 1u, wc, kSiteMma);
+          if (!ok) break;
+          tc_fence_after_sync();
+          mma_abt<128, HD, kF16, true>(tmem + 128 * ((j + 1) & 1), qA, sdesc_sw128(nk, 16, 1024));
+          mma_commit<true>(&bars->s_full[(j + 1) & 1]);
+        }
+        ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(j) & 1u, wc, kSiteMma);
+        if (!ok) break;
+        tc_fence_after_sync();
+        mma_groups<HD, kF16>(tmem + kDqColAcc, tmem + kDqColDP, sdesc_sw128(sk, kT * 128, 1024), j > 0);
+        mma_commit<true>(&bars->empty[a]);
+        if (more) {
+          mma_abt<128, HD, kF16, true>(tmem + kDqColDP, dA, sdesc_sw128(nv, 16, 1024));
+          mma_commit<true>(&bars->dp_full);
+          mma_commit<true>(&bars->empty2[v1]);
+        }
+      }
+      if (ok) mma_commit<true>(&bars->acc_full);
+      mma_commit<true>(&bars->mma_drain);
+      drain(&bars->mma_drain, 0, wc.limit_ns);
+      __syncwarp();
+    }
+  } else {
+    const int c0 = 64 * (warp >> 2);         // this warpgroup's columns (keys)
+    const int row = (warp & 3) * 32 + lane;  // query row of the tile = tensor-memory lane
+    const int q = q0 + row;
+    const bool in = q < p.Nq;
+    const int2 see = plan_row(p.plan, b, p.Nq, q, p.Nkv);
+    const bool row_live = see.x < see.y;
+    const long long rix = static_cast<long long>(bh) * p.Nq + q;
+    const int p0 = q0 + p.q_offset;
+    float slope2 = 0.f;
+    if constexpr (mode_slopes(MODE)) slope2 = p.slopes[h] * kModLog2e;
+    float l2 = -INFINITY;  // -LSE log2 e
+    // D of this row: warpgroup g takes columns g d/2 .. (g + 1) d/2 - 1, O
+    // from global memory (loaded now), dO from the resident tile
+    constexpr int kHalfD = HD / 2, kNv = kHalfD / 8;
+    const int g = warp >> 2;
+    uint4 ov[kNv];
+#pragma unroll
+    for (int v = 0; v < kNv; ++v) ov[v] = make_uint4(0u, 0u, 0u, 0u);
+    if (row_live) {
+      const float L = p.LSE[rix];
+      l2 = (L == -INFINITY) ? -INFINITY : -(L * kModLog2e);
+      const uint4* orow = reinterpret_cast<const uint4*>(
+          p.O + b * p.o_s[0] + h * p.o_s[1] + static_cast<long long>(q) * p.o_s[2] + g * kHalfD);
+#pragma unroll
+      for (int v = 0; v < kNv; ++v) ov[v] = orow[v];
+    }
+    const float4 l2v = make_float4(l2, l2, l2, l2);
+    float4 dv4 = make_float4(0.f, 0.f, 0.f, 0.f);  // -D
+    if (n_kt == 0 && g == 0 && in) p.D[rix] = 0.f;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float far_lo = 0.f, far_hi = 0.f;  // sums of dY at distances <= -R and >= R
+    [[maybe_unused]] uint32_t sync_phase = 0;  // = near tiles so far
+    bool ok = true;
+    for (int j = 0; ok && j < n_kt; ++j) {
+      ok = mbar_wait(&bars->s_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, wc, kSiteElem);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const int kx = (kt0 + j) * kT;
+      const int d0 = kx - (q + p.q_offset);
+      auto vis = [&](int col) { return kx + col >= see.x && kx + col < see.y; };
+      auto l2of4 = [&](int) { return l2v; };
+      auto dist = [&](int col) { return static_cast<float>(d0 + col); };
+      const float* bt = nullptr;
+      float far = 0.f;
+      int side = 0;
+      if constexpr (mode_rel(MODE)) {
+        side = far_side(kx, p0, p.rel.range);
+        far = side < 0 ? bias[0] : bias[rel_entries(p.rel.range) - 1];
+        bt = bias + (d0 + p.rel.range + kRelPad);
+      }
+      const bool full = pt.z <= kx && pt.w >= kx + kT;
+      const uint32_t s_addr = lane_base + 128 * (j & 1);
+      float pr[64];
+      auto part = [&](auto mask) {
+        constexpr bool kMask = decltype(mask)::value;
+        if constexpr (mode_rel(MODE)) {
+          if (side != 0) {
+            p_part<kF16, MODE, false, kMask>(s_addr, c0, p, slope2, vis, l2of4, dist,
+                                             [&](int) { return far; }, pr);
+            return;
+          }
+        }
+        p_part<kF16, MODE, false, kMask>(s_addr, c0, p, slope2, vis, l2of4, dist,
+                                         [&](int col) { return bt[col]; }, pr);
+      };
+      if (full)
+        part(std::false_type{});
+      else
+        part(std::true_type{});
+      if (kx < pt.x || min(kx + kT, p.Nkv) > pt.y) {
+        // keys of this tile that no row sees: zero their rows of K_j, which
+        // dQ += dS_j K_j reads after ds_full (S_j, the other reader, is done)
+        if (kx + row < pt.x || kx + row >= pt.y) {
+          uint8_t* ks = kring + (j % C::kKSlots) * C::kTileBytes;
+          if (HD == 128) zero_row(ks, g, row);
+          else if (g == 0) zero_row(ks, 0, row);
+        }
+        fence_proxy_async();
+      }
+      if (j == 0) {
+        // the half dot product of D over this warpgroup's columns of the
+        // swizzled dO tile, then both halves through shared memory
+        ok = mbar_wait(&bars->fixed_full, 0, wc, kSiteElem);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < kNv; ++v) {
+          const int col = g * kHalfD + v * 8;
+          const uint4 gv = *reinterpret_cast<const uint4*>(
+              sdO + (col / 64) * kT * 128 + row * 128 + ((((col % 64) / 8) ^ (row & 7)) * 16));
+          const uint32_t ow[4] = {ov[v].x, ov[v].y, ov[v].z, ov[v].w};
+          const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = unpack16<kF16>(ow[e]), y = unpack16<kF16>(gw[e]);
+            sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+          }
+        }
+        bars->d_part[g][row] = sum;
+        mbar_arrive(&bars->d_full);
+        ok = mbar_wait(&bars->d_full, 0, wc, kSiteElem);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const float D = row_live ? bars->d_part[0][row] + bars->d_part[1][row] : 0.f;
+        dv4 = make_float4(-D, -D, -D, -D);
+        if (g == 0 && in) p.D[rix] = D;
+      }
+      ok = mbar_wait(&bars->dp_full, static_cast<uint32_t>(j) & 1u, wc, kSiteElem);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      auto dof4 = [&](int) { return dv4; };
+      constexpr bool kKeep = mode_rel(MODE);
+      if (full)
+        ds_part<kF16, false, kKeep>(lane_base + kDqColDP, c0, dof4, pr);
+      else
+        ds_part<kF16, true, kKeep>(lane_base + kDqColDP, c0, dof4, pr);
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&bars->ds_full);
+      if constexpr (mode_rel(MODE)) {
+        if (side != 0) {
+          float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 64; ++x) a[x & 3] += pr[x];
+          const float sum = (a[0] + a[1]) + (a[2] + a[3]);
+          if (side < 0) far_lo += sum;
+          else far_hi += sum;
+        } else {
+          // Sums along the diagonals of the warp's 32 x 64 block: a running
+          // sum moves one lane up with every column, so that it stays on one
+          // distance; lane 31 stores the diagonals that end there.  Strip
+          // entry u holds distance (c0 - 32 quarter) + u - 31 within the tile.
+          const int buf = sync_phase & 1;
+          float* strip = strips + buf * 8 * 96 + warp * 96;
+          float acc = 0.f;
+#pragma unroll
+          for (int x = 0; x < 64; ++x) {
+            acc = __shfl_up_sync(0xffffffffu, acc, 1);
+            acc = (lane == 0 ? 0.f : acc) + pr[x];
+            if (lane == 31) strip[x] = acc;
+          }
+          if (lane < 31) strip[94 - lane] = acc;
+          if (!(ok = elem_sync(bars, sync_phase, wc))) break;
+          // thread u adds distance u - 127 of the tile to the sums
+          const int u = threadIdx.x;
+          if (u < 2 * kT - 1) {
+            float add = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const int at = (u - 127) - 64 * (w >> 2) + 32 * (w & 3) + 31;
+              if (at >= 0 && at < 95) add += strips[buf * 8 * 96 + w * 96 + at];
+            }
+            dsum[kx - p0 + (u - 127) + p.rel.range + kRelPad] += add;
+          }
+        }
+      }
+    }
+    bool has_acc = false;
+    if (ok && n_kt > 0) {
+      ok = mbar_wait(&bars->acc_full, 0, wc, kSiteEpi);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) tc_fence_after_sync();
+      has_acc = ok;
+    }
+    if (ok)
+      write_row<HD / 2, kF16>(p.dQ + b * p.dq_s[0] + h * p.dq_s[1] + q * p.dq_s[2] + c0 * HD / 128,
+                              lane_base + kDqColAcc + c0 * HD / 128, has_acc, in, p.scale);
+    if constexpr (mode_rel(MODE)) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        far_lo += __shfl_xor_sync(0xffffffffu, far_lo, off);
+        far_hi += __shfl_xor_sync(0xffffffffu, far_hi, off);
+      }
+      if (lane == 0) {
+        bars->far_part[0][warp] = far_lo;
+        bars->far_part[1][warp] = far_hi;
+      }
+    }
+  }
+
+  __syncwarp();
+  tmem_st_wait();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kCols);
+  }
+  if constexpr (mode_rel(MODE)) {
+    // this CTA's sums by clamped distance, the pads folded into the ends
+    const int R = p.rel.range;
+    float* out = p.rel_part + (static_cast<long long>(bh) * p.num_tiles + qt) * (2 * R + 1);
+    for (int x = threadIdx.x; x < 2 * R + 1; x += kThreads)
+      if (x != 0 && x != 2 * R) out[x] = dsum[x + kRelPad];
+    if (warp < 2) {  // distance -R (warp 0), R (warp 1)
+      const float* pad = dsum + (warp == 0 ? 0 : 2 * R + kRelPad);
+      float v = 0.f;
+      for (int x = lane; x <= kRelPad; x += 32) v += pad[x];
+      if (lane < 8) v += bars->far_part[warp][lane];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+      if (lane == 0) out[warp == 0 ? 0 : 2 * R] = v;
+    }
+  }
+}
+
+// The table's gradient: one block per head sums the partials of its query
+// tiles over batch entries and tiles in a fixed order, then each warp its
+// buckets over the distances.  Bound by latency at usual ranges (2 R + 1 = 257
+// floats a tile).
+template <bool kF16>
+__global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restrict__ part,
+                                                          uint16_t* __restrict__ out, RelArgs rel, int B,
+                                                          int H, int q_tiles) {
+  __shared__ float sums[2 * kMaxRelRange + 1];
+  __shared__ int map[2 * kMaxRelRange + 1];
+  const int h = blockIdx.x, n = 2 * rel.range + 1;
+  for (int x = threadIdx.x; x < n; x += blockDim.x) {
+    map[x] = rel.map[x];
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int b = 0; b < B; ++b) {
+      const float* src = part + (static_cast<long long>(b) * H + h) * q_tiles * n + x;
+      int t = 0;
+      for (; t + 4 <= q_tiles; t += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) a[u] += src[static_cast<long long>(t + u) * n];
+      }
+      for (; t < q_tiles; ++t) a[0] += src[static_cast<long long>(t) * n];
+    }
+    sums[x] = (a[0] + a[1]) + (a[2] + a[3]);
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int k = warp; k < rel.num; k += blockDim.x / 32) {
+    float v = 0.f;
+    for (int x = lane; x < n; x += 32) v += map[x] == k ? sums[x] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == 0)
+      out[static_cast<long long>(k) * H + h] = static_cast<uint16_t>(pack2<kF16>(v, 0.f) & 0xffffu);
+  }
+}
+
+template <int HD, bool kF16, int MODE>
+cudaError_t set_attrs() {
+  static_assert(dkdv_smem_bytes<HD, MODE>() <= 232448 && dq_smem_bytes<HD, MODE>() <= 232448,
+                "shared memory per CTA");
+  cudaError_t e = cudaFuncSetAttribute(dkdv_kernel<HD, kF16, MODE>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       dkdv_smem_bytes<HD, MODE>());
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(dq_kernel<HD, kF16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              dq_smem_bytes<HD, MODE>());
+}
+
+template <int HD, bool kF16>
+cudaError_t prepare() {
+  cudaError_t e;
+  if ((e = set_attrs<HD, kF16, kModPlain>()) != cudaSuccess) return e;
+  if ((e = set_attrs<HD, kF16, kModCap>()) != cudaSuccess) return e;
+  if ((e = set_attrs<HD, kF16, kModSlopes>()) != cudaSuccess) return e;
+  if ((e = set_attrs<HD, kF16, kModCapSlopes>()) != cudaSuccess) return e;
+  return set_attrs<HD, kF16, kModRel>();
+}
+
+template <int HD, bool kF16, int MODE>
+cudaError_t launch_mode(const ModArgs& a, const Params& pq, const Params& pk, unsigned gq, unsigned gk,
+                        const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                        const CUtensorMap& g) {
+  // dQ first: it writes D, which the dK/dV kernel reads
+  dq_kernel<HD, kF16, MODE><<<gq, kThreads, dq_smem_bytes<HD, MODE>(), a.stream>>>(q, k, v, g, pq);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  dkdv_kernel<HD, kF16, MODE><<<gk, kThreads, dkdv_smem_bytes<HD, MODE>(), a.stream>>>(q, k, v, g, pk);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !mode_rel(MODE)) return e;
+  rel_reduce_kernel<kF16><<<a.H, 1024, 0, a.stream>>>(a.rel_part, static_cast<uint16_t*>(a.dRel), a.rel,
+                                                      a.B, a.H, pq.q_tiles);
+  return cudaGetLastError();
+}
+
+template <int HD, bool kF16>
+cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   const CUtensorMap& g) {
+  Params p;
+  p.dQ = static_cast<uint16_t*>(a.dQ);
+  p.dK = static_cast<uint16_t*>(a.dK);
+  p.dV = static_cast<uint16_t*>(a.dV);
+  for (int i = 0; i < 3; ++i) {
+    p.dq_s[i] = a.dq_s[i];
+    p.dk_s[i] = a.dk_s[i];
+    p.dv_s[i] = a.dv_s[i];
+    p.o_s[i] = a.o_s[i];
+  }
+  p.LSE = a.LSE;
+  p.D = a.D;
+  p.O = static_cast<const uint16_t*>(a.O_in);
+  p.q_tiles = (a.Nq + kT - 1) / kT;
+  p.plan.tiles = static_cast<const int4*>(a.plan);
+  p.plan.rows = a.plan ? reinterpret_cast<const int2*>(p.plan.tiles + static_cast<long long>(a.B) * p.q_tiles)
+                       : nullptr;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.group = a.H / a.Hkv;
+  p.Nq = a.Nq;
+  p.Nkv = a.Nkv;
+  p.scale = a.scale;
+  p.scale_log2 = a.scale * kModLog2e;
+  p.cap_c1 = a.softcap > 0.f ? 2.f * a.scale * kModLog2e / a.softcap : 0.f;
+  p.cap2 = a.softcap * kModLog2e;
+  p.slopes = a.slopes;
+  p.rel = a.rel;
+  p.rel_part = a.rel_part;
+  p.q_offset = a.q_offset;
+  p.status = a.status;
+  p.wait_limit_ns = a.wait_limit_ns;
+  // heads whose streamed tiles take about 32 MB of L2 together
+  auto group = [&](long long rows, long long bh) {
+    const long long gh = (32ll << 20) / (2ll * rows * a.d * 2);
+    return static_cast<int>(gh < 1 ? 1 : (gh > bh ? bh : gh));
+  };
+  Params pk = p, pq = p;
+  pk.BH = a.B * a.Hkv;
+  pk.num_tiles = (a.Nkv + kT - 1) / kT;
+  pk.group_heads = group(static_cast<long long>(a.Nq) * p.group, pk.BH);
+  pq.BH = a.B * a.H;
+  pq.num_tiles = p.q_tiles;
+  pq.group_heads = group(a.Nkv, pq.BH);
+  const long long gk = static_cast<long long>(pk.num_tiles) * pk.BH;
+  const long long gq = static_cast<long long>(pq.num_tiles) * pq.BH;
+  if (gk > 0x7fffffffLL || gq > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const unsigned uq = static_cast<unsigned>(gq), uk = static_cast<unsigned>(gk);
+  switch (mod_score_mode(a)) {
+    case kModCap: return launch_mode<HD, kF16, kModCap>(a, pq, pk, uq, uk, q, k, v, g);
+    case kModSlopes: return launch_mode<HD, kF16, kModSlopes>(a, pq, pk, uq, uk, q, k, v, g);
+    case kModCapSlopes: return launch_mode<HD, kF16, kModCapSlopes>(a, pq, pk, uq, uk, q, k, v, g);
+    case kModRel: return launch_mode<HD, kF16, kModRel>(a, pq, pk, uq, uk, q, k, v, g);
+    default: return launch_mode<HD, kF16, kModPlain>(a, pq, pk, uq, uk, q, k, v, g);
+  }
+}
+
+}  // namespace bwdmod
+}  // namespace osattn

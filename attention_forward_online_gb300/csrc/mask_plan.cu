@@ -1,0 +1,170 @@
+// mask_plan.cu - the key range [lo, hi) of every query row, from causal
+// order, a window, a prefix, key lengths and packed documents.
+//
+// Each of these masks lets a row see one interval of keys, and an
+// intersection of intervals is one, so two integers a row carry any
+// combination; the attention kernels mask with two comparisons and find the
+// tiles they have to visit from a per-tile summary.  A document is a run of
+// equal, non-negative ids.
+//
+// One block per 128 query rows: bound by latency (a launch and, with
+// documents, the search for the ends of the runs that cross the tile).  A
+// run's end outside the tile is found by the whole block, 4096 positions a
+// step with 16 coalesced loads a thread in flight.
+#include <climits>
+#include <cstdint>
+
+#include "mod_common.cuh"
+
+namespace osattn {
+namespace {
+
+constexpr int kPlanThreads = 256;
+constexpr int kPerThread = 16;
+
+struct PlanParams {
+  int4* tiles;
+  int2* rows;
+  int n_tiles, Nq, Nkv, q_offset, causal, window;
+  const int32_t* key_len;
+  const int32_t* prefix_len;
+  const int32_t* doc_ids;
+};
+
+// Smallest (dir = 1) or largest (dir = -1) position x from `from` on in
+// direction dir whose run of ids ends there (id[x + dir] differs or does not
+// exist).  The whole block calls it; `slot` is shared.
+__device__ int run_end(const int32_t* ids, int n, int from, int dir, int* slot) {
+  for (int base = 0;; base += kPlanThreads * kPerThread) {
+    if (threadIdx.x == 0) *slot = INT_MAX;
+    __syncthreads();
+    int best = INT_MAX;  // distance from `from`
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int dist = base + k * kPlanThreads + static_cast<int>(threadIdx.x);
+      const long long x = from + static_cast<long long>(dir) * dist;
+      if (x < 0 || x >= n) continue;
+      const long long y = x + dir;
+      if (y < 0 || y >= n || ids[y] != ids[x]) best = min(best, dist);
+    }
+    if (best != INT_MAX) atomicMin(slot, best);
+    __syncthreads();
+    const int got = *slot;
+    __syncthreads();
+    if (got != INT_MAX) return from + dir * got;
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) mask_plan_kernel(const PlanParams p) {
+  __shared__ int slot, s_lo_min, s_hi_max, s_lo_max, s_hi_min;
+  __shared__ int s_id[kPlanTile];
+  __shared__ unsigned s_bits[2][kPlanThreads / 32];
+  __shared__ int s_start[kPlanTile], s_end[kPlanTile];
+  const int b = blockIdx.x / p.n_tiles, tile = blockIdx.x % p.n_tiles, r = threadIdx.x;
+  const int i = tile * kPlanTile + r;
+  const bool mine = r < kPlanTile && i < p.Nq;
+  const int32_t* ids = p.doc_ids ? p.doc_ids + static_cast<long long>(b) * p.Nkv : nullptr;
+  if (r == 0) {
+    s_lo_min = INT_MAX;
+    s_hi_max = 0;
+    s_lo_max = 0;
+    s_hi_min = INT_MAX;
+  }
+  const long long pos = static_cast<long long>(i) + p.q_offset;
+  if (ids) {
+    // positions of the tile that exist: [first, last]
+    const long long at0 = static_cast<long long>(tile) * kPlanTile + p.q_offset;
+    const long long at1 = at0 + min(kPlanTile, p.Nq - tile * kPlanTile) - 1;
+    const int first = static_cast<int>(at0 < 0 ? 0 : at0);
+    const int last = static_cast<int>(at1 >= p.Nkv ? p.Nkv - 1 : at1);
+    if (at1 >= 0 && at0 < p.Nkv) {  // uniform over the block
+      const int back = run_end(ids, p.Nkv, first, -1, &slot);
+      const int fwd = run_end(ids, p.Nkv, last, 1, &slot);
+      const int n = last - first + 1;
+      for (int x = r; x < n; x += kPlanThreads) s_id[x] = ids[first + x];
+      __syncthreads();
+      // start and end of each position's run inside the tile, from the bits
+      // of the positions where a run starts or ends
+      const bool starts = r < n && (r == 0 || s_id[r - 1] != s_id[r]);
+      const bool ends = r < n && (r == n - 1 || s_id[r + 1] != s_id[r]);
+      const unsigned ms = __ballot_sync(0xffffffffu, starts), me = __ballot_sync(0xffffffffu, ends);
+      if ((r & 31) == 0) {
+        s_bits[0][r >> 5] = ms;
+        s_bits[1][r >> 5] = me;
+      }
+      __syncthreads();
+      if (r < n) {
+        int w = r >> 5;
+        unsigned m = s_bits[0][w] & (0xffffffffu >> (31 - (r & 31)));
+        while (m == 0) m = s_bits[0][--w];  // position 0 starts a run
+        const int a = w * 32 + 31 - __clz(m);
+        w = r >> 5;
+        m = s_bits[1][w] & (0xffffffffu << (r & 31));
+        while (m == 0) m = s_bits[1][++w];  // position n - 1 ends one
+        const int e = w * 32 + __ffs(m) - 1;
+        s_start[r] = a == 0 ? back : first + a;
+        s_end[r] = (e == n - 1 ? fwd : first + e) + 1;
+      }
+    }
+  }
+  __syncthreads();
+  if (mine) {
+    long long lo = 0, hi = p.Nkv;
+    if (p.key_len) hi = min(max(p.key_len[b], 0), p.Nkv);
+    if (p.causal) {
+      long long end = pos + 1;
+      if (p.prefix_len) end = max(end, static_cast<long long>(p.prefix_len[b]));
+      hi = min(hi, end);
+    }
+    if (p.window > 0) {
+      lo = max(lo, pos - p.window + 1);
+      hi = min(hi, pos + p.window);
+    }
+    if (ids) {
+      if (pos < 0 || pos >= p.Nkv) {
+        hi = 0;
+      } else {
+        const int x = static_cast<int>(pos - max(0ll, static_cast<long long>(tile) * kPlanTile + p.q_offset));
+        lo = max(lo, static_cast<long long>(s_start[x]));
+        hi = min(hi, static_cast<long long>(s_end[x]));
+        if (s_id[x] < 0) hi = 0;
+      }
+    }
+    if (lo >= hi) lo = hi = 0;
+    p.rows[static_cast<long long>(b) * p.Nq + i] = make_int2(static_cast<int>(lo), static_cast<int>(hi));
+    if (lo < hi) {
+      atomicMin(&s_lo_min, static_cast<int>(lo));
+      atomicMax(&s_hi_max, static_cast<int>(hi));
+    }
+    atomicMax(&s_lo_max, static_cast<int>(lo));
+    atomicMin(&s_hi_min, static_cast<int>(hi));
+  }
+  __syncthreads();
+  if (r == 0)
+    p.tiles[blockIdx.x] =
+        make_int4(s_hi_max > 0 ? s_lo_min : 0, s_hi_max, s_lo_max, s_hi_min);
+}
+
+}  // namespace
+
+cudaError_t launch_mask_plan(const PlanArgs& a) {
+  PlanParams p;
+  const int nt = (a.Nq + kPlanTile - 1) / kPlanTile;
+  p.tiles = static_cast<int4*>(a.plan);
+  p.rows = reinterpret_cast<int2*>(p.tiles + static_cast<long long>(a.B) * nt);
+  p.n_tiles = nt;
+  p.Nq = a.Nq;
+  p.Nkv = a.Nkv;
+  p.q_offset = a.q_offset;
+  p.causal = a.causal;
+  p.window = a.window;
+  p.key_len = a.key_len;
+  p.prefix_len = a.prefix_len;
+  p.doc_ids = a.doc_ids;
+  const long long blocks = static_cast<long long>(nt) * a.B;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  mask_plan_kernel<<<static_cast<unsigned>(blocks), kPlanThreads, 0, a.stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace osattn

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "osattn.h"
+#include "api_shared.h"
 #include "osattn_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -87,15 +88,15 @@ int device_state(DeviceState** out) {
 }
 
 // 4-D view (d, N, H, B) of a tensor with element strides st = {b, h, row}
-// (d contiguous), 64 x 128 boxes, 128-byte swizzle, zero fill outside it.
+// (d contiguous), 64 x box_rows boxes, 128-byte swizzle, zero fill outside it.
 int encode_map(CUtensorMap* map, const void* base, int fp16, int d, int N, int H, int B,
-               const long long* st) {
+               const long long* st, int box_rows = osattn::kBoxRows) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N),
                               static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(st[2]) * 2,
                                  static_cast<cuuint64_t>(st[1]) * 2,
                                  static_cast<cuuint64_t>(st[0]) * 2};
-  const cuuint32_t box[4] = {osattn::kBoxInner, osattn::kBoxRows, 1, 1};
+  const cuuint32_t box[4] = {osattn::kBoxInner, static_cast<cuuint32_t>(box_rows), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = g_encode_tiled(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -503,6 +504,26 @@ int softmax_rows_offload_impl(const void* in_h, void* out_h, float* lse_h, void*
 }  // namespace
 
 namespace osattn {
+
+int api_device(ApiDevice* out) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != OSATTN_OK) return rc;
+  if (cudaGetDevice(&out->device) != cudaSuccess) return OSATTN_ERR_CUDA;
+  out->num_sms = st->num_sms;
+  out->status = st->status;
+  out->wait_limit_ns = g_wait_limit_ns.load();
+  return OSATTN_OK;
+}
+
+int api_strides(const int64_t* in, int H, int N, int d, int dtype, long long* out) {
+  return take_strides(in, H, N, d, dtype, out);
+}
+
+int api_encode_map(CUtensorMap* map, const void* base, int fp16, int d, int N, int H, int B,
+                   const long long* st, int box_rows) {
+  return encode_map(map, base, fp16, d, N, H, B, st, box_rows);
+}
 
 int validate_splitkv(const void* Q, const void* K, const void* V, const void* O, const float* LSE,
                      int B, int H, int Nq, int Nkv, int d, float scale, const int32_t* key_len,

@@ -11,6 +11,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -36,10 +37,21 @@ EXPORTS = ("osattn_fwd", "osattn_fwd_strided", "osattn_fwd_splitkv",
            "osattn_softmax_rows_offload",
            "osattn_status_string", "osattn_get_device_status",
            "osattn_version", "osattn_set_wait_limit_ns", "osattn_test_wait_timeout",
-           "osattn_last_timeout_site", "osattn_step_trace_read")
+           "osattn_last_timeout_site", "osattn_step_trace_read",
+           "osattn_mask_plan", "osattn_mask_plan_bytes", "osattn_fwd_mod", "osattn_bwd_mod",
+           "osattn_bwd_mod_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
+
+
+class _Score(ctypes.Structure):
+    """struct osattn_score of include/osattn.h."""
+
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("rel_table", ctypes.c_void_p), ("rel_map", ctypes.c_void_p),
+                ("rel_num", ctypes.c_int), ("rel_range", ctypes.c_int),
+                ("q_offset", ctypes.c_int)]
 
 
 class OsattnError(RuntimeError):
@@ -109,6 +121,20 @@ def lib():
             L.osattn_last_timeout_site.restype = i32
             L.osattn_step_trace_read.argtypes = [vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)]
             L.osattn_step_trace_read.restype = i32
+            sz = ctypes.c_size_t
+            L.osattn_mask_plan_bytes.argtypes = [i32, i32]
+            L.osattn_mask_plan_bytes.restype = sz
+            L.osattn_mask_plan.argtypes = [vp, sz] + [i32] * 6 + [vp] * 4
+            L.osattn_mask_plan.restype = i32
+            scp = ctypes.POINTER(_Score)
+            L.osattn_fwd_mod.argtypes = ([vp] * 5 + [i32] * 6 + [i64p] * 4 +
+                                         [ctypes.c_float, scp, vp, i32, vp])
+            L.osattn_fwd_mod.restype = i32
+            L.osattn_bwd_mod_workspace_bytes.argtypes = [i32] * 4
+            L.osattn_bwd_mod_workspace_bytes.restype = sz
+            L.osattn_bwd_mod.argtypes = ([vp] * 10 + [i32] * 6 + [i64p] * 8 +
+                                         [ctypes.c_float, scp, vp, i32, vp, sz, vp])
+            L.osattn_bwd_mod.restype = i32
             _lib = L
         return _lib
 
@@ -514,6 +540,309 @@ def softmax_rows_offload(x_host, out_host=None, lse_host=None, x=None, out=None,
     if st != OK:
         raise OsattnError(st, "osattn_softmax_rows_offload")
     return out_host, lse_host
+
+
+# ---------------------------------------------------------------- modified scores
+class MaskPlan:
+    """Which keys each query row sees: what mask_plan() returns and fwd_mod()
+    and bwd_mod() take.  `buffer` is private to the library."""
+
+    __slots__ = ("buffer", "B", "Nq", "Nkv", "q_offset")
+
+    def __init__(self, buffer, B, Nq, Nkv, q_offset):
+        self.buffer, self.B, self.Nq, self.Nkv, self.q_offset = buffer, B, Nq, Nkv, q_offset
+
+
+def _int32(t, shape, device, name):
+    import torch
+
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a CUDA int32 tensor of shape {list(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on another device")
+    return t.contiguous()
+
+
+def _on(device):
+    """The context of calls for tensors of `device`."""
+    import contextlib
+
+    import torch
+
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _stream_for(stream, device):
+    import torch
+
+    return torch.cuda.current_stream(device) if stream is None else stream
+
+
+def _keep(stream, device, *tensors):
+    """Temporaries of this call, used on `stream`: not to be handed out again
+    before the work there is done."""
+    import torch
+
+    if stream != torch.cuda.current_stream(device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _strides3(a, b, c):
+    return (ctypes.c_int64 * 3)(a, b, c)
+
+
+def _view_strides(t, name):
+    """(b, h, row) element strides of a [B, H, N, d] view.  The stride of an
+    axis of length 1 is never used to reach an element; one that the library
+    would refuse is replaced."""
+    b, h, n, one = t.stride()
+    if one != 1:
+        raise ValueError(f"the last (d) axis of {name} must have stride 1")
+    if min(t.shape) == 1:
+        B, H, N, d = t.shape
+        n = d if N == 1 else n
+        h = max(n * N, 8) if H == 1 else h
+        b = max(h * H, 8) if B == 1 else b
+    return _strides3(b, h, n)
+
+
+def mask_plan(B: int, Nq: int, Nkv: int, causal: bool = False, window: int = 0, q_offset: int = 0,
+              key_len=None, prefix_len=None, doc_ids=None, device=None, out=None, stream=None):
+    """The keys that each of B x Nq query rows sees, for fwd_mod() and
+    bwd_mod(); one plan serves every layer and both passes of a step.
+
+    Row i stands at position p = i + q_offset; key j is visible to it iff
+    j < key_len[b]; with `causal` j <= p or j < prefix_len[b]; with a window
+    |j - p| < window; with doc_ids ([B, Nkv] int32) j and p lie in one run of
+    equal, non-negative ids.  key_len, prefix_len: CUDA int32 [B].  `out`: a
+    MaskPlan of the same B and Nq to overwrite."""
+    import torch
+
+    B, Nq, Nkv, window, q_offset = int(B), int(Nq), int(Nkv), int(window), int(q_offset)
+    for t in (key_len, prefix_len, doc_ids):
+        if t is not None:
+            device = t.device if device is None else torch.device(device)
+            break
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("a mask plan lives on a CUDA device")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    key_len = _int32(key_len, (B,), device, "key_len")
+    prefix_len = _int32(prefix_len, (B,), device, "prefix_len")
+    doc_ids = _int32(doc_ids, (B, Nkv), device, "doc_ids")
+    need = int(lib().osattn_mask_plan_bytes(B, Nq))
+    with _on(device):
+        stream = _stream_for(stream, device)
+        if out is None:
+            buffer = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+            _keep(stream, device, buffer)
+        else:
+            buffer = out.buffer
+            if out.B != B or out.Nq != Nq or buffer.device != device:
+                raise ValueError("out must be a MaskPlan of the same B, Nq and device")
+        st = lib().osattn_mask_plan(buffer.data_ptr(), buffer.numel(), B, Nq, Nkv, q_offset,
+                                    int(bool(causal)), window, *(
+                                        None if t is None else t.data_ptr()
+                                        for t in (key_len, prefix_len, doc_ids)),
+                                    stream.cuda_stream)
+        _keep(stream, device, key_len, prefix_len, doc_ids)
+    if st != OK:
+        raise OsattnError(st, "osattn_mask_plan")
+    if out is not None:
+        out.Nkv, out.q_offset = Nkv, q_offset
+        return out
+    return MaskPlan(buffer, B, Nq, Nkv, q_offset)
+
+
+def rel_buckets(num_buckets: int, max_distance: int, bidirectional: bool = True):
+    """A bucket map for fwd_mod()'s rel_map: int32 [2 * max_distance + 1], the
+    bucket of each distance (key position less query position) from
+    -max_distance to max_distance.  Small distances get a bucket each, the
+    rest share buckets spaced by the logarithm up to max_distance; with
+    `bidirectional` one half of the buckets is for keys behind the query,
+    otherwise all such keys fall into bucket 0.  A CPU tensor."""
+    import torch
+
+    num_buckets, max_distance = int(num_buckets), int(max_distance)
+    n = num_buckets // 2 if bidirectional else num_buckets
+    small = n // 2
+    if small < 1 or max_distance <= small:
+        raise ValueError("need at least 2 buckets a side and max_distance above the exact ones")
+    out = []
+    for rel in range(-max_distance, max_distance + 1):
+        base = n if bidirectional and rel > 0 else 0
+        dist = abs(rel) if bidirectional else max(-rel, 0)
+        if dist >= small:
+            dist = min(n - 1, small + int(math.log(dist / small) / math.log(max_distance / small)
+                                          * (n - small)))
+        out.append(base + dist)
+    return torch.tensor(out, dtype=torch.int32)
+
+
+def _mod_shapes(q, k, v):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B, H, Nq, d], k and v [B, Hkv, Nkv, d]")
+    B, H, Nq, d = q.shape
+    Hkv, Nkv = k.shape[1], k.shape[2]
+    if tuple(k.shape) != (B, Hkv, Nkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [B, Hkv, Nkv, d] matching q")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("the number of key/value heads must divide the number of query heads")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k, v must share one dtype")
+    if not (q.is_cuda and k.is_cuda and v.is_cuda):
+        raise ValueError("q, k, v must be CUDA tensors")
+    if k.device != q.device or v.device != q.device:
+        raise ValueError("q, k, v must be on one device")
+    return B, H, Hkv, Nq, Nkv, d
+
+
+def _score(q, plan, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map):
+    """struct osattn_score of a call, and the tensors it points into."""
+    import torch
+
+    s = _Score(softcap=float(softcap))
+    if plan is not None:
+        if (plan.B, plan.Nq, plan.Nkv) != (B, Nq, Nkv) or plan.buffer.device != q.device:
+            raise ValueError("plan was made for other sizes or another device")
+        s.q_offset = plan.q_offset
+    held = []
+    if slopes is not None:
+        if tuple(slopes.shape) != (H,) or slopes.dtype != torch.float32 or slopes.device != q.device:
+            raise ValueError("slopes must be an fp32 tensor of shape [H] on q's device")
+        held.append(slopes.contiguous())
+        s.slopes = held[-1].data_ptr()
+    if (rel_table is None) != (rel_map is None):
+        raise ValueError("rel_table and rel_map go together")
+    if rel_table is not None:
+        if (rel_table.dim() != 2 or rel_table.shape[1] != H or rel_table.dtype != q.dtype
+                or rel_table.device != q.device):
+            raise ValueError("rel_table must be [buckets, H] with q's dtype and device")
+        if (rel_map.dim() != 1 or rel_map.numel() % 2 == 0 or rel_map.dtype != torch.int32
+                or rel_map.device != q.device):
+            raise ValueError("rel_map must be int32 [2 R + 1] on q's device")
+        held += [rel_table.contiguous(), rel_map.contiguous()]
+        s.rel_table, s.rel_map = held[-2].data_ptr(), held[-1].data_ptr()
+        s.rel_num, s.rel_range = rel_table.shape[0], rel_map.numel() // 2
+    return s, held
+
+
+def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0, slopes=None,
+            rel_table=None, rel_map=None, out=None, lse=None, stream=None):
+    """O, LSE = attention forward with modified scores: q [B,H,Nq,d], k/v
+    [B,Hkv,Nkv,d] with Hkv dividing H, bf16 or fp16, any views whose last axis
+    is contiguous.
+
+    The scaled score y of query position p and key j becomes
+    softcap * tanh(y / softcap) if softcap > 0, then y - slopes[h] |j - p|
+    (slopes: fp32 [H]) or y + rel_table[rel_map[clamp(j - p, -R, R) + R], h]
+    (rel_table: [buckets, H] in q's dtype; rel_map: int32 [2 R + 1], see
+    rel_buckets()).  plan: a MaskPlan, or None for no mask.  A row that sees
+    no key gets O = 0 and LSE = -inf."""
+    import torch
+
+    B, H, Hkv, Nq, Nkv, d = _mod_shapes(q, k, v)
+    dtype = _dtype_code(q)
+    score, held = _score(q, plan, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    device = q.device
+    with _on(device):
+        stream = _stream_for(stream, device)
+        made = []
+        if out is None:
+            out = torch.empty_like(q)
+            made.append(out)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.device != device:
+            raise ValueError("out must match q")
+        if lse is None:
+            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=device)
+            made.append(lse)
+        elif (tuple(lse.shape) != (B, H, Nq) or lse.dtype != torch.float32
+              or not lse.is_contiguous() or lse.device != device):
+            raise ValueError("lse must be contiguous fp32 [B, H, Nq] on q's device")
+        st = lib().osattn_fwd_mod(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq,
+            Nkv, d, _view_strides(q, "q"), _view_strides(k, "k"), _view_strides(v, "v"),
+            _view_strides(out, "out"), float(scale), ctypes.byref(score),
+            None if plan is None else plan.buffer.data_ptr(), dtype, stream.cuda_stream)
+        _keep(stream, device, *made, *held)
+    if st != OK:
+        raise OsattnError(st, "osattn_fwd_mod")
+    return out, lse
+
+
+def bwd_mod_workspace_bytes(B: int, H: int, Nq: int, rel_range: int = 0) -> int:
+    return int(lib().osattn_bwd_mod_workspace_bytes(int(B), int(H), int(Nq), int(rel_range)))
+
+
+def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap: float = 0.0,
+            slopes=None, rel_table=None, rel_map=None, dq=None, dk=None, dv=None, drel=None,
+            workspace=None, stream=None):
+    """dQ, dK, dV, and with a rel_table dRel [buckets, H], of fwd_mod() for the
+    upstream gradient `do`, from its outputs o and lse.  Arguments as for
+    fwd_mod(); dk and dv are summed over the query heads of a key head.
+    Outputs and the workspace (a CUDA uint8 tensor of at least
+    bwd_mod_workspace_bytes(B, H, Nq, R or 0) bytes) may be given."""
+    import torch
+
+    B, H, Hkv, Nq, Nkv, d = _mod_shapes(q, k, v)
+    dtype = _dtype_code(q)
+    device = q.device
+    for t in (o, do):
+        if t.shape != q.shape or t.dtype != q.dtype or t.device != device:
+            raise ValueError("o and do must be shaped, typed and placed like q")
+    if (tuple(lse.shape) != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()
+            or lse.device != device):
+        raise ValueError("lse must be contiguous fp32 [B, H, Nq] on q's device")
+    score, held = _score(q, plan, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map)
+    if drel is not None and rel_table is None:
+        raise ValueError("drel needs a rel_table")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _on(device):
+        stream = _stream_for(stream, device)
+        made = []
+        grads = []
+        for g, ref in ((dq, q), (dk, k), (dv, v), (drel, rel_table)):
+            if g is None and ref is not None:
+                g = torch.empty_like(ref, memory_format=torch.contiguous_format) \
+                    if ref is rel_table else torch.empty_like(ref)
+                made.append(g)
+            elif g is not None and (g.shape != ref.shape or g.dtype != ref.dtype or g.device != device):
+                raise ValueError("gradients must be shaped, typed and placed like their tensors")
+            grads.append(g)
+        dq, dk, dv, drel = grads
+        if drel is not None and not drel.is_contiguous():
+            raise ValueError("drel must be contiguous")
+        if workspace is None:
+            workspace = torch.empty(bwd_mod_workspace_bytes(B, H, Nq, score.rel_range),
+                                    dtype=torch.uint8, device=device)
+            made.append(workspace)
+        elif not workspace.is_contiguous() or workspace.device != device:
+            raise ValueError("workspace must be contiguous on q's device")
+        names = ("q", "k", "v", "o", "do", "dq", "dk", "dv")
+        ts = (q, k, v, o, do, dq, dk, dv)
+        st = lib().osattn_bwd_mod(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if drel is None else drel.data_ptr(), B,
+            H, Hkv, Nq, Nkv, d, *(_view_strides(t, n) for t, n in zip(ts, names)), float(scale),
+            ctypes.byref(score), None if plan is None else plan.buffer.data_ptr(), dtype,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream.cuda_stream)
+        _keep(stream, device, *made, *held)
+    if st != OK:
+        raise OsattnError(st, "osattn_bwd_mod")
+    return (dq, dk, dv) if drel is None else (dq, dk, dv, drel)
 
 
 def get_device_status(stream=None) -> int:

@@ -20,6 +20,10 @@
  *                  osattn_fwd_offload (host-memory tensors, pipelined copies)
  *   backward       osattn_bwd, osattn_bwd_strided, osattn_bwd_offload
  *   row softmax    osattn_softmax_rows, osattn_softmax_rows_offload
+ *   modified scores  osattn_fwd_mod, osattn_bwd_mod (tanh cap, distance slopes
+ *                  or a learned bias by distance bucket; shared key/value
+ *                  heads), with the masks of osattn_mask_plan (causal, window,
+ *                  prefix, packed documents, key lengths)
  *   helpers        workspace sizes, status strings, the device status word,
  *                  the version, and test hooks for the bounded waits
  *
@@ -445,6 +449,109 @@ int osattn_last_timeout_site(void);
  * OSATTN_ERR_UNSUPPORTED.
  */
 int osattn_step_trace_read(void* host, size_t bytes, size_t* needed);
+
+/* ------------------------------------------------------- modified scores */
+
+/*
+ * osattn_mask_plan - the keys that each query row sees, as one interval a
+ * row, for osattn_fwd_mod and osattn_bwd_mod.  A plan depends on the masks
+ * only, so one plan serves every layer and both passes of a step.
+ *
+ * Query row i of batch entry b stands at position p = i + q_offset among the
+ * keys.  Key j < Nkv is visible to it iff all of these hold:
+ *   j < min(max(key_len[b], 0), Nkv)            (key_len not NULL)
+ *   j <= p, or j < prefix_len[b]                (causal; prefix_len may be NULL)
+ *   |j - p| < window                            (window > 0)
+ *   j and p lie in one document                 (doc_ids not NULL)
+ * A document is a run of equal, non-negative ids in doc_ids[b][0 .. Nkv): the
+ * same id again after another one is another document, and positions with a
+ * negative id, or outside [0, Nkv), see nothing.
+ *
+ *   plan       device, 16-byte aligned, osattn_mask_plan_bytes(B, Nq) bytes
+ *              (written).  Its content is private to the library.
+ *   B, Nq, Nkv >= 1; Nq, Nkv <= 2^30;  |q_offset| <= 2^30
+ *   window     0: none
+ *   key_len, prefix_len   device int32 [B] or NULL; prefix_len needs causal
+ *   doc_ids    device int32 [B, Nkv] contiguous, or NULL
+ * Enqueued on `stream`; errors as for osattn_fwd.
+ */
+size_t osattn_mask_plan_bytes(int B, int Nq);
+int osattn_mask_plan(void* plan, size_t plan_bytes, int B, int Nq, int Nkv, int q_offset,
+                     int causal, int window, const int32_t* key_len, const int32_t* prefix_len,
+                     const int32_t* doc_ids, void* stream);
+
+/*
+ * What happens to a scaled score before the softmax.  For query row i, with
+ * p = i + q_offset, and key j:
+ *   y = scale * <Q[b,h,i,:], K[b,h/(H/Hkv),j,:]>
+ *   y = softcap * tanh(y / softcap)                         (softcap > 0)
+ *   y = y - slopes[h] * |j - p|                             (slopes), or
+ *   y = y + rel_table[rel_map[clamp(j - p, -R, R) + R]][h]  (rel_table), R = rel_range
+ * slopes and rel_table exclude each other (OSATTN_ERR_INVALID_ARG); softcap
+ * with rel_table is OSATTN_ERR_UNSUPPORTED.
+ */
+typedef struct osattn_score {
+  float softcap;          /* >= 0, finite; 0: no cap */
+  const float* slopes;    /* device fp32 [H] or NULL */
+  const void* rel_table;  /* device [rel_num, H] contiguous, element type `dtype`, or NULL */
+  const int32_t* rel_map; /* device int32 [2 R + 1]: bucket of each distance -R .. R; an entry
+                             outside [0, rel_num) adds nothing and has no gradient */
+  int rel_num;            /* >= 1 */
+  int rel_range;          /* R: 1 .. 1024 (more: OSATTN_ERR_UNSUPPORTED) */
+  int q_offset;           /* position of query row 0, the one the plan was made with */
+} osattn_score;
+
+/*
+ * osattn_fwd_mod - attention forward with modified scores:
+ *     O[b,h,i,:] = sum_j e^{y_j} V[b,h/(H/Hkv),j,:] / sum_j e^{y_j},  LSE = log sum_j e^{y_j}
+ * over the keys j that the plan lets row i see.  A row that sees none gets
+ * O = 0 and LSE = -inf.
+ *
+ *   Q, O    device [B, H, Nq, d], K, V  device [B, Hkv, Nkv, d], with element
+ *           strides as for osattn_fwd_strided (NULL: contiguous); Hkv divides
+ *           H, and query heads h with the same h / (H / Hkv) share a key head
+ *   LSE     device fp32 [B, H, Nq] contiguous (written)
+ *   scale   finite;  score  NULL: y is the scaled score
+ *   plan    from osattn_mask_plan for the same B, Nq, Nkv and q_offset, or
+ *           NULL: every row sees every key
+ *   dtype   OSATTN_BF16 or OSATTN_FP16 (fp32: OSATTN_ERR_UNSUPPORTED);
+ *           products accumulate in fp32, P is rounded to dtype before P V
+ *   d       64 or 128
+ * K and V may hold anything (NaN included) at keys before the first and
+ * behind the last key that a block of 256 query rows (rows 256 n ..) sees;
+ * within that range a non-finite V row reaches all rows of the block.
+ * Alignment, ownership, asynchrony and errors as for osattn_fwd_strided.
+ */
+int osattn_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H,
+                   int Hkv, int Nq, int Nkv, int d, const int64_t* q_strides,
+                   const int64_t* k_strides, const int64_t* v_strides, const int64_t* o_strides,
+                   float scale, const osattn_score* score, const void* plan, int dtype,
+                   void* stream);
+
+/*
+ * osattn_bwd_mod - gradients of osattn_fwd_mod from its O and LSE and the
+ * upstream gradient dO: dQ, dK, dV (dK and dV summed over the query heads
+ * that share a key head) and, with a rel_table, its gradient
+ *     dRel[k][h] = sum over b and the visible pairs of bucket k of dy.
+ * slopes get no gradient.  Rows that see no key, and keys that no row sees,
+ * get zeros, whatever Q, dO, K and V hold there (K and V under the rule of
+ * osattn_fwd_mod).  No atomics: the same call gives the same bits.
+ *
+ *   dRel       device [rel_num, H], element type `dtype` (written), exactly
+ *              when score->rel_table is given, else NULL
+ *   workspace  device, 16-byte aligned, osattn_bwd_mod_workspace_bytes(B, H,
+ *              Nq, rel_range or 0 without a rel_table) bytes
+ * The other arguments as for osattn_fwd_mod; errors likewise.
+ */
+size_t osattn_bwd_mod_workspace_bytes(int B, int H, int Nq, int rel_range);
+int osattn_bwd_mod(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                   const float* LSE, void* dQ, void* dK, void* dV, void* dRel, int B, int H,
+                   int Hkv, int Nq, int Nkv, int d, const int64_t* q_strides,
+                   const int64_t* k_strides, const int64_t* v_strides, const int64_t* o_strides,
+                   const int64_t* do_strides, const int64_t* dq_strides,
+                   const int64_t* dk_strides, const int64_t* dv_strides, float scale,
+                   const osattn_score* score, const void* plan, int dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
