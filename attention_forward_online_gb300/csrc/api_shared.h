@@ -24,8 +24,8 @@ int api_device(ApiDevice* out);
 int api_strides(const int64_t* in, int H, int N, int d, int dtype, long long* out);
 
 // 4-D tensor map (d, N, H, B) of a 16-bit tensor with those strides: 64 x
-// box_rows boxes, 128-byte swizzle, zero fill.
+// box_rows x box_heads boxes, 128-byte swizzle, zero fill.
 int api_encode_map(CUtensorMap* map, const void* base, int fp16, int d, int N, int H, int B,
-                   const long long* st, int box_rows);
+                   const long long* st, int box_rows, int box_heads = 1);
 
 }  // namespace osattn

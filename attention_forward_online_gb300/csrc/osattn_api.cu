@@ -88,15 +88,16 @@ int device_state(DeviceState** out) {
 }
 
 // 4-D view (d, N, H, B) of a tensor with element strides st = {b, h, row}
-// (d contiguous), 64 x box_rows boxes, 128-byte swizzle, zero fill outside it.
+// (d contiguous), 64 x box_rows x box_heads boxes, 128-byte swizzle, zero fill outside it.
 int encode_map(CUtensorMap* map, const void* base, int fp16, int d, int N, int H, int B,
-               const long long* st, int box_rows = osattn::kBoxRows) {
+               const long long* st, int box_rows = osattn::kBoxRows, int box_heads = 1) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N),
                               static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(st[2]) * 2,
                                  static_cast<cuuint64_t>(st[1]) * 2,
                                  static_cast<cuuint64_t>(st[0]) * 2};
-  const cuuint32_t box[4] = {osattn::kBoxInner, static_cast<cuuint32_t>(box_rows), 1, 1};
+  const cuuint32_t box[4] = {osattn::kBoxInner, static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(box_heads), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = g_encode_tiled(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -521,8 +522,8 @@ int api_strides(const int64_t* in, int H, int N, int d, int dtype, long long* ou
 }
 
 int api_encode_map(CUtensorMap* map, const void* base, int fp16, int d, int N, int H, int B,
-                   const long long* st, int box_rows) {
-  return encode_map(map, base, fp16, d, N, H, B, st, box_rows);
+                   const long long* st, int box_rows, int box_heads) {
+  return encode_map(map, base, fp16, d, N, H, B, st, box_rows, box_heads);
 }
 
 int validate_splitkv(const void* Q, const void* K, const void* V, const void* O, const float* LSE,

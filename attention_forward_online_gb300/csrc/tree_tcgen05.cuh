@@ -1,0 +1,916 @@
+// tree_tcgen05.cuh - attention of drafted tokens over a paged cache: T <= 64
+// tokens a sequence (one: the ordinary decode step) attend to the cached keys
+// and to those drafts that their mask names, on the tcgen05 tensor cores.
+// Built for sm_103a; bf16 or fp16, d = 64 or 128.
+//
+// What it has to do is read the visible cache once, 4 d bytes a key and key
+// head, so the design is about keeping HBM busy:
+//   - The query heads of a key head and the drafts of a sequence are the rows
+//     of one 128-row operand (row = token x group + head of the group), so a
+//     key tile is loaded once for all of them.
+//   - One CTA per SM, persistent.  The key tiles of all sequences, key heads
+//     and row tiles form one list, cut into equal shares; a share's piece of
+//     one (sequence, key head, row tile) is a segment.  Ragged lengths need no
+//     plan on the host, and the loads of the next segment run while the last
+//     one is finished.  A segment that is not the whole of its unit leaves
+//     O / l in fp32 and its LSE, folded by the combine kernel in CTA order:
+//     no atomics.
+//   - Within a segment the even key tiles go to accumulator 0 and the odd ones
+//     to accumulator 1, each with its own running (m, l), so that two
+//     softmax warpgroups work while the tensor core fills the other's scores;
+//     the two states are merged once at the segment's end.
+//
+// Warps 0-3 and 4-7: softmax of the even and odd tiles, one row a thread; 8-11
+// rescale O; 12 TMA producer (lane x loads box x of a tile, a box lying in one
+// page); 13 MMA issue.  Tensor memory: S0, S1 (P in 16 bits over them), O0, O1.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mod_common.cuh"
+#include "sm100_ptx.cuh"
+#include "tc_attn_mma.cuh"
+#include "tree_internal.h"
+
+namespace osattn {
+namespace tree {
+
+constexpr int BM = 128;
+constexpr int BN = 128;
+constexpr int kThreads = 512;
+constexpr int kCorrWarp0 = 8, kProducerWarp = 12, kMmaWarp = 13;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol0 = 256;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr unsigned kBadArg = 1u;  // OSATTN_ERR_INVALID_ARG in the status word
+
+enum : uint32_t {
+  kSiteQ = 81,
+  kSiteQEmpty = 82,
+  kSiteK = 83,
+  kSiteV = 84,
+  kSiteKEmpty = 85,
+  kSiteVEmpty = 86,
+  kSiteS = 87,
+  kSiteAlpha = 88,
+  kSiteP = 89,
+  kSiteO = 90,
+  kSiteOEmpty = 91,
+  kSiteMerge = 92,
+  kSiteZero = 93
+};
+
+template <int HD>
+struct Cfg {
+  static constexpr int kTileBytes = BN * HD * 2;
+  // K_i is read until S_i, two tiles ahead of the product with V_i, so V needs
+  // the deeper ring where not both fit.
+  static constexpr int kKSlots = HD == 128 ? 2 : 6;
+  static constexpr int kVSlots = HD == 128 ? 3 : 6;
+  static constexpr int kTileRegion = (1 + kKSlots + kVSlots) * kTileBytes;
+};
+
+struct __align__(16) Bars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t s_full[2];
+  uint64_t alpha_full[2];  // 128 arrivals
+  uint64_t p_full[2];      // 256 arrivals: softmax and correction
+  uint64_t o_full;         // the segment's last product is done
+  uint64_t o_empty;        // 256 arrivals: the accumulators have been read
+  uint64_t merge;          // 256 arrivals: both states of the segment are stored
+  uint64_t mma_drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int start_b, start_base, total;
+  int warp_sum[16];
+  float alpha[2][BM];
+  float2 state[2][2][BM];  // [segment parity][accumulator][row]: m, l
+};
+
+template <int HD>
+constexpr int smem_bytes() {
+  return Cfg<HD>::kTileRegion + static_cast<int>(sizeof(Bars)) + 1024;
+}
+
+struct Params {
+  uint16_t* O;
+  long long o_sb, o_sh, o_sn;
+  float* LSE;  // [B, H, T]
+  const int32_t* table;
+  const int32_t* ctx;
+  const long long* mask;  // [B, T] or null
+  int B, H, Hkv, group, T;
+  int tok_tile;   // tokens of a row tile: its rows are tok_tile * group <= 128
+  int row_tiles;  // ceil(T / tok_tile)
+  int max_pages, page, num_pages;
+  int box_rows;   // keys of one TMA box: min(page, 128)
+  int window;
+  float scale_log2, cap_c1, cap2;
+  const float* slopes;
+  float* o_part;    // [2 grid][slot_rows][d]
+  float* lse_part;  // [2 grid][slot_rows]
+  int slot_rows;    // tok_tile' * group, tok_tile' = min(T, tok_tile)
+  int* head;        // [B + 1]: first list position of each sequence, and the list's length
+  unsigned int* status;
+  uint64_t wait_limit_ns;
+};
+
+template <uint32_t N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kF16) return pack_f16x2(lo, hi);
+  else return pack_bf16x2(lo, hi);
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) return;
+  }
+}
+
+__device__ __forceinline__ float max128(const uint32_t* v) {
+  float a[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 8]));
+#pragma unroll
+  for (int j = 16; j < BN; j += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      a[i] = fmax3(a[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 8 + i]));
+  return fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+}
+
+// Cached keys of a sequence, kept within its page table.
+__device__ __forceinline__ int ctx_of(const Params& p, int b) {
+  const long long room = static_cast<long long>(p.max_pages) * p.page - p.T;
+  const int c = __ldg(p.ctx + b);
+  return c < 0 ? 0 : (c > room ? static_cast<int>(room) : c);
+}
+// First key that any draft can see, and the key tiles [first, first + n).
+__device__ __forceinline__ int first_key(const Params& p, int ctx) {
+  return p.window > 0 ? max(0, ctx - p.window + 1) : 0;
+}
+__device__ __forceinline__ void key_tiles(const Params& p, int ctx, int& first, int& n) {
+  first = first_key(p, ctx) / BN;
+  n = (ctx + p.T + BN - 1) / BN - first;  // T >= 1: at least one
+}
+
+__device__ __forceinline__ unsigned long long draft_bits(int T) {
+  return T >= 64 ? ~0ull : (1ull << T) - 1;
+}
+// The drafts that draft t of sequence b sees.
+__device__ __forceinline__ unsigned long long mask_of(const Params& p, int b, int t) {
+  if (!p.mask) return t >= 63 ? ~0ull : (2ull << t) - 1;
+  return static_cast<unsigned long long>(__ldg(p.mask + static_cast<long long>(b) * p.T + t)) &
+         draft_bits(p.T);
+}
+// A draft's place behind the context: how many other drafts lie on its line.
+__device__ __forceinline__ int depth_of(unsigned long long mask) {
+  return mask ? __popcll(mask) - 1 : 0;
+}
+
+// Shares of a list of `total` key tiles: no share is empty.
+__device__ __forceinline__ int shares(int total, int grid) { return total < grid ? total : grid; }
+
+// A share's next segment; every role walks the same ones.
+struct Walk {
+  int at, end;  // list positions
+  int b, base;  // sequence and its first list position
+  int ctx, first, n_b;
+  // the segment
+  int hk, rt, tile0, n;
+  bool head_cut, tail_cut;  // misses the unit's first or last tiles
+};
+
+__device__ __forceinline__ Walk walk_start(const Params& p, const Bars* bars) {
+  Walk w;
+  const long long total = bars->total, c = blockIdx.x, G = shares(bars->total, gridDim.x);
+  w.at = c < G ? static_cast<int>(c * total / G) : 0;
+  w.end = c < G ? static_cast<int>((c + 1) * total / G) : 0;
+  w.b = bars->start_b;
+  w.base = bars->start_base;
+  if (w.at < w.end) {
+    w.ctx = ctx_of(p, w.b);
+    key_tiles(p, w.ctx, w.first, w.n_b);
+  }
+  return w;
+}
+
+__device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
+  if (w.at >= w.end) return false;
+  const int units = p.Hkv * p.row_tiles;
+  int in = w.at - w.base;
+  if (in >= units * w.n_b) {
+    w.base += units * w.n_b;
+    ++w.b;
+    w.ctx = ctx_of(p, w.b);
+    key_tiles(p, w.ctx, w.first, w.n_b);
+    in = w.at - w.base;
+  }
+  const int unit = in / w.n_b, tile = in - unit * w.n_b;
+  w.hk = unit / p.row_tiles;
+  w.rt = unit - w.hk * p.row_tiles;
+  w.tile0 = w.first + tile;
+  w.n = min(w.n_b - tile, w.end - w.at);
+  w.head_cut = tile > 0;
+  w.tail_cut = tile + w.n < w.n_b;
+  w.at += w.n;
+  return true;
+}
+
+// ------------------------------------------------------------------ softmax
+template <int HD, bool kF16, int MODE>
+__device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32_t tmem, int t,
+                                             WaitCtl wc) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3;
+  const int row = quarter * 32 + lane;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const uint32_t s_addr = lane_base + static_cast<uint32_t>(t * BN);
+  const int tl = row / p.group, g = row - tl * p.group;
+  const float c = p.scale_log2;
+  uint32_t s_phase = 0, seg = 0;
+  bool ok = true;
+  for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
+    const int tok = w.rt * p.tok_tile + tl;
+    const bool live = tl < p.tok_tile && tok < p.T;
+    const int h = w.hk * p.group + g;
+    unsigned long long mask = live ? mask_of(p, w.b, tok) : 0ull;
+    const int depth = depth_of(mask);
+    int lo = w.ctx + p.T;  // first key of the row's context; a padding row sees nothing
+    if (mask) {
+      lo = 0;
+      if (p.window > 0) {
+        lo = max(0, w.ctx + depth - p.window + 1);
+        if (p.T > p.window) {  // drafts of its line that are a window away
+          for (int u = 0; u < p.T; ++u)
+            if (((mask >> u) & 1) && abs(depth - depth_of(mask_of(p, w.b, u))) >= p.window)
+              mask &= ~(1ull << u);
+        }
+      }
+    }
+    [[maybe_unused]] float slope2 = 0.f;
+    if constexpr (mode_slopes(MODE)) slope2 = live ? __ldg(p.slopes + h) * kModLog2e : 0.f;
+    const int tile_lo = p.window > 0 ? max(0, w.ctx + p.T - p.window) : 0;  // every row's context starts at or before it
+    float m = -INFINITY, l = 0.f;
+    for (int i = t; ok && i < w.n; i += 2) {
+      ok = mbar_wait(&bars->s_full[t], s_phase & 1u, wc, kSiteS);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ++s_phase;
+      tc_fence_after_sync();
+      uint32_t v[BN];
+#pragma unroll
+      for (int ch = 0; ch < BN / 32; ++ch) tmem_ld_32x32b_x32(s_addr + ch * 32, v + ch * 32);
+      tmem_ld_wait();
+#pragma unroll
+      for (int ch = 0; ch < BN / 32; ++ch) reg_fence32(v + ch * 32);
+      const int k0 = (w.tile0 + i) * BN;
+      const bool tail = k0 + BN > w.ctx;  // holds drafts or keys behind them
+#pragma unroll
+      for (int e = 0; e < BN; ++e) {
+        const float s = __uint_as_float(v[e]);
+        float x;
+        if constexpr (mode_cap(MODE))
+          x = fmaf(cap_r(s, p.cap_c1), -2.f * p.cap2, p.cap2);
+        else
+          x = s * c;
+        v[e] = __float_as_uint(x);
+      }
+      if constexpr (mode_slopes(MODE)) {
+        const float d0 = static_cast<float>(w.ctx + depth - k0);  // distance of the tile's first key
+        if (!tail) {
+#pragma unroll
+          for (int e = 0; e < BN; ++e)
+            v[e] = __float_as_uint(fmaf(-slope2, d0 - static_cast<float>(e), __uint_as_float(v[e])));
+        } else {
+#pragma unroll
+          for (int e = 0; e < BN; ++e) {
+            const int u = k0 + e - w.ctx;
+            float dist = d0 - static_cast<float>(e);
+            if (u >= 0) dist = u < p.T ? fabsf(static_cast<float>(depth - depth_of(mask_of(p, w.b, u)))) : 0.f;
+            v[e] = __float_as_uint(fmaf(-slope2, dist, __uint_as_float(v[e])));
+          }
+        }
+      }
+      if (tail || k0 < tile_lo) {
+        // visible keys of the tile as 128 bits: context keys [lo, ctx), then the mask
+        const int nc = w.ctx - k0;  // keys of the tile before the drafts (may be negative or > 128)
+        const int from = lo - k0;
+        unsigned long long bits[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int a = 64 * x;  // bits a .. a + 63
+          const int up = min(max(nc - a, 0), 64), dn = min(max(from - a, 0), 64);
+          unsigned long long cb = up >= 64 ? ~0ull : (1ull << up) - 1;
+          cb &= dn >= 64 ? 0ull : ~0ull << dn;
+          const int sh = nc - a;  // where draft 0 falls
+          unsigned long long db = 0ull;
+          if (sh >= 0 && sh < 64) db = mask << sh;
+          else if (sh < 0 && sh > -64) db = mask >> -sh;
+          bits[x] = cb | db;
+        }
+#pragma unroll
+        for (int e = 0; e < BN; ++e)
+          if (!((bits[e >> 6] >> (e & 63)) & 1ull)) v[e] = __float_as_uint(-INFINITY);
+      } else if (!live) {
+#pragma unroll
+        for (int e = 0; e < BN; ++e) v[e] = __float_as_uint(-INFINITY);
+      } else if (!mask) {
+#pragma unroll
+        for (int e = 0; e < BN; ++e) v[e] = __float_as_uint(-INFINITY);
+      }
+      const float m_new = fmaxf(m, max128(v));
+      const float alpha = (m_new == m) ? 1.f : ex2_approx(m - m_new);
+      bars->alpha[t][row] = alpha;
+      mbar_arrive(&bars->alpha_full[t]);
+      const float neg_m = (m_new == -INFINITY) ? 0.f : -m_new;
+      const uint64_t nm2 = f2_pack(neg_m, neg_m);
+      uint64_t rs_a = 0, rs_b = 0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int x = half * 64 + 2 * e;
+          float x0, x1;
+          f2_unpack(f2_add(f2_pack(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), nm2), x0, x1);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          const uint64_t pp = f2_pack(p0, p1);
+          if (e & 1)
+            rs_b = f2_add(rs_b, pp);
+          else
+            rs_a = f2_add(rs_a, pp);
+          pk[e] = pack2<kF16>(p0, p1);
+        }
+        tmem_st_32x32b_x32(s_addr + half * 32, pk);
+      }
+      float r0, r1, r2, r3;
+      f2_unpack(rs_a, r0, r1);
+      f2_unpack(rs_b, r2, r3);
+      l = fmaf(l, alpha, (r0 + r1) + (r2 + r3));
+      m = m_new;
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&bars->p_full[t]);
+    }
+    if (!ok) break;
+    // ---- merge the two states; warpgroup t finishes columns t d/2 .. of both
+    bars->state[seg & 1][t][row] = make_float2(m, l);
+    mbar_arrive(&bars->merge);
+    ok = mbar_wait(&bars->merge, seg & 1u, wc, kSiteMerge);
+    if (ok) ok = mbar_wait(&bars->o_full, seg & 1u, wc, kSiteO);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    tc_fence_after_sync();
+    const float2 s0 = bars->state[seg & 1][0][row], s1 = bars->state[seg & 1][1][row];
+    const float M = fmaxf(s0.x, s1.x);
+    const float f0 = s0.x == -INFINITY ? 0.f : ex2_approx(s0.x - M);
+    const float f1 = s1.x == -INFINITY ? 0.f : ex2_approx(s1.x - M);
+    const float L = fmaf(s0.y, f0, s1.y * f1);
+    const bool empty = L == 0.f;
+    const float inv = empty ? 0.f : 1.f / L;
+    const float g0 = f0 * inv, g1 = f1 * inv;
+    const bool whole = !w.head_cut && !w.tail_cut;
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (w.head_cut ? 0 : 1);
+    constexpr int kHalf = HD / 2;
+    const uint32_t o_addr = lane_base + kOCol0 + static_cast<uint32_t>(t * kHalf);
+    uint16_t* orow = p.O + w.b * p.o_sb + h * p.o_sh + tok * p.o_sn + t * kHalf;
+    const long long prow = static_cast<long long>(slot) * p.slot_rows + row;
+    float* part = p.o_part + prow * HD + t * kHalf;
+#pragma unroll
+    for (int ch = 0; ch < kHalf / 32; ++ch) {
+      uint32_t a0[32], a1[32];
+      tmem_ld_32x32b_x32(o_addr + ch * 32, a0);
+      if (w.n > 1) tmem_ld_32x32b_x32(o_addr + HD + ch * 32, a1);
+      tmem_ld_wait();
+      reg_fence32(a0);
+      reg_fence32(a1);
+      float o[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        o[e] = __uint_as_float(a0[e]) * g0;
+        if (w.n > 1) o[e] = fmaf(__uint_as_float(a1[e]), g1, o[e]);
+        if (empty) o[e] = 0.f;
+      }
+      if (live) {
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + ch * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack2<kF16>(o[8 * e], o[8 * e + 1]), pack2<kF16>(o[8 * e + 2], o[8 * e + 3]),
+                                pack2<kF16>(o[8 * e + 4], o[8 * e + 5]), pack2<kF16>(o[8 * e + 6], o[8 * e + 7]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(part + ch * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+    }
+    tc_fence_before_sync();
+    mbar_arrive(&bars->o_empty);
+    if (live && t == 0) {
+      const float lse = empty ? -INFINITY : (M + log2f(L)) * kLn2;
+      if (whole)
+        p.LSE[(static_cast<long long>(w.b) * p.H + h) * p.T + tok] = lse;
+      else
+        p.lse_part[prow] = lse;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ correction
+template <int HD>
+__device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uint8_t* sV, uint32_t tmem,
+                                                WaitCtl wc) {
+  using C = Cfg<HD>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3;
+  const int row = quarter * 32 + lane;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  uint32_t a_phase[2] = {0, 0}, vc = 0;  // vc: V tiles so far
+  bool ok = true;
+  for (Walk w = walk_start(p, bars); ok && walk_next(p, w);) {
+    // Drafts that some draft sees; the rows of V of the others, like those of
+    // keys before the window and behind the drafts, are zeroed below.
+    unsigned long long seen = 0ull;
+    int seen_for = -1;
+    for (int i = 0; ok && i < w.n; ++i, ++vc) {
+      const int t = i & 1;
+      const int k0 = (w.tile0 + i) * BN;
+      const int lo = first_key(p, w.ctx);
+      if (k0 < lo || k0 + BN > w.ctx) {
+        if (seen_for != w.b) {
+          for (int u = 0; u < p.T; ++u) seen |= mask_of(p, w.b, u);
+          seen_for = w.b;
+        }
+        ok = mbar_wait(&bars->v_full[vc % C::kVSlots], (vc / C::kVSlots) & 1u, wc, kSiteZero);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int u = k0 + row - w.ctx;
+        if (k0 + row < lo || (u >= 0 && (u >= p.T || !((seen >> u) & 1ull)))) {
+          uint8_t* v = sV + (vc % C::kVSlots) * C::kTileBytes + row * 128;
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<uint4*>(v + cb * BN * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();
+      }
+      ok = mbar_wait(&bars->alpha_full[t], a_phase[t] & 1u, wc, kSiteAlpha);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ++a_phase[t];
+      const float alpha = bars->alpha[t][row];
+      // the accumulator's earlier products are done: S_t of this tile was
+      // issued after them
+      if (i >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        tc_fence_after_sync();
+        const uint64_t a2 = f2_pack(alpha, alpha);
+        const uint32_t o_addr = lane_base + kOCol0 + static_cast<uint32_t>(t * HD);
+#pragma unroll
+        for (int ch = 0; ch < HD / 32; ++ch) {
+          uint32_t orr[32];
+          tmem_ld_32x32b_x32(o_addr + ch * 32, orr);
+          tmem_ld_wait();
+          reg_fence32(orr);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float b0, b1;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(orr[2 * e]), __uint_as_float(orr[2 * e + 1])), a2), b0, b1);
+            orr[2 * e] = __float_as_uint(b0);
+            orr[2 * e + 1] = __float_as_uint(b1);
+          }
+          tmem_st_32x32b_x32(o_addr + ch * 32, orr);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&bars->p_full[t]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ producer
+// The whole warp: lane x loads box x of each tile.  A box that holds no
+// visible key, or whose page number is not one of the pool's, is read from
+// behind the pool, which fills it with zeros; the latter also sets the status.
+template <int HD>
+__device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
+                                              const CUtensorMap* tmV, const Params& p, Bars* bars,
+                                              uint8_t* sQ, uint8_t* sK, uint8_t* sV, WaitCtl wc) {
+  using C = Cfg<HD>;
+  const int lane = threadIdx.x & 31;
+  const int boxes = BN / p.box_rows;
+  const uint32_t q_bytes = static_cast<uint32_t>(p.tok_tile * p.group * HD * 2);
+  uint32_t kc = 0, seg = 0;  // key tiles and segments so far
+  bool ok = true;
+  for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
+    if (seg > 0) {
+      ok = warp_wait(&bars->q_empty, (seg - 1) & 1u, wc, kSiteQEmpty);
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars->q_full, q_bytes);
+#pragma unroll
+      for (int cb = 0; cb < HD / 64; ++cb)
+        tma_load_4d(sQ + cb * BM * 128, tmQ, &bars->q_full, cb * 64, w.hk * p.group,
+                    w.rt * p.tok_tile, w.b);
+    }
+    const int lo = first_key(p, w.ctx), end = w.ctx + p.T;
+    for (int i = 0; ok && i < w.n; ++i, ++kc) {
+      const int s = static_cast<int>(kc % C::kKSlots), sv = static_cast<int>(kc % C::kVSlots);
+      const uint32_t use = kc / C::kKSlots, use_v = kc / C::kVSlots;
+      const int k0 = (w.tile0 + i) * BN;
+      int page = p.num_pages, in_page = 0;
+      if (lane < boxes) {
+        const int key = k0 + lane * p.box_rows;
+        if (key < end && key + p.box_rows > lo) {
+          const int at = key / p.page;  // < max_pages: ctx + T fits the table
+          in_page = key - at * p.page;
+          page = __ldg(p.table + static_cast<long long>(w.b) * p.max_pages + at);
+          if (page < 0 || page >= p.num_pages) {
+            page = p.num_pages;
+            atomicMax(p.status, kBadArg);
+          }
+        }
+      }
+      if (use > 0) ok = warp_wait(&bars->k_empty[s], (use - 1) & 1u, wc, kSiteKEmpty);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[s], C::kTileBytes);
+      __syncwarp();
+      if (lane < boxes)
+#pragma unroll
+        for (int cb = 0; cb < HD / 64; ++cb)
+          tma_load_4d(sK + s * C::kTileBytes + cb * BN * 128 + lane * p.box_rows * 128, tmK,
+                      &bars->k_full[s], cb * 64, in_page, w.hk, page);
+      if (use_v > 0) ok = warp_wait(&bars->v_empty[sv], (use_v - 1) & 1u, wc, kSiteVEmpty);
+      if (!ok) {
+        ++kc;  // this K tile is in flight: the drain below covers it
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[sv], C::kTileBytes);
+      __syncwarp();
+      if (lane < boxes)
+#pragma unroll
+        for (int cb = 0; cb < HD / 64; ++cb)
+          tma_load_4d(sV + sv * C::kTileBytes + cb * BN * 128 + lane * p.box_rows * 128, tmV,
+                      &bars->v_full[sv], cb * 64, in_page, w.hk, page);
+    }
+    if (!ok) break;
+  }
+  // Let every load of this warp land before the CTA can exit (a V tile that
+  // was not issued makes its wait run into the limit, on the give-up path only).
+  if (lane == 0 && kc > 0) {
+    const uint32_t q_uses = ok ? seg : seg + 1;
+    if (q_uses > 0) drain_wait(&bars->q_full, (q_uses - 1) & 1u, wc.limit_ns);
+    for (uint32_t x = (kc > C::kKSlots ? kc - C::kKSlots : 0); x < kc; ++x)
+      drain_wait(&bars->k_full[x % C::kKSlots], (x / C::kKSlots) & 1u, wc.limit_ns);
+    for (uint32_t x = (kc > C::kVSlots ? kc - C::kVSlots : 0); x < kc; ++x)
+      drain_wait(&bars->v_full[x % C::kVSlots], (x / C::kVSlots) & 1u, wc.limit_ns);
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ MMA issuer
+template <int HD, bool kF16>
+__device__ __forceinline__ void mma_role(const Params& p, Bars* bars, uint32_t tmem, uint8_t* sQ,
+                                         uint8_t* sK, uint8_t* sV, WaitCtl wc) {
+  using C = Cfg<HD>;
+  const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+  const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);        // slot 0, K-major
+  const uint64_t v_desc = sdesc_sw128(smem_u32(sV), BN * 128, 1024);  // slot 0, MN-major
+  constexpr uint64_t kStep = static_cast<uint64_t>(C::kTileBytes >> 4);
+  uint32_t kc = 0, vc = 0, seg = 0, p_phase[2] = {0, 0};
+  bool ok = true;
+  for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
+    ok = warp_wait(&bars->q_full, seg & 1u, wc, kSiteQ);
+    if (!ok) break;
+    // scores of tile i into buffer i mod 2
+    auto scores = [&](int i) {
+      const uint32_t s = kc % C::kKSlots;
+      if (!warp_wait(&bars->k_full[s], (kc / C::kKSlots) & 1u, wc, kSiteK)) return false;
+      tc_fence_after_sync();
+      mma_abt_128<HD, kF16, true>(tmem + (i & 1) * BN, q_desc, k_desc + s * kStep);
+      mma_commit<true>(&bars->s_full[i & 1]);
+      mma_commit<true>(&bars->k_empty[s]);
+      if (i == w.n - 1) mma_commit<true>(&bars->q_empty);
+      ++kc;
+      return true;
+    };
+    ok = scores(0);
+    if (ok && w.n > 1) ok = scores(1);
+    for (int i = 0; ok && i < w.n; ++i) {
+      const int t = i & 1;
+      ok = warp_wait(&bars->p_full[t], p_phase[t] & 1u, wc, kSiteP);
+      if (!ok) break;
+      ++p_phase[t];
+      if (i == 0 && seg > 0) {
+        ok = warp_wait(&bars->o_empty, (seg - 1) & 1u, wc, kSiteOEmpty);
+        if (!ok) break;
+      }
+      const uint32_t s = vc % C::kVSlots;
+      ok = warp_wait(&bars->v_full[s], (vc / C::kVSlots) & 1u, wc, kSiteV);
+      if (!ok) break;
+      tc_fence_after_sync();
+      mma_tmem_a_128<HD, kF16, true>(tmem + kOCol0 + t * HD, tmem + t * BN, v_desc + s * kStep, i >= 2);
+      mma_commit<true>(&bars->v_empty[s]);
+      ++vc;
+      if (i == w.n - 1) mma_commit<true>(&bars->o_full);
+      if (i + 2 < w.n) ok = scores(i + 2);
+    }
+  }
+  mma_commit<true>(&bars->mma_drain);
+  drain_wait(&bars->mma_drain, 0, wc.limit_ns);
+  __syncwarp();
+}
+
+// Where this CTA's share starts in the list, and the list's length; CTA 0
+// also writes every sequence's first position for the combine kernel.
+__device__ __forceinline__ void find_start(const Params& p, Bars* bars) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = p.Hkv * p.row_tiles;
+  auto tiles_of = [&](int b) {
+    int first, n;
+    key_tiles(p, ctx_of(p, b), first, n);
+    return n * units;
+  };
+  // pass 0 sums, pass 1 scans; one pass over up to 512 sequences at a time
+  int total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int before = 0;
+    long long start = 0;
+    if (pass) start = static_cast<long long>(blockIdx.x) * total / shares(total, gridDim.x);
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + static_cast<int>(threadIdx.x);
+      const int mine = b < p.B ? tiles_of(b) : 0;
+      if (pass == 0 && b < p.B && blockIdx.x == 0 && __ldg(p.ctx + b) != ctx_of(p, b))
+        atomicMax(p.status, kBadArg);
+      int scan = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, scan, off);
+        if (lane >= off) scan += y;
+      }
+      if (lane == 31) bars->warp_sum[warp] = scan;
+      __syncthreads();
+      int pre = before, all = 0;
+      for (int x = 0; x < kThreads / 32; ++x) {
+        const int y = bars->warp_sum[x];
+        if (x < warp) pre += y;
+        all += y;
+      }
+      __syncthreads();
+      if (pass) {
+        const int base = pre + scan - mine;
+        if (b < p.B && start >= base && start < base + mine) {
+          bars->start_b = b;
+          bars->start_base = base;
+        }
+        if (blockIdx.x == 0 && b < p.B) p.head[b] = base;
+      }
+      before += all;
+    }
+    total = before;
+  }
+  if (threadIdx.x == 0) {
+    bars->total = total;
+    if (blockIdx.x == 0) p.head[p.B] = total;
+  }
+}
+
+template <int HD, bool kF16, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const Params p) {
+  using C = Cfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + C::kTileBytes;
+  uint8_t* sV = sK + C::kKSlots * C::kTileBytes;
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kTileRegion);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < C::kKSlots; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+    }
+    for (int s = 0; s < C::kVSlots; ++s) {
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->alpha_full[t], 128);
+      mbar_init(&bars->p_full[t], 256);
+    }
+    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->o_empty, 256);
+    mbar_init(&bars->merge, 256);
+    mbar_init(&bars->mma_drain, 1);
+    bars->abort_flag = 0;
+    bars->start_b = 0;
+    bars->start_base = 0;
+    fence_barrier_init();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  // rows of Q that no load writes (tok_tile * group < 128) stay zero
+  for (int x = threadIdx.x; x < C::kTileBytes / 16; x += kThreads)
+    reinterpret_cast<uint4*>(sQ)[x] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async();
+  __syncthreads();
+  find_start(p, bars);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
+
+  // 256 x 184 + 128 x 88 + 128 x 56 = 512 x 128 registers
+  if (warp < kCorrWarp0) {
+    regs_inc<184>();
+    softmax_role<HD, kF16, MODE>(p, bars, tmem, warp >> 2, wc);
+  } else if (warp < kProducerWarp) {
+    regs_dec<88>();
+    correction_role<HD>(p, bars, sV, tmem, wc);
+  } else {
+    regs_dec<56>();
+    if (warp == kProducerWarp)
+      producer_role<HD>(&tmQ, &tmK, &tmV, p, bars, sQ, sK, sV, wc);
+    else if (warp == kMmaWarp)
+      mma_role<HD, kF16>(p, bars, tmem, sQ, sK, sV, wc);
+  }
+
+  __syncwarp();
+  tmem_st_wait();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ combine
+// One warp a row: folds the partials of the CTAs that share the row's unit,
+// in CTA order, as (m, l) = (lse, 1) states.  Rows of units that one CTA did
+// whole are done already.
+template <int HD, bool kF16>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const Params p, int grid) {
+  constexpr int CPL = HD / 32;
+  const int per_unit = (p.slot_rows + 7) / 8;
+  const int unit_all = blockIdx.x / per_unit;
+  const int row = (blockIdx.x - unit_all * per_unit) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int units = p.Hkv * p.row_tiles;
+  const int b = unit_all / units, unit = unit_all - b * units;
+  const int hk = unit / p.row_tiles, rt = unit - hk * p.row_tiles;
+  const int tl = row / p.group, g = row - tl * p.group;
+  const int tok = rt * p.tok_tile + tl;
+  if (row >= p.slot_rows || tl >= p.tok_tile || tok >= p.T) return;
+  const int base = p.head[b], n_b = (p.head[b + 1] - base) / units;
+  const long long total = p.head[p.B], G = shares(p.head[p.B], grid);
+  const long long x0 = base + static_cast<long long>(unit) * n_b, x1 = x0 + n_b - 1;
+  // the share that holds list position x: the largest c with c total / G <= x
+  const int c0 = static_cast<int>(((x0 + 1) * G - 1) / total), c1 = static_cast<int>(((x1 + 1) * G - 1) / total);
+  if (c0 == c1) return;
+  float m = -INFINITY, l = 0.f, acc[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    const int slot = 2 * c + (c == c0 ? 1 : 0);
+    const long long prow = static_cast<long long>(slot) * p.slot_rows + row;
+    const float lse = p.lse_part[prow];
+    const float* src = p.o_part + prow * HD + lane * CPL;
+    float o[CPL];
+    if constexpr (CPL == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      o[0] = v.x; o[1] = v.y;
+    }
+    if (lse == -INFINITY) continue;
+    const float M = fmaxf(m, lse);
+    const float alpha = expf(m - M), beta = expf(lse - M);
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) acc[k] = fmaf(acc[k], alpha, beta * o[k]);
+    l = fmaf(l, alpha, beta);
+    m = M;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int h = hk * p.group + g;
+  uint16_t* dst = p.O + b * p.o_sb + h * p.o_sh + tok * p.o_sn + lane * CPL;
+#pragma unroll
+  for (int k = 0; k < CPL; k += 2)
+    *reinterpret_cast<uint32_t*>(dst + k) = pack2<kF16>(acc[k] * inv, acc[k + 1] * inv);
+  if (lane == 0) p.LSE[(static_cast<long long>(b) * p.H + h) * p.T + tok] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// ------------------------------------------------------------------ host
+constexpr int kLaunchRegs = 128;  // the setmaxnreg split above assumes it
+
+template <int HD, bool kF16, int MODE>
+cudaError_t set_attrs() {
+  static_assert(smem_bytes<HD>() <= 232448, "shared memory per CTA");
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, tree_kernel<HD, kF16, MODE>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(tree_kernel<HD, kF16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smem_bytes<HD>());
+}
+
+template <int HD, bool kF16>
+cudaError_t prepare() {
+  cudaError_t e;
+  if ((e = set_attrs<HD, kF16, kModPlain>()) != cudaSuccess) return e;
+  if ((e = set_attrs<HD, kF16, kModCap>()) != cudaSuccess) return e;
+  if ((e = set_attrs<HD, kF16, kModSlopes>()) != cudaSuccess) return e;
+  return set_attrs<HD, kF16, kModCapSlopes>();
+}
+
+template <int HD, bool kF16, int MODE>
+cudaError_t launch_mode(int grid, cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k,
+                        const CUtensorMap& v, const Params& p) {
+  tree_kernel<HD, kF16, MODE><<<grid, kThreads, smem_bytes<HD>(), s>>>(q, k, v, p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.row_tiles * ((p.slot_rows + 7) / 8);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  tree_combine_kernel<HD, kF16><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p, grid);
+  return cudaGetLastError();
+}
+
+template <int HD, bool kF16>
+cudaError_t launch(const TreeArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v) {
+  Params p;
+  p.O = static_cast<uint16_t*>(a.O);
+  p.o_sb = a.o_s[0];
+  p.o_sh = a.o_s[1];
+  p.o_sn = a.o_s[2];
+  p.LSE = a.LSE;
+  p.table = a.table;
+  p.ctx = a.ctx;
+  p.mask = reinterpret_cast<const long long*>(a.mask);
+  p.B = a.B;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.group = a.H / a.Hkv;
+  p.T = a.T;
+  p.tok_tile = tree_tok_tile(p.group);
+  p.row_tiles = (a.T + p.tok_tile - 1) / p.tok_tile;
+  p.max_pages = a.max_pages;
+  p.page = a.page;
+  p.num_pages = a.num_pages;
+  p.box_rows = a.page < BN ? a.page : BN;
+  p.window = a.window;
+  p.scale_log2 = a.scale * kModLog2e;
+  p.cap_c1 = a.softcap > 0.f ? 2.f * a.scale * kModLog2e / a.softcap : 0.f;
+  p.cap2 = a.softcap * kModLog2e;
+  p.slopes = a.slopes;
+  p.slot_rows = tree_slot_rows(p.group, a.T);
+  const int grid = a.num_sms < kTreeMaxCtas ? a.num_sms : kTreeMaxCtas;
+  p.head = static_cast<int*>(a.workspace);
+  p.o_part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + tree_head_bytes(a.B));
+  p.lse_part = p.o_part + static_cast<long long>(2) * kTreeMaxCtas * p.slot_rows * HD;
+  p.status = a.status;
+  p.wait_limit_ns = a.wait_limit_ns;
+  if (a.slopes)
+    return a.softcap > 0.f ? launch_mode<HD, kF16, kModCapSlopes>(grid, a.stream, q, k, v, p)
+                           : launch_mode<HD, kF16, kModSlopes>(grid, a.stream, q, k, v, p);
+  return a.softcap > 0.f ? launch_mode<HD, kF16, kModCap>(grid, a.stream, q, k, v, p)
+                         : launch_mode<HD, kF16, kModPlain>(grid, a.stream, q, k, v, p);
+}
+
+}  // namespace tree
+}  // namespace osattn

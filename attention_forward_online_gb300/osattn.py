@@ -39,7 +39,7 @@ EXPORTS = ("osattn_fwd", "osattn_fwd_strided", "osattn_fwd_splitkv",
            "osattn_version", "osattn_set_wait_limit_ns", "osattn_test_wait_timeout",
            "osattn_last_timeout_site", "osattn_step_trace_read",
            "osattn_mask_plan", "osattn_mask_plan_bytes", "osattn_fwd_mod", "osattn_bwd_mod",
-           "osattn_bwd_mod_workspace_bytes")
+           "osattn_bwd_mod_workspace_bytes", "osattn_tree_attn", "osattn_tree_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
@@ -135,6 +135,11 @@ def lib():
             L.osattn_bwd_mod.argtypes = ([vp] * 10 + [i32] * 6 + [i64p] * 8 +
                                          [ctypes.c_float, scp, vp, i32, vp, sz, vp])
             L.osattn_bwd_mod.restype = i32
+            L.osattn_tree_workspace_bytes.argtypes = [i32] * 5
+            L.osattn_tree_workspace_bytes.restype = sz
+            L.osattn_tree_attn.argtypes = ([vp] * 8 + [i32] * 8 + [i64p] * 4 +
+                                           [ctypes.c_float, ctypes.c_float, vp, i32, i32, vp, sz, vp])
+            L.osattn_tree_attn.restype = i32
             _lib = L
         return _lib
 
@@ -843,6 +848,88 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
     if st != OK:
         raise OsattnError(st, "osattn_bwd_mod")
     return (dq, dk, dv) if drel is None else (dq, dk, dv, drel)
+
+
+# ---------------------------------------------------------------- paged cache
+def tree_workspace_bytes(B: int, H: int, Hkv: int, T: int, d: int) -> int:
+    return int(lib().osattn_tree_workspace_bytes(int(B), int(H), int(Hkv), int(T), int(d)))
+
+
+def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: float | None = None,
+              softcap: float = 0.0, slopes=None, window: int = 0, out=None, lse=None,
+              workspace=None, stream=None):
+    """O, LSE of T drafted tokens of every sequence (T = 1: a decode step) over
+    its paged cache: q [B,H,T,d], k_pages/v_pages [pages,Hkv,page_size,d], bf16
+    or fp16, any views whose last axis is contiguous; page_table int32
+    [B,max_pages]; ctx_len int32 [B], the cached keys before the drafts, whose
+    own keys follow them in the pages; tree_mask int64 [B,T], bit u of entry t
+    set iff draft t sees draft u (None: u <= t; 0: padding, O = 0, LSE = -inf).
+
+    softcap and slopes (fp32 [H]) as in fwd_mod(), with a window keys at a
+    distance of at least `window` are hidden; a draft stands behind the
+    context by the number of other drafts it sees."""
+    import torch
+
+    if q.dim() != 4 or k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("q must be [B, H, T, d], k_pages and v_pages [pages, Hkv, page_size, d]")
+    B, H, T, d = q.shape
+    pages, Hkv, page_size, dk = k_pages.shape
+    device = q.device
+    if dk != d or Hkv < 1 or H % Hkv:
+        raise ValueError("k_pages must have q's d and a number of heads that divides q's")
+    if k_pages.dtype != q.dtype or v_pages.dtype != q.dtype:
+        raise TypeError("q, k_pages, v_pages must share one dtype")
+    dtype = _dtype_code(q)
+    if not q.is_cuda or k_pages.device != device or v_pages.device != device:
+        raise ValueError("q, k_pages, v_pages must be CUDA tensors on one device")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    max_pages = page_table.shape[1]
+    page_table = _int32(page_table, (B, max_pages), device, "page_table")
+    ctx_len = _int32(ctx_len, (B,), device, "ctx_len")
+    if tree_mask is not None:
+        if (tree_mask.dtype != torch.int64 or tuple(tree_mask.shape) != (B, T)
+                or tree_mask.device != device):
+            raise ValueError("tree_mask must be int64 [B, T] on q's device")
+        tree_mask = tree_mask.contiguous()
+    if slopes is not None:
+        if tuple(slopes.shape) != (H,) or slopes.dtype != torch.float32 or slopes.device != device:
+            raise ValueError("slopes must be an fp32 tensor of shape [H] on q's device")
+        slopes = slopes.contiguous()
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _on(device):
+        stream = _stream_for(stream, device)
+        made = []
+        if out is None:
+            out = torch.empty_like(q)
+            made.append(out)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.device != device:
+            raise ValueError("out must match q")
+        if lse is None:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
+            made.append(lse)
+        elif (tuple(lse.shape) != (B, H, T) or lse.dtype != torch.float32
+              or not lse.is_contiguous() or lse.device != device):
+            raise ValueError("lse must be contiguous fp32 [B, H, T] on q's device")
+        if workspace is None:
+            workspace = torch.empty(max(tree_workspace_bytes(B, H, Hkv, T, d), 16),
+                                    dtype=torch.uint8, device=device)
+            made.append(workspace)
+        elif not workspace.is_contiguous() or workspace.device != device:
+            raise ValueError("workspace must be contiguous on q's device")
+        st = lib().osattn_tree_attn(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+            ctx_len.data_ptr(), None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(),
+            lse.data_ptr(), B, H, Hkv, T, d, pages, page_size, max_pages, _view_strides(q, "q"),
+            _view_strides(k_pages, "k_pages"), _view_strides(v_pages, "v_pages"),
+            _view_strides(out, "out"), float(scale), float(softcap),
+            None if slopes is None else slopes.data_ptr(), int(window), dtype, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), stream.cuda_stream)
+        _keep(stream, device, *made, page_table, ctx_len, tree_mask, slopes)
+    if st != OK:
+        raise OsattnError(st, "osattn_tree_attn")
+    return out, lse
 
 
 def get_device_status(stream=None) -> int:

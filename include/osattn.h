@@ -24,6 +24,8 @@
  *                  or a learned bias by distance bucket; shared key/value
  *                  heads), with the masks of osattn_mask_plan (causal, window,
  *                  prefix, packed documents, key lengths)
+ *   paged cache    osattn_tree_attn (one token or a tree of drafted tokens of
+ *                  every sequence over its pages)
  *   helpers        workspace sizes, status strings, the device status word,
  *                  the version, and test hooks for the bounded waits
  *
@@ -552,6 +554,60 @@ int osattn_bwd_mod(const void* Q, const void* K, const void* V, const void* O, c
                    const int64_t* dk_strides, const int64_t* dv_strides, float scale,
                    const osattn_score* score, const void* plan, int dtype, void* workspace,
                    size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------- paged cache */
+
+/*
+ * osattn_tree_attn - T drafted tokens of every sequence attend to the
+ * sequence's paged cache and to the drafts on their own line; T = 1 is the
+ * ordinary decode step.
+ *
+ * Sequence b has ctx_len[b] cached keys; the drafts' own keys and values
+ * follow them in the same pages, at positions ctx_len[b] .. + T - 1 (the
+ * caller has written them).  The key at position x is row x mod page_size of
+ * page page_table[b][x / page_size].  Bit u of tree_mask[b][t] says that
+ * draft t sees draft u (for a tree: its ancestors and itself; bits from T on
+ * say nothing); tree_mask NULL is the chain u <= t.  A draft whose mask is 0
+ * is padding: it sees nothing and gets O = 0, LSE = -inf.  Otherwise it sees
+ * the whole context besides.
+ *
+ * Positions, for the window and the slopes: a cached key stands at its index,
+ * draft t at ctx_len[b] + (bits of its mask) - 1.  With y the scaled score,
+ * capped as in osattn_score, and dist = |position of the query less that of
+ * the key|:
+ *   y = y - slopes[h] * dist;  key visible only if dist < window (window > 0)
+ * O and LSE as for osattn_fwd_mod, head h reading key head h / (H / Hkv).
+ *
+ *   Q, O       device [B, H, T, d] with element strides as for
+ *              osattn_fwd_strided (NULL: contiguous)
+ *   K_pages, V_pages   device [num_pages, Hkv, page_size, d], strides of the
+ *              page, head and row axes likewise
+ *   page_table device int32 [B, max_pages]; only the entries of pages that
+ *              hold a visible key are used.  Such an entry outside
+ *              [0, num_pages) reads as zeros, and osattn_get_device_status
+ *              then returns OSATTN_ERR_INVALID_ARG
+ *   ctx_len    device int32 [B], 0 .. max_pages * page_size - T (values
+ *              outside are clamped, with the same status)
+ *   tree_mask  device int64 [B, T] or NULL
+ *   LSE        device fp32 [B, H, T] contiguous
+ *   T          1 .. 64, H / Hkv <= 128, d 64 or 128, bf16 or fp16 (else
+ *              OSATTN_ERR_UNSUPPORTED); max_pages * page_size in T .. 2^30
+ *   page_size  a divisor of 128 from 8 on, or a multiple of 128 (else
+ *              OSATTN_ERR_UNSUPPORTED)
+ *   workspace  device, 16-byte aligned, osattn_tree_workspace_bytes(...)
+ *              bytes; holds nothing between calls
+ * Pages may hold anything (NaN included) at positions that no draft sees.
+ * No atomics on results: the same call gives the same bits.  Alignment,
+ * ownership, asynchrony and errors as for osattn_fwd_strided.
+ */
+size_t osattn_tree_workspace_bytes(int B, int H, int Hkv, int T, int d);
+int osattn_tree_attn(const void* Q, const void* K_pages, const void* V_pages,
+                     const int32_t* page_table, const int32_t* ctx_len, const int64_t* tree_mask,
+                     void* O, float* LSE, int B, int H, int Hkv, int T, int d, int num_pages,
+                     int page_size, int max_pages, const int64_t* q_strides,
+                     const int64_t* k_strides, const int64_t* v_strides, const int64_t* o_strides,
+                     float scale, float softcap, const float* slopes, int window, int dtype,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

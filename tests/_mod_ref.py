@@ -173,3 +173,49 @@ def check(got, want, bound, name):
     bad = err > lim
     assert not bad.any(), (f"{name}: {int(bad.sum())} of {err.numel()} over the bound, worst "
                            f"{float((err / lim.clamp(min=1e-30)).max()):.3g} times it")
+
+
+def tree_reference(q, k_pages, v_pages, table, ctx, mask, scale, cap=0.0, slopes=None, window=0):
+    """O, LSE of osattn_tree_attn with the bounds above: q [B, H, T, d], mask a
+    list of T bit masks a sequence."""
+    B, H, T, d = q.shape
+    Hkv, page = k_pages.shape[1], k_pages.shape[2]
+    u, tiny = U[q.dtype], TINY[q.dtype]
+    o = torch.zeros(B, H, T, d, dtype=F64, device=q.device)
+    lse = torch.full((B, H, T), -math.inf, dtype=F64, device=q.device)
+    eo, el = torch.zeros_like(o), torch.zeros_like(lse)
+    for b in range(B):
+        n = ctx[b]
+        pos = [n + max(bin(m).count("1") - 1, 0) for m in mask[b]]
+        kpos = torch.tensor(list(range(n)) + pos)
+        gap = (torch.tensor(pos)[:, None] - kpos[None]).abs()
+        see = torch.zeros(T, n + T, dtype=torch.bool)
+        for t, m in enumerate(mask[b]):
+            see[t, :n] = m != 0
+            for x in range(T):
+                see[t, n + x] = bool((m >> x) & 1)
+        if window:
+            see &= gap < window
+        gap, see = gap.to(q.device), see.to(q.device)
+        keys = torch.arange(n + T, device=q.device)
+        ids = table[b].long()[keys // page].clamp(0, k_pages.shape[0] - 1)
+        used = see.any(0)
+        k, v = (torch.where(used[:, None, None], x[ids, :, keys % page].to(F64), torch.zeros((), dtype=F64,
+                                                                                             device=q.device))
+                .transpose(0, 1).repeat_interleave(H // Hkv, 0) for x in (k_pages, v_pages))
+        qq = q[b].to(F64)
+        y = scale * (qq @ k.transpose(-1, -2))
+        if cap:
+            y = cap * torch.tanh(y / cap)
+        fall = torch.zeros(H, 1, 1, dtype=F64, device=q.device) if slopes is None else slopes.to(F64)[:, None, None]
+        y = y - fall * gap
+        o[b], lse[b], p = softmax_out(y, see[None], v)
+        s_abs = abs(scale) * (qq.abs() @ k.abs().transpose(-1, -2))
+        big = y.abs() + cap + fall * gap + s_abs
+        delta = torch.where(see[None], d * 2.0 ** -24 * s_abs + 8 * 2.0 ** -24 * big, torch.zeros_like(y))
+        delta = delta.amax(-1, keepdim=True)
+        rel = 2 * delta + 2.0 ** -21
+        eo[b] = ((u + rel) * (p @ v.abs()) + 2 * tiny * (n + T) * (float(v.abs().max()) + 1) + 2.0 ** -40
+                 + u * o[b].abs() + tiny)
+        el[b] = delta.squeeze(-1) + 2.0 ** -20 + 2.0 ** -22 * lse[b].abs().nan_to_num(posinf=0)
+    return {"o": (o, eo), "lse": (lse, el)}
