@@ -36,6 +36,7 @@
 #include "mod_common.cuh"
 #include "mod_internal.h"
 #include "sm100_ptx.cuh"
+#include "softmax_tile.cuh"
 #include "tc_attn_mma.cuh"
 
 namespace osattn {
@@ -69,7 +70,9 @@ struct Cfg {
   static constexpr int kStages = HD == 128 ? (mode_rel(MODE) ? 4 : 5) : (mode_rel(MODE) ? 10 : 12);
   static constexpr int kIters = HD == 128 ? 4 : 8;  // > kStages / 2 + 1
   static constexpr int kTileRegion = kQTiles * kQBytes + kStages * kTileBytes;
-  static constexpr int kRelBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16 : 0;
+  // shared-memory table: learned biases by distance, or slope * e of a tile
+  static constexpr int kRelBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16
+                                                  : (mode_slopes(MODE) ? BN * 4 : 0);
   static constexpr uint32_t kOCol0 = 256;
 };
 
@@ -138,18 +141,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
   }
 }
 
-__device__ __forceinline__ float max128(const uint32_t* v) {
-  float a[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 8]));
-#pragma unroll
-  for (int j = 16; j < BN; j += 16)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      a[i] = fmax3(a[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 8 + i]));
-  return fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
-}
-
 // ------------------------------------------------------------------ softmax
 template <int HD, bool kF16, int MODE>
 __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, const float* bias,
@@ -164,8 +155,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, const 
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t s_addr = lane_base + static_cast<uint32_t>(t * BN);
   const float c = p.scale_log2;
+  const int pos = qi + p.q_offset;
   float slope2 = 0.f;
-  if constexpr (mode_slopes(MODE)) slope2 = p.slopes[h] * kModLog2e;
+  bool left = false;  // no row of the warp sees a key behind its own position
+  if constexpr (mode_slopes(MODE)) {
+    slope2 = p.slopes[h] * kModLog2e;
+    left = __all_sync(0xffffffffu, see.y <= pos + 1 || see.x >= see.y);
+  }
   float m = -INFINITY, l = 0.f;
   bool ok = true;
 
@@ -174,78 +170,104 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, const 
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     tc_fence_after_sync();
+    const int k0 = (kt0 + rg.a + j) * BN;
+    const bool masked = !(tile.z <= k0 && tile.w >= k0 + BN);
     uint32_t v[BN];
+    float ext[BN / 32];  // max of each chunk's raw scores, formed by the loads
 #pragma unroll
-    for (int ch = 0; ch < BN / 32; ++ch) tmem_ld_32x32b_x32(s_addr + ch * 32, v + ch * 32);
+    for (int ch = 0; ch < BN / 32; ++ch)
+      tmem_ld_red_32x32b_x32<true>(s_addr + ch * 32, v + ch * 32, ext[ch]);
     tmem_ld_wait();
 #pragma unroll
-    for (int ch = 0; ch < BN / 32; ++ch) reg_fence32(v + ch * 32);
-
-    const int k0 = (kt0 + rg.a + j) * BN;
-    const int d0 = k0 - (qi + p.q_offset);  // distance of the tile's first key
-    // x in base-2 units
+    for (int ch = 0; ch < BN / 32; ++ch) {
+      reg_fence32(v + ch * 32);
+      asm volatile("" : "+f"(ext[ch]));
+    }
+    float raw = fmaxf(fmaxf(ext[0], ext[1]), fmaxf(ext[2], ext[3]));
+    uint32_t bits[4];  // the row's visible keys, if the tile has others
+    if (masked) {
+      const int lo = see.x - k0, hi = see.y - k0;
 #pragma unroll
-    for (int e = 0; e < BN; ++e) {
-      const float s = __uint_as_float(v[e]);
-      float x;
-      if constexpr (mode_cap(MODE))
-        x = fmaf(cap_r(s, p.cap_c1), -2.f * p.cap2, p.cap2);
-      else
-        x = s * c;
-      if constexpr (mode_slopes(MODE)) x = fmaf(-slope2, fabsf(static_cast<float>(d0 + e)), x);
-      v[e] = __float_as_uint(x);
+      for (int x = 0; x < 4; ++x) bits[x] = bit_range(lo - 32 * x, hi - 32 * x);
+    }
+
+    // x = v * cm + off in base-2 units.  `known`: raw gives the max of v * cm
+    // (the scale is not negative and nothing but the scale or the cap, both
+    // monotonic, has touched the scores).
+    float cm = c, off = 0.f;
+    bool known = c >= 0.f && !masked;
+    float mx = raw * c;
+    if constexpr (mode_cap(MODE)) {
+      if (masked) {  // four scores share a reciprocal: a masked one may hold anything
+        mask_tile<0u>(v, bits);
+        raw = max_tile(v);
+      }
+      cap_tile(v, p.cap_c1, p.cap2,
+               __all_sync(0xffffffffu, p.cap_c1 >= 0.f && raw * p.cap_c1 <= kCapFast));
+      cm = 1.f;
+      mx = fmaf(cap_r(raw, p.cap_c1), -2.f * p.cap2, p.cap2);
+    }
+    if constexpr (mode_slopes(MODE)) {
+      // - slope2 |d0 + e|, d0 the distance of the tile's first key: on one
+      // side of the row's position a multiple of e (or of 127 - e) from the
+      // table plus a constant, which joins the max; both sides: term by term
+      const int d0 = k0 - pos;
+      known = false;
+      if (left || __all_sync(0xffffffffu, d0 + BN - 1 <= 0)) {
+        off = slope2 * static_cast<float>(d0);
+        const uint64_t c2 = f2_pack(cm, cm);
+#pragma unroll
+        for (int e = 0; e < BN; e += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(bias + e);
+          set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(s4.x, s4.y)));
+          set_pair(v, e + 2, f2_fma(pair_of(v, e + 2), c2, f2_pack(s4.z, s4.w)));
+        }
+      } else if (__all_sync(0xffffffffu, d0 >= 0)) {
+        off = -slope2 * static_cast<float>(d0 + BN - 1);
+        const uint64_t c2 = f2_pack(cm, cm);
+#pragma unroll
+        for (int e = 0; e < BN; e += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(bias + (BN - 4 - e));
+          set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(s4.w, s4.z)));
+          set_pair(v, e + 2, f2_fma(pair_of(v, e + 2), c2, f2_pack(s4.y, s4.x)));
+        }
+      } else {
+        const float f0 = static_cast<float>(d0);
+#pragma unroll
+        for (int e = 0; e < BN; ++e)
+          v[e] = __float_as_uint(fmaf(-slope2, fabsf(f0 + static_cast<float>(e)), __uint_as_float(v[e]) * cm));
+      }
+      cm = 1.f;
     }
     if constexpr (mode_rel(MODE)) {
       const int R = p.rel.range;
       const int first = k0 - (q0 + p.q_offset);  // distances of the whole tile: first - 127 .. first + 127
       if (first + BN - 1 <= -R || first - (BM - 1) >= R) {
-        const float far = bias[first <= 0 ? 0 : rel_entries(R) - 1];
-#pragma unroll
-        for (int e = 0; e < BN; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + far);
+        off = bias[first <= 0 ? 0 : rel_entries(R) - 1];
       } else {
-        const float* at = bias + (d0 + R + kRelPad);
+        const float* at = bias + (k0 - pos + R + kRelPad);
+        const uint64_t c2 = f2_pack(c, c);
 #pragma unroll
-        for (int e = 0; e < BN; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + at[e]);
+        for (int e = 0; e < BN; e += 2)
+          set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(at[e], at[e + 1])));
+        cm = 1.f;
+        known = false;
       }
     }
-    if (!(tile.z <= k0 && tile.w >= k0 + BN)) {
-      const int lo = see.x - k0, hi = see.y - k0;
-#pragma unroll
-      for (int e = 0; e < BN; ++e)
-        if (e < lo || e >= hi) v[e] = __float_as_uint(-INFINITY);
+    if (!known) {
+      if (cm != 1.f) scale_tile(v, cm);
+      cm = 1.f;
+      if (masked) mask_tile(v, bits);
+      mx = max_tile(v);
     }
-    const float m_new = fmaxf(m, max128(v));
+    const float m_new = next_max(m, mx + off);
     const float alpha = (m_new == m) ? 1.f : ex2_approx(m - m_new);
     bars->alpha[t][row] = alpha;
     mbar_arrive(&bars->alpha_full[t]);
-
-    // A row with no key so far has m_new = -inf and every x = -inf: with
-    // neg_m = 0 each p is exactly 0.
-    const float neg_m = (m_new == -INFINITY) ? 0.f : -m_new;
-    const uint64_t nm2 = f2_pack(neg_m, neg_m);
-    uint64_t rs_a = 0, rs_b = 0;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t pk[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int i = half * 64 + 2 * e;
-        float x0, x1;
-        f2_unpack(f2_add(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), nm2), x0, x1);
-        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        const uint64_t pp = f2_pack(p0, p1);
-        if (e & 1)
-          rs_b = f2_add(rs_b, pp);
-        else
-          rs_a = f2_add(rs_a, pp);
-        pk[e] = pack2<kF16>(p0, p1);
-      }
-      tmem_st_32x32b_x32(s_addr + half * 32, pk);
-    }
-    float r0, r1, r2, r3;
-    f2_unpack(rs_a, r0, r1);
-    f2_unpack(rs_b, r2, r3);
-    l = fmaf(l, alpha, (r0 + r1) + (r2 + r3));
+    // A row with no key so far has m_new = -inf and every x = -inf: with the
+    // offset 0 each p is exactly 0.
+    const float neg = (m_new == -INFINITY) ? 0.f : off - m_new;
+    l = fmaf(l, alpha, exp_tile<kF16>(v, cm, neg, s_addr));
     m = m_new;
     tmem_st_wait();
     tc_fence_before_sync();
@@ -310,23 +332,20 @@ __device__ __forceinline__ void correction_tile(Bars* bars, uint32_t lane_base, 
     const uint64_t a2 = f2_pack(alpha, alpha);
     const uint32_t o_addr = lane_base + C::kOCol0 + static_cast<uint32_t>(t * HD);
 #pragma unroll
-    for (int ch = 0; ch < HD / 32; ch += 2) {
-      uint32_t orr[64];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) tmem_ld_32x32b_x32(o_addr + (ch + k) * 32, orr + k * 32);
+    for (int ch = 0; ch < HD / 32; ++ch) {
+      uint32_t orr[32];
+      tmem_ld_32x32b_x32(o_addr + ch * 32, orr);
       tmem_ld_wait();
+      reg_fence32(orr);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) reg_fence32(orr + k * 32);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
+      for (int e = 0; e < 16; ++e) {
         float a0, a1;
         f2_unpack(f2_mul(f2_pack(__uint_as_float(orr[2 * e]), __uint_as_float(orr[2 * e + 1])), a2),
                   a0, a1);
         orr[2 * e] = __float_as_uint(a0);
         orr[2 * e + 1] = __float_as_uint(a1);
       }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) tmem_st_32x32b_x32(o_addr + (ch + k) * 32, orr + k * 32);
+      tmem_st_32x32b_x32(o_addr + ch * 32, orr);
     }
     tmem_st_wait();
   }
@@ -546,6 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if constexpr (mode_rel(MODE)) rel_fill<kF16>(bias, p.rel, p.H, h);
+  if constexpr (mode_slopes(MODE)) {
+    if (threadIdx.x < BN) bias[threadIdx.x] = p.slopes[h] * kModLog2e * static_cast<float>(threadIdx.x);
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
