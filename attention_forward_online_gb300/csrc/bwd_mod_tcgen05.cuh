@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // Query tiles [it_lo, it_hi) hold every row that sees one of these keys.
   for (int q = threadIdx.x; q < p.q_tiles; q += kThreads) {
-    const int4 pt = plan_tile(p.plan, b, p.q_tiles, q, p.Nkv);
-    if (pt.x < k0 + kT && pt.y > k0) {
+    const PlanTile pt = plan_tile(p.plan, b, p.q_tiles, q, p.Nkv);
+    if (pt.lo < k0 + kT && pt.hi > k0) {
       atomicMin(&bars->it_lo, q);
       atomicMax(&bars->it_hi, q + 1);
     }
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         h_of = h;
       }
-      const int4 pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
+      const PlanTile pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
       ok = mbar_wait(&bars->s_full[0], static_cast<uint32_t>(it) & 1u, wc, kSiteElem);
       if (ok) ok = mbar_wait(&bars->full[s], static_cast<uint32_t>(it / C::kStages) & 1u, wc, kSiteElem);
       ok = __all_sync(0xffffffffu, ok);
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float pr[64];
       // Every key of the tile visible to every query: no per-entry mask.
       // (Uniform over the CTA.)
-      const bool full = pt.z <= k0 && pt.w >= k0 + kT;
+      const bool full = pt.lo_max <= k0 && pt.hi_min >= k0 + kT;
       auto part = [&](auto mask) {
         constexpr bool kMask = decltype(mask)::value;
         if constexpr (mode_rel(MODE)) {
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         part(std::false_type{});
       } else {
         part(std::true_type{});
-        if (pt.w == 0) {
+        if (pt.hi_min == 0) {
           // Queries of this tile that see nothing: their rows of Q and dO
           // must not reach the sums (0 * NaN is NaN).  dP^T, the last other
           // reader of dO, is awaited first.
@@ -690,9 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int qt = p.num_tiles - 1 - rank;
   const int b = bh / p.H, h = bh % p.H, hk = h / p.group;
   const int q0 = qt * kT;
-  const int4 pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
-  const int kt0 = pt.x / kT;
-  const int n_kt = pt.x < pt.y ? (pt.y + kT - 1) / kT - kt0 : 0;
+  const PlanTile pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
+  const int kt0 = pt.lo / kT;
+  const int n_kt = pt.lo < pt.hi ? (pt.hi + kT - 1) / kT - kt0 : 0;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->fixed_full, 1);
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         far = side < 0 ? bias[0] : bias[rel_entries(p.rel.range) - 1];
         bt = bias + (d0 + p.rel.range + kRelPad);
       }
-      const bool full = pt.z <= kx && pt.w >= kx + kT;
+      const bool full = pt.lo_max <= kx && pt.hi_min >= kx + kT;
       const uint32_t s_addr = lane_base + 128 * (j & 1);
       float pr[64];
       auto part = [&](auto mask) {
@@ -872,10 +872,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         part(std::false_type{});
       else
         part(std::true_type{});
-      if (kx < pt.x || min(kx + kT, p.Nkv) > pt.y) {
+      if (kx < pt.lo || min(kx + kT, p.Nkv) > pt.hi) {
         // keys of this tile that no row sees: zero their rows of K_j, which
         // dQ += dS_j K_j reads after ds_full (S_j, the other reader, is done)
-        if (kx + row < pt.x || kx + row >= pt.y) {
+        if (kx + row < pt.lo || kx + row >= pt.hi) {
           uint8_t* ks = kring + (j % C::kKSlots) * C::kTileBytes;
           if (HD == 128) zero_row(ks, g, row);
           else if (g == 0) zero_row(ks, 0, row);

@@ -6,6 +6,6 @@ namespace osattn {
 namespace fwdmod {
 template cudaError_t prepare<64, false>();
 template cudaError_t launch<64, false>(const ModArgs&, const CUtensorMap&, const CUtensorMap&,
-                                    const CUtensorMap&);
+                                    const CUtensorMap&, const CUtensorMap&);
 }  // namespace fwdmod
 }  // namespace osattn

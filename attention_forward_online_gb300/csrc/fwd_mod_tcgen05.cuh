@@ -23,6 +23,8 @@
 // set to zero in shared memory by the correction warps before the product
 // (0 * NaN is NaN: what lies behind a sequence's last key must not reach O).
 //
+// O leaves through the query tile's place in shared memory and TMA stores.
+//
 // What bounds it: the elementwise work on the scores.  Per key tile of 128 x
 // 128 scores and two products of 256 cycles at d = 128, the exponentials
 // alone take 512 cycles of the multifunction unit, a cap twice as many again
@@ -58,21 +60,22 @@ enum : uint32_t {
   kSiteS = 45,
   kSiteAlpha = 46,
   kSiteO = 48,
-  kSiteZero = 49
+  kSiteZero = 49,
+  kSiteStage = 50
 };
 
 template <int HD, int MODE>
 struct Cfg {
   static constexpr int kTileBytes = BN * HD * 2;
   static constexpr int kQBytes = BM * HD * 2;
-  // The learned-bias table takes one stage's place at d = 128 (rel_entries of
-  // kMaxRelRange, 10 KB) and two at d = 64, where a stage is 16 KB.
-  static constexpr int kStages = HD == 128 ? (mode_rel(MODE) ? 4 : 5) : (mode_rel(MODE) ? 10 : 12);
+  // The learned-bias table (10 KB) or the slope operands (12 KB) take the
+  // place of one stage (32 KB at d = 128, 16 KB at d = 64).
+  static constexpr bool kTable = mode_rel(MODE) || MODE == kModSlopes;
+  static constexpr int kStages = HD == 128 ? (kTable ? 4 : 5) : (kTable ? 11 : 12);
   static constexpr int kIters = HD == 128 ? 4 : 8;  // > kStages / 2 + 1
   static constexpr int kTileRegion = kQTiles * kQBytes + kStages * kTileBytes;
-  // shared-memory table: learned biases by distance, or slope * e of a tile
-  static constexpr int kRelBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16
-                                                  : (mode_slopes(MODE) ? BN * 4 : 0);
+  static constexpr int kTableBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16
+                                                    : (MODE == kModSlopes ? kSlopeBytes : 0);
   static constexpr uint32_t kOCol0 = 256;
 };
 
@@ -84,6 +87,7 @@ struct __align__(16) Bars {
   uint64_t alpha_full[kQTiles];  // 128 arrivals
   uint64_t p_full[kQTiles];      // softmax and correction, 256 arrivals
   uint64_t o_full[kQTiles];
+  uint64_t staged[kQTiles];      // O_t is in shared memory, 128 arrivals
   uint64_t mma_drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -92,20 +96,17 @@ struct __align__(16) Bars {
 
 template <int HD, int MODE>
 constexpr int smem_bytes() {
-  return Cfg<HD, MODE>::kTileRegion + Cfg<HD, MODE>::kRelBytes + static_cast<int>(sizeof(Bars)) + 1024;
+  return Cfg<HD, MODE>::kTileRegion + Cfg<HD, MODE>::kTableBytes + static_cast<int>(sizeof(Bars));
 }
 
 struct Params {
-  uint16_t* O;
-  long long o_sb, o_sh, o_sn;
   float* LSE;
   PlanView plan;
   int H, group, Nq, Nkv, BH;  // group: query heads per key/value head
   int num_q_blocks, n_tiles;  // 256-row units and 128-row tiles per (b, h)
   int group_heads;
-  float scale_log2;  // scale * log2(e)
-  float cap_c1;      // 2 scale log2(e) / cap
-  float cap2;        // cap * log2(e)
+  float scale, scale_log2;  // scale, scale * log2(e)
+  CapArgs cap;
   const float* slopes;
   RelArgs rel;
   int q_offset;
@@ -143,9 +144,10 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
 
 // ------------------------------------------------------------------ softmax
 template <int HD, bool kF16, int MODE>
-__device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, const float* bias,
-                                             uint32_t tmem, int t, int b, int h, int q0, Range rg,
-                                             int4 tile, int kt0, WaitCtl wc) {
+__device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Params& p, Bars* bars,
+                                             const float* bias, uint8_t* sQt, uint32_t tmem, int t, int b,
+                                             int h, int q0, Range rg, const PlanTile& tile, int kt0,
+                                             WaitCtl wc) {
   using C = Cfg<HD, MODE>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;
@@ -155,12 +157,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, const 
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t s_addr = lane_base + static_cast<uint32_t>(t * BN);
   const float c = p.scale_log2;
-  const int pos = qi + p.q_offset;
+  [[maybe_unused]] const int p0 = q0 + p.q_offset, pos = p0 + row;
   float slope2 = 0.f;
-  bool left = false;  // no row of the warp sees a key behind its own position
+  bool linear = false;
   if constexpr (mode_slopes(MODE)) {
     slope2 = p.slopes[h] * kModLog2e;
-    left = __all_sync(0xffffffffu, see.y <= pos + 1 || see.x >= see.y);
+    linear = MODE == kModSlopes && slope_linear(p.slopes[h], p.scale);
   }
   float m = -INFINITY, l = 0.f;
   bool ok = true;
@@ -171,103 +173,67 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, const 
     if (!ok) break;
     tc_fence_after_sync();
     const int k0 = (kt0 + rg.a + j) * BN;
-    const bool masked = !(tile.z <= k0 && tile.w >= k0 + BN);
-    uint32_t v[BN];
-    float ext[BN / 32];  // max of each chunk's raw scores, formed by the loads
-#pragma unroll
-    for (int ch = 0; ch < BN / 32; ++ch)
-      tmem_ld_red_32x32b_x32<true>(s_addr + ch * 32, v + ch * 32, ext[ch]);
-    tmem_ld_wait();
-#pragma unroll
-    for (int ch = 0; ch < BN / 32; ++ch) {
-      reg_fence32(v + ch * 32);
-      asm volatile("" : "+f"(ext[ch]));
-    }
-    float raw = fmaxf(fmaxf(ext[0], ext[1]), fmaxf(ext[2], ext[3]));
-    uint32_t bits[4];  // the row's visible keys, if the tile has others
+    const bool masked = !(tile.lo_max <= k0 && tile.hi_min >= k0 + BN);
+    Row v;
+    float ext[kChunks];
+    load_row(s_addr, v, ext);
+    TileMask mk;
+    mk.none = 0u;
     if (masked) {
       const int lo = see.x - k0, hi = see.y - k0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) bits[x] = bit_range(lo - 32 * x, hi - 32 * x);
+      for (int ch = 0; ch < kChunks; ++ch) mk.bits[ch] = bit_range(lo - 32 * ch, hi - 32 * ch);
+      classify(mk);
     }
-
-    // x = v * cm + off in base-2 units.  `known`: raw gives the max of v * cm
-    // (the scale is not negative and nothing but the scale or the cap, both
-    // monotonic, has touched the scores).
+    // x = v * cm + off in base-2 units; ext: the max of each chunk of v
     float cm = c, off = 0.f;
-    bool known = c >= 0.f && !masked;
-    float mx = raw * c;
     if constexpr (mode_cap(MODE)) {
-      if (masked) {  // four scores share a reciprocal: a masked one may hold anything
-        mask_tile<0u>(v, bits);
-        raw = max_tile(v);
-      }
-      cap_tile(v, p.cap_c1, p.cap2,
-               __all_sync(0xffffffffu, p.cap_c1 >= 0.f && raw * p.cap_c1 <= kCapFast));
+      cap_row(v, ext, p.cap, masked, mk);
       cm = 1.f;
-      mx = fmaf(cap_r(raw, p.cap_c1), -2.f * p.cap2, p.cap2);
+    } else if (!(c > 0.f)) {
+      scale_row(v, ext, c);
+      cm = 1.f;
     }
     if constexpr (mode_slopes(MODE)) {
-      // - slope2 |d0 + e|, d0 the distance of the tile's first key: on one
-      // side of the row's position a multiple of e (or of 127 - e) from the
-      // table plus a constant, which joins the max; both sides: term by term
-      const int d0 = k0 - pos;
-      known = false;
-      if (left || __all_sync(0xffffffffu, d0 + BN - 1 <= 0)) {
-        off = slope2 * static_cast<float>(d0);
-        const uint64_t c2 = f2_pack(cm, cm);
-#pragma unroll
-        for (int e = 0; e < BN; e += 4) {
-          const float4 s4 = *reinterpret_cast<const float4*>(bias + e);
-          set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(s4.x, s4.y)));
-          set_pair(v, e + 2, f2_fma(pair_of(v, e + 2), c2, f2_pack(s4.z, s4.w)));
-        }
-      } else if (__all_sync(0xffffffffu, d0 >= 0)) {
-        off = -slope2 * static_cast<float>(d0 + BN - 1);
-        const uint64_t c2 = f2_pack(cm, cm);
-#pragma unroll
-        for (int e = 0; e < BN; e += 4) {
-          const float4 s4 = *reinterpret_cast<const float4*>(bias + (BN - 4 - e));
-          set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(s4.w, s4.z)));
-          set_pair(v, e + 2, f2_fma(pair_of(v, e + 2), c2, f2_pack(s4.y, s4.x)));
-        }
+      const int d0 = k0 - pos;  // distance of the tile's first key
+      const int side = linear ? slope_side(k0, p0, tile.left) : 0;
+      if (side != 0) {
+        off = (side > 0 ? slope2 : -slope2) * static_cast<float>(d0);
       } else {
         const float f0 = static_cast<float>(d0);
 #pragma unroll
         for (int e = 0; e < BN; ++e)
           v[e] = __float_as_uint(fmaf(-slope2, fabsf(f0 + static_cast<float>(e)), __uint_as_float(v[e]) * cm));
+        cm = 1.f;
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) ext[ch] = chunk_max(v, ch);
       }
-      cm = 1.f;
     }
     if constexpr (mode_rel(MODE)) {
       const int R = p.rel.range;
-      const int first = k0 - (q0 + p.q_offset);  // distances of the whole tile: first - 127 .. first + 127
+      const int first = k0 - p0;  // distances of the whole tile: first - 127 .. first + 127
       if (first + BN - 1 <= -R || first - (BM - 1) >= R) {
         off = bias[first <= 0 ? 0 : rel_entries(R) - 1];
       } else {
         const float* at = bias + (k0 - pos + R + kRelPad);
-        const uint64_t c2 = f2_pack(c, c);
+        const uint64_t c2 = f2_pack(cm, cm);
 #pragma unroll
         for (int e = 0; e < BN; e += 2)
           set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(at[e], at[e + 1])));
         cm = 1.f;
-        known = false;
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) ext[ch] = chunk_max(v, ch);
       }
     }
-    if (!known) {
-      if (cm != 1.f) scale_tile(v, cm);
-      cm = 1.f;
-      if (masked) mask_tile(v, bits);
-      mx = max_tile(v);
-    }
-    const float m_new = next_max(m, mx + off);
+    if (masked) apply_mask(v, ext, mk);
+    const float m_new = next_max(m, fmaf(max4(ext), cm, off));
     const float alpha = (m_new == m) ? 1.f : ex2_approx(m - m_new);
     bars->alpha[t][row] = alpha;
     mbar_arrive(&bars->alpha_full[t]);
     // A row with no key so far has m_new = -inf and every x = -inf: with the
     // offset 0 each p is exactly 0.
     const float neg = (m_new == -INFINITY) ? 0.f : off - m_new;
-    l = fmaf(l, alpha, exp_tile<kF16>(v, cm, neg, s_addr));
+    l = fmaf(l, alpha, exp_row<kF16>(v, cm, neg, s_addr, mk.none));
     m = m_new;
     tmem_st_wait();
     tc_fence_before_sync();
@@ -279,13 +245,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, const 
     ok = __all_sync(0xffffffffu, ok);
     if (ok) tc_fence_after_sync();
   }
-  if (!ok) return;
-  const float inv_l = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-  const uint64_t inv2 = f2_pack(inv_l, inv_l);
-  const bool store = qi < p.Nq;
+  if (!ok || q0 >= p.Nq) return;
   // a row that saw nothing gets zeros even if its tile's products hold NaN
   const bool empty = l == 0.f;
-  uint16_t* orow = p.O + b * p.o_sb + h * p.o_sh + qi * p.o_sn;
+  const float inv_l = empty ? 0.f : 1.f / l;
+  const uint64_t inv2 = f2_pack(inv_l, inv_l);
   const uint32_t o_addr = lane_base + C::kOCol0 + static_cast<uint32_t>(t * HD);
 #pragma unroll
   for (int ch = 0; ch < HD / 32; ++ch) {
@@ -306,15 +270,21 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, const 
                 a0, a1);
       packed[e] = empty ? 0u : pack2<kF16>(a0, a1);
     }
-    if (store) {
-      uint4* dst = reinterpret_cast<uint4*>(orow + ch * 32);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        dst[e] = make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]);
-    }
+    stage_row32(sQt, row, ch * 32, packed);  // over Q_t, whose last reader is done
   }
-  if (store)
+  if (qi < p.Nq)
     p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+  fence_proxy_async();
+  mbar_arrive(&bars->staged[t]);
+  if (quarter == 0) {
+    ok = mbar_wait(&bars->staged[t], 0u, wc, kSiteStage);
+    if (ok && lane == 0) {
+#pragma unroll
+      for (int cb = 0; cb < HD / 64; ++cb) tma_store_4d(tmO, sQt + cb * BM * 128, cb * 64, q0, h, b);
+      tma_store_drain();
+    }
+    __syncwarp();
+  }
 }
 
 // ------------------------------------------------------------------ correction
@@ -443,9 +413,12 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUte
 
 // ------------------------------------------------------------------ MMA issuer
 // Warp-wide: one elected lane issues (mma_ss_k).
+// slope_tiles: the slope operands (mode slopes, 0 if this head's slope is not
+// used that way); p0: position of the first row, left0, left1: PlanTile::left.
 template <int HD, bool kF16, int MODE>
 __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ, uint8_t* sKV,
-                                         Range r0, Range r1, int n, WaitCtl wc) {
+                                         Range r0, Range r1, int n, int kt0, uint32_t slope_tiles, int p0,
+                                         bool left0, bool left1, WaitCtl wc) {
   using C = Cfg<HD, MODE>;
   const uint64_t q_desc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
   const uint64_t q_desc1 = q_desc0 + static_cast<uint64_t>(C::kQBytes >> 4);
@@ -454,6 +427,14 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
   constexpr uint64_t kStageStep = static_cast<uint64_t>(C::kTileBytes >> 4);
   const uint32_t s_col0 = tmem, s_col1 = tmem + BN;
   const uint32_t o_col0 = tmem + C::kOCol0, o_col1 = tmem + C::kOCol0 + HD;
+  // the slope's share of a score tile: one more step of 16 inner elements
+  [[maybe_unused]] auto add_slope = [&](uint32_t s_col, int j, int pt, bool left) {
+    if (slope_tiles == 0) return;
+    const int side = slope_side((kt0 + j) * BN, pt, left);
+    if (side == 0) return;
+    mma_ss_k<1, true>(s_col, sdesc_plain(slope_tiles + (side < 0 ? kSlopeTileBytes : 0)),
+                      sdesc_plain(slope_tiles + 2 * kSlopeTileBytes), idesc_f16_f32(128, 128, 0, kF16));
+  };
   bool ok = true;
 
   for (int j = 0; ok && j <= n; ++j) {
@@ -478,6 +459,7 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
     }
     if (i0 >= 0 && i0 < r0.n) {
       mma_abt_128<HD, kF16, true>(s_col0, q_desc0, k_desc + ks * kStageStep);
+      if constexpr (MODE == kModSlopes) add_slope(s_col0, j, p0, left0);
       mma_commit<true>(&bars->s_full[0]);
     }
     if (i1 > 0 && i1 <= r1.n) {
@@ -489,6 +471,7 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
     }
     if (i1 >= 0 && i1 < r1.n) {
       mma_abt_128<HD, kF16, true>(s_col1, q_desc1, k_desc + ks * kStageStep);
+      if constexpr (MODE == kModSlopes) add_slope(s_col1, j, p0 + BM, left1);
       mma_commit<true>(&bars->s_full[1]);
     }
     mma_commit<true>(&bars->kv_empty[j % C::kIters]);
@@ -501,15 +484,20 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
 template <int HD, bool kF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_mod_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const Params p) {
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                   const Params p) {
   using C = Cfg<HD, MODE>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // No static shared memory: the dynamic part starts on the alignment that
+  // swizzled tiles need.  (Rounding up at run time would take another 1 KB.)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicExch(p.status, 3u /* OSATTN_ERR_CUDA */);
+    return;
+  }
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + kQTiles * C::kQBytes;
   float* bias = reinterpret_cast<float*>(smem + C::kTileRegion);
-  Bars* bars = reinterpret_cast<Bars*>(smem + C::kTileRegion + C::kRelBytes);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kTileRegion + C::kTableBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // Work unit: 256 query rows of one (b, h).  Within groups of group_heads
@@ -524,20 +512,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b = bh / p.H, h = bh % p.H;
   const int q0 = qb * (kQTiles * BM);
   const int t0 = qb * kQTiles;
-  const int4 pt0 = plan_tile(p.plan, b, p.n_tiles, t0, p.Nkv);
-  const int4 pt1 = t0 + 1 < p.n_tiles ? plan_tile(p.plan, b, p.n_tiles, t0 + 1, p.Nkv) : make_int4(0, 0, 0, 0);
-  const bool any0 = pt0.x < pt0.y, any1 = pt1.x < pt1.y;
+  const PlanTile pt0 = plan_tile(p.plan, b, p.n_tiles, t0, p.Nkv);
+  const PlanTile pt1 =
+      t0 + 1 < p.n_tiles ? plan_tile(p.plan, b, p.n_tiles, t0 + 1, p.Nkv) : PlanTile{0, 0, 0, 0, false};
+  const bool any0 = pt0.lo < pt0.hi, any1 = pt1.lo < pt1.hi;
   int lo = 0, hi = 0;  // keys that either tile sees
-  if (any0) lo = pt0.x, hi = pt0.y;
+  if (any0) lo = pt0.lo, hi = pt0.hi;
   if (any1) {
-    lo = any0 ? min(lo, pt1.x) : pt1.x;
-    hi = max(hi, pt1.y);
+    lo = any0 ? min(lo, pt1.lo) : pt1.lo;
+    hi = max(hi, pt1.hi);
   }
   const int kt0 = lo / BN;
   const int n = (hi + BN - 1) / BN - kt0;  // 0 when no row sees a key (lo = hi = 0)
   Range r0{0, 0}, r1{0, 0};
-  if (any0) r0 = Range{pt0.x / BN - kt0, (pt0.y + BN - 1) / BN - pt0.x / BN};
-  if (any1) r1 = Range{pt1.x / BN - kt0, (pt1.y + BN - 1) / BN - pt1.x / BN};
+  if (any0) r0 = Range{pt0.lo / BN - kt0, (pt0.hi + BN - 1) / BN - pt0.lo / BN};
+  if (any1) r1 = Range{pt1.lo / BN - kt0, (pt1.hi + BN - 1) / BN - pt1.lo / BN};
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < kQTiles; ++t) {
@@ -546,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->alpha_full[t], 128);
       mbar_init(&bars->p_full[t], 256);
       mbar_init(&bars->o_full[t], 1);
+      mbar_init(&bars->staged[t], 128);
     }
     for (int i = 0; i < C::kIters; ++i) {
       mbar_init(&bars->kv_full[i], 1);
@@ -565,8 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if constexpr (mode_rel(MODE)) rel_fill<kF16>(bias, p.rel, p.H, h);
-  if constexpr (mode_slopes(MODE)) {
-    if (threadIdx.x < BN) bias[threadIdx.x] = p.slopes[h] * kModLog2e * static_cast<float>(threadIdx.x);
+  if constexpr (MODE == kModSlopes) {
+    if (threadIdx.x < BN)
+      slope_fill_row<kF16>(reinterpret_cast<uint8_t*>(bias), threadIdx.x, p.slopes[h], p.scale);
+    fence_proxy_async();
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -578,8 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kCorrWarp0) {
     regs_inc<184>();
     const int t = warp >> 2;
-    softmax_role<HD, kF16, MODE>(p, bars, bias, tmem, t, b, h, q0 + t * BM, t ? r1 : r0, t ? pt1 : pt0,
-                                 kt0, wc);
+    softmax_role<HD, kF16, MODE>(&tmO, p, bars, bias, sQ + t * C::kQBytes, tmem, t, b, h, q0 + t * BM,
+                                 t ? r1 : r0, t ? pt1 : pt0, kt0, wc);
   } else if (warp < kProducerWarp) {
     regs_dec<88>();
     correction_role<HD, MODE>(bars, sKV, tmem, r0, r1, n, kt0, lo, hi, p.Nkv, wc);
@@ -587,8 +579,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<56>();
     if (warp == kProducerWarp && lane == 0 && n > 0)
       producer_role<HD, MODE>(&tmQ, &tmK, &tmV, bars, sQ, sKV, b, h, h / p.group, q0, r0, r1, n, kt0, wc);
-    else if (warp == kMmaWarp && n > 0)
-      mma_role<HD, kF16, MODE>(bars, tmem, sQ, sKV, r0, r1, n, wc);
+    else if (warp == kMmaWarp && n > 0) {
+      uint32_t slope_tiles = 0;
+      if constexpr (MODE == kModSlopes)
+        if (slope_linear(p.slopes[h], p.scale)) slope_tiles = smem_u32(bias);
+      mma_role<HD, kF16, MODE>(bars, tmem, sQ, sKV, r0, r1, n, kt0, slope_tiles, q0 + p.q_offset, pt0.left,
+                               pt1.left, wc);
+    }
   }
 
   __syncwarp();
@@ -629,18 +626,15 @@ cudaError_t prepare() {
 
 template <int HD, bool kF16, int MODE>
 cudaError_t launch_mode(unsigned grid, cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k,
-                        const CUtensorMap& v, const Params& p) {
-  fwd_mod_kernel<HD, kF16, MODE><<<grid, kThreads, smem_bytes<HD, MODE>(), s>>>(q, k, v, p);
+                        const CUtensorMap& v, const CUtensorMap& o, const Params& p) {
+  fwd_mod_kernel<HD, kF16, MODE><<<grid, kThreads, smem_bytes<HD, MODE>(), s>>>(q, k, v, o, p);
   return cudaGetLastError();
 }
 
 template <int HD, bool kF16>
-cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v) {
+cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   const CUtensorMap& o) {
   Params p;
-  p.O = static_cast<uint16_t*>(a.O);
-  p.o_sb = a.o_s[0];
-  p.o_sh = a.o_s[1];
-  p.o_sn = a.o_s[2];
   p.LSE = a.LSE;
   p.n_tiles = (a.Nq + BM - 1) / BM;
   p.plan.tiles = static_cast<const int4*>(a.plan);
@@ -659,8 +653,8 @@ cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k,
     p.group_heads = static_cast<int>(gh < 1 ? 1 : (gh > p.BH ? p.BH : gh));
   }
   p.scale_log2 = a.scale * kModLog2e;
-  p.cap_c1 = a.softcap > 0.f ? 2.f * a.scale * kModLog2e / a.softcap : 0.f;
-  p.cap2 = a.softcap * kModLog2e;
+  p.scale = a.scale;
+  p.cap = make_cap(a.scale, a.softcap);
   p.slopes = a.slopes;
   p.rel = a.rel;
   p.q_offset = a.q_offset;
@@ -670,11 +664,11 @@ cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k,
   if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned g = static_cast<unsigned>(units);
   switch (mod_score_mode(a)) {
-    case kModCap: return launch_mode<HD, kF16, kModCap>(g, a.stream, q, k, v, p);
-    case kModSlopes: return launch_mode<HD, kF16, kModSlopes>(g, a.stream, q, k, v, p);
-    case kModCapSlopes: return launch_mode<HD, kF16, kModCapSlopes>(g, a.stream, q, k, v, p);
-    case kModRel: return launch_mode<HD, kF16, kModRel>(g, a.stream, q, k, v, p);
-    default: return launch_mode<HD, kF16, kModPlain>(g, a.stream, q, k, v, p);
+    case kModCap: return launch_mode<HD, kF16, kModCap>(g, a.stream, q, k, v, o, p);
+    case kModSlopes: return launch_mode<HD, kF16, kModSlopes>(g, a.stream, q, k, v, o, p);
+    case kModCapSlopes: return launch_mode<HD, kF16, kModCapSlopes>(g, a.stream, q, k, v, o, p);
+    case kModRel: return launch_mode<HD, kF16, kModRel>(g, a.stream, q, k, v, o, p);
+    default: return launch_mode<HD, kF16, kModPlain>(g, a.stream, q, k, v, o, p);
   }
 }
 

@@ -56,7 +56,7 @@ __device__ int run_end(const int32_t* ids, int n, int from, int dir, int* slot) 
 }
 
 __global__ void __launch_bounds__(kPlanThreads) mask_plan_kernel(const PlanParams p) {
-  __shared__ int slot, s_lo_min, s_hi_max, s_lo_max, s_hi_min;
+  __shared__ int slot, s_lo_min, s_hi_max, s_lo_max, s_hi_min, s_right;
   __shared__ int s_id[kPlanTile];
   __shared__ unsigned s_bits[2][kPlanThreads / 32];
   __shared__ int s_start[kPlanTile], s_end[kPlanTile];
@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kPlanThreads) mask_plan_kernel(const PlanParam
     s_hi_max = 0;
     s_lo_max = 0;
     s_hi_min = INT_MAX;
+    s_right = 0;
   }
   const long long pos = static_cast<long long>(i) + p.q_offset;
   if (ids) {
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) mask_plan_kernel(const PlanParam
     if (lo < hi) {
       atomicMin(&s_lo_min, static_cast<int>(lo));
       atomicMax(&s_hi_max, static_cast<int>(hi));
+      if (hi > pos + 1) s_right = 1;
     }
     atomicMax(&s_lo_max, static_cast<int>(lo));
     atomicMin(&s_hi_min, static_cast<int>(hi));
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kPlanThreads) mask_plan_kernel(const PlanParam
   __syncthreads();
   if (r == 0)
     p.tiles[blockIdx.x] =
-        make_int4(s_hi_max > 0 ? s_lo_min : 0, s_hi_max, s_lo_max, s_hi_min);
+        make_int4(s_hi_max > 0 ? s_lo_min : 0, s_hi_max, s_lo_max | (s_right ? 0 : kPlanLeft), s_hi_min);
 }
 
 }  // namespace

@@ -17,7 +17,8 @@ namespace fwdmod {
 template <int HD, bool kF16>
 cudaError_t prepare();
 template <int HD, bool kF16>
-cudaError_t launch(const ModArgs&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&);
+cudaError_t launch(const ModArgs&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                   const CUtensorMap&);
 }  // namespace fwdmod
 namespace bwdmod {
 template <int HD, bool kF16>
@@ -164,13 +165,12 @@ int osattn_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* 
   if (rc != OSATTN_OK) return rc;
   ModArgs a;
   common_args(&a, B, H, Hkv, Nq, Nkv, d, scale, score, plan, dtype, stream, dev);
-  a.O = O;
   a.LSE = LSE;
-  for (int i = 0; i < 3; ++i) a.o_s[i] = os[i];
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   if (api_encode_map(&tq, Q, a.fp16, d, Nq, H, B, qs, kBoxRows) != OSATTN_OK ||
       api_encode_map(&tk, K, a.fp16, d, Nkv, Hkv, B, ks, kBoxRows) != OSATTN_OK ||
-      api_encode_map(&tv, V, a.fp16, d, Nkv, Hkv, B, vs, kBoxRows) != OSATTN_OK)
+      api_encode_map(&tv, V, a.fp16, d, Nkv, Hkv, B, vs, kBoxRows) != OSATTN_OK ||
+      api_encode_map(&to, O, a.fp16, d, Nq, H, B, os, kBoxRows) != OSATTN_OK)
     return OSATTN_ERR_CUDA;
   const int slot = (d == 128 ? 2 : 0) + a.fp16;
   cudaError_t (*const prep[4])() = {fwdmod::prepare<64, false>, fwdmod::prepare<64, true>,
@@ -179,10 +179,10 @@ int osattn_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* 
   if (rc != OSATTN_OK) return rc;
   cudaError_t e;
   switch (slot) {
-    case 0: e = fwdmod::launch<64, false>(a, tq, tk, tv); break;
-    case 1: e = fwdmod::launch<64, true>(a, tq, tk, tv); break;
-    case 2: e = fwdmod::launch<128, false>(a, tq, tk, tv); break;
-    default: e = fwdmod::launch<128, true>(a, tq, tk, tv); break;
+    case 0: e = fwdmod::launch<64, false>(a, tq, tk, tv, to); break;
+    case 1: e = fwdmod::launch<64, true>(a, tq, tk, tv, to); break;
+    case 2: e = fwdmod::launch<128, false>(a, tq, tk, tv, to); break;
+    default: e = fwdmod::launch<128, true>(a, tq, tk, tv, to); break;
   }
   return e == cudaSuccess ? OSATTN_OK : OSATTN_ERR_CUDA;
 }

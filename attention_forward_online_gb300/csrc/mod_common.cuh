@@ -24,6 +24,10 @@ constexpr float kModLog2e = 1.4426950408889634f;
 // each pair that a call can ask for; a cap together with a learned bias is
 // refused by the entry points (its backward pass would have to hold two
 // factors per score in registers).
+// The polynomial of CapArgs.
+constexpr double kTanh0 = 0.9999999269, kTanh1 = -0.3333230998, kTanh2 = 0.1331017370,
+                 kTanh3 = -0.0521014809, kTanh4 = 0.0154754276;
+
 enum ScoreMode : int { kModPlain = 0, kModCap = 1, kModSlopes = 2, kModCapSlopes = 3, kModRel = 4 };
 __host__ __device__ constexpr bool mode_cap(int m) { return m == kModCap || m == kModCapSlopes; }
 __host__ __device__ constexpr bool mode_slopes(int m) { return m == kModSlopes || m == kModCapSlopes; }
@@ -32,15 +36,22 @@ __host__ __device__ constexpr bool mode_rel(int m) { return m == kModRel; }
 // Mask plan: per 128-row query tile {smallest lo, largest hi, largest lo,
 // smallest hi} (the first two over the rows that see a key, 0 and 0 if none
 // does), [B][tiles]; then per query row {lo, hi}, [B][Nq], {0, 0} for a row
-// that sees nothing.
+// that sees nothing.  Keys number at most 2^30; bit 30 of the third entry says
+// that no row of the tile sees a key behind its own position.
+constexpr int kPlanLeft = 1 << 30;
 struct PlanView {
   const int4* tiles;  // null: every row sees [0, Nkv)
   const int2* rows;
 };
+struct PlanTile {
+  int lo, hi, lo_max, hi_min;
+  bool left;
+};
 
-__device__ __forceinline__ int4 plan_tile(const PlanView& pv, int b, int n_tiles, int tile, int Nkv) {
-  if (!pv.tiles) return make_int4(0, Nkv, 0, Nkv);
-  return pv.tiles[static_cast<long long>(b) * n_tiles + tile];
+__device__ __forceinline__ PlanTile plan_tile(const PlanView& pv, int b, int n_tiles, int tile, int Nkv) {
+  if (!pv.tiles) return PlanTile{0, Nkv, 0, Nkv, false};
+  const int4 t = pv.tiles[static_cast<long long>(b) * n_tiles + tile];
+  return PlanTile{t.x, t.y, t.z & (kPlanLeft - 1), t.w, (t.z & kPlanLeft) != 0};
 }
 
 __device__ __forceinline__ int2 plan_row(const PlanView& pv, int b, int Nq, int i, int Nkv) {
@@ -68,6 +79,113 @@ __device__ __forceinline__ void fence_proxy_async() {
 // tanh (relative error 2^-11) would move it by 0.02.  E = inf gives r = 0.
 // c1 = 2 scale log2(e) / cap.
 __device__ __forceinline__ float cap_r(float s, float c1) { return rcp_approx(1.f + ex2_approx(s * c1)); }
+
+// A cap's constants.  For |y / cap| <= 0.6, tanh(z) = z t(z^2) with t of degree
+// 4: coefficients fitted here for the least relative error on that range
+// (2^-23.7, reweighted least squares on Chebyshev points).  k[n] carries
+// cap2 (scale / cap)^(2 n + 1), so that the polynomial is in the raw score:
+// cap2 tanh = s (k0 + s^2 (k1 + ...)).  s_max = 0.6 cap / scale, or -1 where
+// scale / cap is not in [2^-12, 2^12] (products could leave fp32's range) or
+// not positive: then the other form is used.
+struct CapArgs {
+  float c1, cap2, s_max;  // c1 = 2 scale log2(e) / cap
+  float k[5];
+};
+inline CapArgs make_cap(float scale, float softcap) {
+  CapArgs c{};
+  if (!(softcap > 0.f)) return c;
+  const double a = static_cast<double>(scale) / softcap;
+  const double cap2 = static_cast<double>(softcap) * 1.4426950408889634;
+  c.c1 = static_cast<float>(2.0 * a * 1.4426950408889634);
+  c.cap2 = static_cast<float>(cap2);
+  const double t[5] = {kTanh0, kTanh1, kTanh2, kTanh3, kTanh4};
+  const bool ok = a >= 1.0 / 4096 && a <= 4096.0;
+  c.s_max = ok ? static_cast<float>(0.6 / a) : -1.f;
+  double pw = a;
+  for (int n = 0; n < 5; ++n, pw *= a * a) c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;
+  return c;
+}
+__device__ __forceinline__ float cap_small(float s, const CapArgs& c) {
+  const float u = s * s;
+  return s * fmaf(fmaf(fmaf(fmaf(c.k[4], u, c.k[3]), u, c.k[2]), u, c.k[1]), u, c.k[0]);
+}
+// min(x, 30); NaN stays NaN
+__device__ __forceinline__ float min30(float x) {
+  float y;
+  asm("min.NaN.f32 %0, %1, 0f41F00000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Slopes on the tensor cores.  For keys on one side of a query,
+// -slope |j - p| = +-slope (j - p) is linear in the key's place e in its
+// tile; with one more MMA step of 16 inner elements, whose operands hold
+// (hi, mid, lo, 0 ...) of +-slope / scale in every query row and (e, e, e,
+// 0 ...) in key row e, the scores come out as s +- (slope / scale) e and what
+// is left of the bias is one constant per row and tile.  hi + mid + lo carry
+// slope / scale to 2^-24 in bf16 (three 8-bit pieces; fp16: to its smallest
+// step), e < 128 is exact, and the products are summed in fp32 as s is.
+// Tiles with keys on both sides of a row that sees them get the bias score
+// by score instead.
+// The operands: 128 rows of 16 elements as 8 x 16-byte core matrices, the two
+// of a row group 128 bytes apart, row groups 256 bytes apart, no swizzle.
+constexpr int kSlopeTileBytes = 128 * 32;
+constexpr int kSlopeBytes = 3 * kSlopeTileBytes;  // + pieces, - pieces, e
+constexpr float kSlopeMax = 16384.f;              // |slope / scale| beyond: score by score
+
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128u >> 4) << 16;  // next core matrix along the inner axis
+  d |= static_cast<uint64_t>(256u >> 4) << 32;  // next 8 rows
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+__device__ __forceinline__ bool slope_linear(float slope, float scale) {
+  return scale != 0.f && fabsf(slope / scale) <= kSlopeMax;
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint16_t to_16(float x) {
+  if constexpr (kF16) return __half_as_ushort(__float2half_rn(x));
+  else return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+template <bool kF16>
+__device__ __forceinline__ float from_16(uint16_t w) {
+  if constexpr (kF16) return __half2float(__ushort_as_half(w));
+  else return __bfloat162float(__ushort_as_bfloat16(w));
+}
+
+// Writes row `row` of the three operand tiles; the caller orders the writes
+// before the MMAs (fence_proxy_async and a barrier).
+template <bool kF16>
+__device__ __forceinline__ void slope_fill_row(uint8_t* tiles, int row, float slope, float scale) {
+  const float q = slope_linear(slope, scale) ? slope / scale : 0.f;
+  uint16_t w[3];
+  float rest = q;
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    w[x] = to_16<kF16>(rest);
+    rest -= from_16<kF16>(w[x]);
+  }
+  const uint32_t e = to_16<kF16>(static_cast<float>(row));
+  uint8_t* at = tiles + (row / 8) * 256 + (row % 8) * 16;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  *reinterpret_cast<uint4*>(at) = make_uint4(w[0] | (static_cast<uint32_t>(w[1]) << 16), w[2], 0u, 0u);
+  *reinterpret_cast<uint4*>(at + kSlopeTileBytes) =
+      make_uint4((w[0] ^ 0x8000u) | ((static_cast<uint32_t>(w[1]) ^ 0x8000u) << 16), w[2] ^ 0x8000u, 0u, 0u);
+  *reinterpret_cast<uint4*>(at + 2 * kSlopeTileBytes) = make_uint4(e | (e << 16), e, 0u, 0u);
+#pragma unroll
+  for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(at + t * kSlopeTileBytes + 128) = zero;
+}
+
+// Which side of a tile's rows its keys k0 .. k0 + 127 lie on: 1 before or at
+// (j <= p), -1 behind or at, 0 both.  p0: position of the tile's first row of
+// 128; `left`: no row of the tile sees a key behind its position.
+__device__ __forceinline__ int slope_side(int k0, int p0, bool left) {
+  if (left || k0 + 127 <= p0) return 1;
+  return k0 >= p0 + 127 ? -1 : 0;
+}
 
 // Bias by distance in shared memory, in base-2 units: entry j - p + R + kRelPad
 // holds table[map[clamp(j - p)]][h] * log2 e.  The pad lets a thread index a

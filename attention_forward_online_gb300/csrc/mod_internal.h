@@ -41,14 +41,12 @@ struct ModArgs {
   uint64_t wait_limit_ns;
   int num_sms;
   float* LSE;  // written by the forward pass, read by the backward pass
-  // forward
-  void* O;
-  long long o_s[3];  // element strides of the b, h and row axes
   // backward
   const void* O_in;
   void* dQ;
   void* dK;
   void* dV;
+  long long o_s[3];  // element strides of the b, h and row axes
   long long dq_s[3], dk_s[3], dv_s[3];
   float* D;         // workspace [B, H, Nq]
   float* rel_part;  // workspace [B, H, query tiles, 2 range + 1]
