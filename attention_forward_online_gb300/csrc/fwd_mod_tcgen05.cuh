@@ -92,6 +92,7 @@ struct __align__(16) Bars {
   uint32_t tmem_base;
   int abort_flag;
   float alpha[kQTiles][BM];
+  float rel_lo, rel_hi;  // least and greatest learned bias of the head
 };
 
 template <int HD, int MODE>
@@ -105,7 +106,8 @@ struct Params {
   int H, group, Nq, Nkv, BH;  // group: query heads per key/value head
   int num_q_blocks, n_tiles;  // 256-row units and 128-row tiles per (b, h)
   int group_heads;
-  float scale, scale_log2;  // scale, scale * log2(e)
+  float scale, scale_log2;  // |scale|, |scale| * log2(e) (positive_scale)
+  uint32_t neg_q;           // kIdescNegA if the scale is negative
   CapArgs cap;
   const float* slopes;
   RelArgs rel;
@@ -156,13 +158,19 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
   const int2 see = plan_row(p.plan, b, p.Nq, qi, p.Nkv);
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t s_addr = lane_base + static_cast<uint32_t>(t * BN);
-  const float c = p.scale_log2;
   [[maybe_unused]] const int p0 = q0 + p.q_offset, pos = p0 + row;
-  float slope2 = 0.f;
-  bool linear = false;
+  TileScore<kF16, MODE> ts;
+  ts.c = p.scale_log2;
+  ts.off = 0.f;
+  ts.cap = &p.cap;
+  [[maybe_unused]] bool linear = false;
   if constexpr (mode_slopes(MODE)) {
-    slope2 = p.slopes[h] * kModLog2e;
+    ts.slope2 = p.slopes[h] * kModLog2e;
     linear = MODE == kModSlopes && slope_linear(p.slopes[h], p.scale);
+  }
+  if constexpr (mode_rel(MODE)) {
+    ts.strip_lo = bars->rel_lo;
+    ts.strip_close = bars->rel_hi - bars->rel_lo <= ts.kSpread;
   }
   float m = -INFINITY, l = 0.f;
   bool ok = true;
@@ -174,67 +182,28 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
     tc_fence_after_sync();
     const int k0 = (kt0 + rg.a + j) * BN;
     const bool masked = !(tile.lo_max <= k0 && tile.hi_min >= k0 + BN);
-    Row v;
-    float ext[kChunks];
-    load_row(s_addr, v, ext);
+    const int lo = see.x - k0, hi = see.y - k0;
+    auto bits_of = [&](int ch) { return bit_range(lo - 32 * ch, hi - 32 * ch); };
     TileMask mk;
-    mk.none = 0u;
-    if (masked) {
-      const int lo = see.x - k0, hi = see.y - k0;
-#pragma unroll
-      for (int ch = 0; ch < kChunks; ++ch) mk.bits[ch] = bit_range(lo - 32 * ch, hi - 32 * ch);
-      classify(mk);
-    }
-    // x = v * cm + off in base-2 units; ext: the max of each chunk of v
-    float cm = c, off = 0.f;
-    if constexpr (mode_cap(MODE)) {
-      cap_row(v, ext, p.cap, masked, mk);
-      cm = 1.f;
-    } else if (!(c > 0.f)) {
-      scale_row(v, ext, c);
-      cm = 1.f;
-    }
+    if (masked) mk.classify(bits_of);
     if constexpr (mode_slopes(MODE)) {
       const int d0 = k0 - pos;  // distance of the tile's first key
       const int side = linear ? slope_side(k0, p0, tile.left) : 0;
-      if (side != 0) {
-        off = (side > 0 ? slope2 : -slope2) * static_cast<float>(d0);
-      } else {
-        const float f0 = static_cast<float>(d0);
-#pragma unroll
-        for (int e = 0; e < BN; ++e)
-          v[e] = __float_as_uint(fmaf(-slope2, fabsf(f0 + static_cast<float>(e)), __uint_as_float(v[e]) * cm));
-        cm = 1.f;
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) ext[ch] = chunk_max(v, ch);
-      }
+      ts.both_sides = side == 0;
+      ts.d0 = static_cast<float>(d0);
+      ts.off = side == 0 ? 0.f : (side > 0 ? ts.slope2 : -ts.slope2) * ts.d0;
     }
     if constexpr (mode_rel(MODE)) {
       const int R = p.rel.range;
       const int first = k0 - p0;  // distances of the whole tile: first - 127 .. first + 127
-      if (first + BN - 1 <= -R || first - (BM - 1) >= R) {
-        off = bias[first <= 0 ? 0 : rel_entries(R) - 1];
-      } else {
-        const float* at = bias + (k0 - pos + R + kRelPad);
-        const uint64_t c2 = f2_pack(cm, cm);
-#pragma unroll
-        for (int e = 0; e < BN; e += 2)
-          set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(at[e], at[e + 1])));
-        cm = 1.f;
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) ext[ch] = chunk_max(v, ch);
-      }
+      const bool far = first + BN - 1 <= -R || first - (BM - 1) >= R;
+      ts.strip = far ? nullptr : bias + (k0 - pos + R + kRelPad);
+      ts.off = far ? bias[first <= 0 ? 0 : rel_entries(R) - 1] : 0.f;
     }
-    if (masked) apply_mask(v, ext, mk);
-    const float m_new = next_max(m, fmaf(max4(ext), cm, off));
-    const float alpha = (m_new == m) ? 1.f : ex2_approx(m - m_new);
-    bars->alpha[t][row] = alpha;
-    mbar_arrive(&bars->alpha_full[t]);
-    // A row with no key so far has m_new = -inf and every x = -inf: with the
-    // offset 0 each p is exactly 0.
-    const float neg = (m_new == -INFINITY) ? 0.f : off - m_new;
-    l = fmaf(l, alpha, exp_row<kF16>(v, cm, neg, s_addr, mk.none));
-    m = m_new;
+    ts.tile(s_addr, masked, mk, bits_of, m, l, [&](float alpha) {
+      bars->alpha[t][row] = alpha;
+      mbar_arrive(&bars->alpha_full[t]);
+    });
     tmem_st_wait();
     tc_fence_before_sync();
     mbar_arrive(&bars->p_full[t]);
@@ -414,11 +383,12 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUte
 // ------------------------------------------------------------------ MMA issuer
 // Warp-wide: one elected lane issues (mma_ss_k).
 // slope_tiles: the slope operands (mode slopes, 0 if this head's slope is not
-// used that way); p0: position of the first row, left0, left1: PlanTile::left.
+// used that way); p0: position of the first row, left0, left1: PlanTile::left;
+// neg_q: kIdescNegA for a negative scale.
 template <int HD, bool kF16, int MODE>
 __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ, uint8_t* sKV,
                                          Range r0, Range r1, int n, int kt0, uint32_t slope_tiles, int p0,
-                                         bool left0, bool left1, WaitCtl wc) {
+                                         bool left0, bool left1, uint32_t neg_q, WaitCtl wc) {
   using C = Cfg<HD, MODE>;
   const uint64_t q_desc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
   const uint64_t q_desc1 = q_desc0 + static_cast<uint64_t>(C::kQBytes >> 4);
@@ -427,6 +397,7 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
   constexpr uint64_t kStageStep = static_cast<uint64_t>(C::kTileBytes >> 4);
   const uint32_t s_col0 = tmem, s_col1 = tmem + BN;
   const uint32_t o_col0 = tmem + C::kOCol0, o_col1 = tmem + C::kOCol0 + HD;
+  const uint32_t s_id = idesc_f16_f32(128, 128, 0, kF16) | neg_q;
   // the slope's share of a score tile: one more step of 16 inner elements
   [[maybe_unused]] auto add_slope = [&](uint32_t s_col, int j, int pt, bool left) {
     if (slope_tiles == 0) return;
@@ -458,7 +429,7 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
       if (i0 == r0.n) mma_commit<true>(&bars->o_full[0]);
     }
     if (i0 >= 0 && i0 < r0.n) {
-      mma_abt_128<HD, kF16, true>(s_col0, q_desc0, k_desc + ks * kStageStep);
+      mma_abt_id<HD>(s_col0, q_desc0, k_desc + ks * kStageStep, s_id);
       if constexpr (MODE == kModSlopes) add_slope(s_col0, j, p0, left0);
       mma_commit<true>(&bars->s_full[0]);
     }
@@ -470,7 +441,7 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
       if (i1 == r1.n) mma_commit<true>(&bars->o_full[1]);
     }
     if (i1 >= 0 && i1 < r1.n) {
-      mma_abt_128<HD, kF16, true>(s_col1, q_desc1, k_desc + ks * kStageStep);
+      mma_abt_id<HD>(s_col1, q_desc1, k_desc + ks * kStageStep, s_id);
       if constexpr (MODE == kModSlopes) add_slope(s_col1, j, p0 + BM, left1);
       mma_commit<true>(&bars->s_full[1]);
     }
@@ -563,6 +534,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  if constexpr (mode_rel(MODE)) {
+    if (warp == 0) {  // the range of the head's biases, for the softmax's bounds
+      float a = INFINITY, z = -INFINITY;
+      for (int x = lane + kRelPad; x <= 2 * p.rel.range + kRelPad; x += 32) {
+        a = fminf(a, bias[x]);
+        z = fmaxf(z, bias[x]);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, off));
+      }
+      if (lane == 0) {
+        bars->rel_lo = a;
+        bars->rel_hi = z;
+      }
+    }
+    __syncthreads();
+  }
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
 
@@ -584,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (MODE == kModSlopes)
         if (slope_linear(p.slopes[h], p.scale)) slope_tiles = smem_u32(bias);
       mma_role<HD, kF16, MODE>(bars, tmem, sQ, sKV, r0, r1, n, kt0, slope_tiles, q0 + p.q_offset, pt0.left,
-                               pt1.left, wc);
+                               pt1.left, p.neg_q, wc);
     }
   }
 
@@ -652,9 +642,10 @@ cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k,
     const long long gh = (32ll << 20) / kv_head * p.group;
     p.group_heads = static_cast<int>(gh < 1 ? 1 : (gh > p.BH ? p.BH : gh));
   }
-  p.scale_log2 = a.scale * kModLog2e;
-  p.scale = a.scale;
-  p.cap = make_cap(a.scale, a.softcap);
+  p.scale = positive_scale(a.scale);
+  p.scale_log2 = p.scale * kModLog2e;
+  p.neg_q = a.scale < 0.f ? kIdescNegA : 0u;
+  p.cap = make_cap(p.scale, a.softcap);
   p.slopes = a.slopes;
   p.rel = a.rel;
   p.q_offset = a.q_offset;

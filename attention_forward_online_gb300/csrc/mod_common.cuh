@@ -24,10 +24,6 @@ constexpr float kModLog2e = 1.4426950408889634f;
 // each pair that a call can ask for; a cap together with a learned bias is
 // refused by the entry points (its backward pass would have to hold two
 // factors per score in registers).
-// The polynomial of CapArgs.
-constexpr double kTanh0 = 0.9999999269, kTanh1 = -0.3333230998, kTanh2 = 0.1331017370,
-                 kTanh3 = -0.0521014809, kTanh4 = 0.0154754276;
-
 enum ScoreMode : int { kModPlain = 0, kModCap = 1, kModSlopes = 2, kModCapSlopes = 3, kModRel = 4 };
 __host__ __device__ constexpr bool mode_cap(int m) { return m == kModCap || m == kModCapSlopes; }
 __host__ __device__ constexpr bool mode_slopes(int m) { return m == kModSlopes || m == kModCapSlopes; }
@@ -80,40 +76,57 @@ __device__ __forceinline__ void fence_proxy_async() {
 // c1 = 2 scale log2(e) / cap.
 __device__ __forceinline__ float cap_r(float s, float c1) { return rcp_approx(1.f + ex2_approx(s * c1)); }
 
-// A cap's constants.  For |y / cap| <= 0.6, tanh(z) = z t(z^2) with t of degree
-// 4: coefficients fitted here for the least relative error on that range
-// (2^-23.7, reweighted least squares on Chebyshev points).  k[n] carries
+// A cap's constants.  For |y / cap| <= 0.4, tanh(z) = z t(z^2) with t of degree
+// 3: coefficients fitted here for the least relative error on that range
+// (2^-23.3, reweighted least squares on Chebyshev points).  k[n] carries
 // cap2 (scale / cap)^(2 n + 1), so that the polynomial is in the raw score:
-// cap2 tanh = s (k0 + s^2 (k1 + ...)).  s_max = 0.6 cap / scale, or -1 where
-// scale / cap is not in [2^-12, 2^12] (products could leave fp32's range) or
-// not positive: then the other form is used.
+// cap2 tanh = s (k0 + s^2 (k1 + ...)).  s_max = 0.4 cap / scale, or -1 where
+// scale / cap is not in [2^-12, 2^12] (products could leave fp32's range):
+// then the other form is used.
 struct CapArgs {
   float c1, cap2, s_max;  // c1 = 2 scale log2(e) / cap
-  float k[5];
+  float k[4];
 };
 inline CapArgs make_cap(float scale, float softcap) {
   CapArgs c{};
   if (!(softcap > 0.f)) return c;
-  const double a = static_cast<double>(scale) / softcap;
+  const double a = static_cast<double>(scale) / softcap;  // scale >= 0
   const double cap2 = static_cast<double>(softcap) * 1.4426950408889634;
   c.c1 = static_cast<float>(2.0 * a * 1.4426950408889634);
   c.cap2 = static_cast<float>(cap2);
-  const double t[5] = {kTanh0, kTanh1, kTanh2, kTanh3, kTanh4};
+  const double t[4] = {0.9999999019, -0.3333136247, 0.1327097680, -0.0475536037};
   const bool ok = a >= 1.0 / 4096 && a <= 4096.0;
-  c.s_max = ok ? static_cast<float>(0.6 / a) : -1.f;
+  c.s_max = ok ? static_cast<float>(0.4 / a) : -1.f;
   double pw = a;
-  for (int n = 0; n < 5; ++n, pw *= a * a) c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;
+  for (int n = 0; n < 4; ++n, pw *= a * a) c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;
   return c;
-}
-__device__ __forceinline__ float cap_small(float s, const CapArgs& c) {
-  const float u = s * s;
-  return s * fmaf(fmaf(fmaf(fmaf(c.k[4], u, c.k[3]), u, c.k[2]), u, c.k[1]), u, c.k[0]);
 }
 // min(x, 30); NaN stays NaN
 __device__ __forceinline__ float min30(float x) {
   float y;
   asm("min.NaN.f32 %0, %1, 0f41F00000;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The kernels that negate an MMA operand for a negative scale work with its
+// magnitude; 0 becomes a value whose products with finite scores vanish but
+// that keeps -inf (a masked score) what it is.
+inline float positive_scale(float scale) {
+  const float a = scale < 0.f ? -scale : scale;
+  return a > 1e-30f ? a : 1e-30f;
+}
+// Instruction descriptor bit that negates A.
+constexpr uint32_t kIdescNegA = 1u << 13;
+
+// mma_abt with the instruction descriptor given.
+template <int KD>
+__device__ __forceinline__ void mma_abt_id(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t id) {
+  mma_ss_k<0, true>(d_tmem, a_desc, b_desc, id);
+#pragma unroll
+  for (int kk = 1; kk < KD / 16; ++kk) {
+    const uint32_t off = static_cast<uint32_t>(((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4);
+    mma_ss_k<1, true>(d_tmem, sdesc_add(a_desc, off), sdesc_add(b_desc, off), id);
+  }
 }
 
 // Slopes on the tensor cores.  For keys on one side of a query,
@@ -142,7 +155,7 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t smem_addr) {
 }
 
 __device__ __forceinline__ bool slope_linear(float slope, float scale) {
-  return scale != 0.f && fabsf(slope / scale) <= kSlopeMax;
+  return fabsf(slope / scale) <= kSlopeMax;
 }
 
 template <bool kF16>

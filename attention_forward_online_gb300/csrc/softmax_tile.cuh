@@ -1,6 +1,15 @@
 // softmax_tile.cuh - the elementwise work of one row of a 128-key score tile,
 // shared by the forward kernels with modified scores and over a paged cache.
-// A thread holds the row's 128 scores in registers, as four chunks of 32.
+//
+// One thread has a row and holds its 128 scores in registers.  The max that P
+// is formed against comes from the max that the tensor-memory loads return,
+// where the modification of the scores is monotonic or its spread over 32 keys
+// is small (a lower bound of the max will do, see kMaxSlack); the modification
+// then takes the shift by the max into its last multiply-add, and P follows in
+// the same pass.  Every instruction here costs time: the tiles' softmaxes are
+// bound by issue and latency, not by one pipe.  (A rolled loop that reads each
+// chunk of 32 scores again from tensor memory is a fourth of the code, and
+// 10 to 25 % slower.)
 #pragma once
 
 #include <cstdint>
@@ -10,66 +19,63 @@
 
 namespace osattn {
 
-constexpr int kTileKeys = 128;
 constexpr int kChunks = 4;
 constexpr uint32_t kMinusInf = 0xff800000u;
 
-// The running max is moved only when it grows by more than this (log2 units):
-// P then stays below 2^8, which neither fp32 sums nor 16-bit P mind, and the
-// accumulator in tensor memory is left alone on almost every tile.
+// The max that P is formed against is moved only when it grows by more than
+// this (log2 units), so that the accumulator in tensor memory is left alone on
+// almost every tile.  P may then exceed 1, by 2^8 and by as much as the max was
+// a lower bound only: fp32 sums and 16-bit P keep their relative precision.
 constexpr float kMaxSlack = 8.f;
 __device__ __forceinline__ float next_max(float m, float mx) { return mx > m + kMaxSlack ? mx : m; }
 
-using Row = uint32_t[kTileKeys];
+using Chunk = uint32_t[32];
 
-__device__ __forceinline__ uint64_t pair_of(const Row& v, int e) {
+__device__ __forceinline__ uint64_t pair_of(const Chunk& v, int e) {
   return f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
 }
-__device__ __forceinline__ void set_pair(Row& v, int e, uint64_t x) {
+__device__ __forceinline__ void set_pair(Chunk& v, int e, uint64_t x) {
   float a, b;
   f2_unpack(x, a, b);
   v[e] = __float_as_uint(a);
   v[e + 1] = __float_as_uint(b);
 }
 
+using Row = Chunk[kChunks];
+
 // The row's scores and the max of each chunk, formed by the loads.
-__device__ __forceinline__ void load_row(uint32_t s_addr, Row& v, float (&ext)[kChunks]) {
+__device__ __forceinline__ void load_row(uint32_t s_addr, Row& v, float (&top)[kChunks]) {
 #pragma unroll
-  for (int ch = 0; ch < kChunks; ++ch) tmem_ld_red_32x32b_x32<true>(s_addr + ch * 32, v + ch * 32, ext[ch]);
+  for (int ch = 0; ch < kChunks; ++ch) tmem_ld_red_32x32b_x32<true>(s_addr + ch * 32, v[ch], top[ch]);
   tmem_ld_wait();
 #pragma unroll
   for (int ch = 0; ch < kChunks; ++ch) {
-    reg_fence32(v + ch * 32);
-    asm volatile("" : "+f"(ext[ch]));
+    reg_fence32(v[ch]);
+    asm volatile("" : "+f"(top[ch]));
   }
 }
 
-__device__ __forceinline__ float chunk_max(const Row& v, int ch) {
+__device__ __forceinline__ float chunk_max(const Chunk& v) {
   float a[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = fmaxf(__uint_as_float(v[ch * 32 + i]), __uint_as_float(v[ch * 32 + 4 + i]));
+  for (int i = 0; i < 4; ++i) a[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[4 + i]));
 #pragma unroll
   for (int j = 8; j < 32; j += 8)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      a[i] = fmax3(a[i], __uint_as_float(v[ch * 32 + j + i]), __uint_as_float(v[ch * 32 + j + 4 + i]));
+      a[i] = fmax3(a[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 4 + i]));
   return fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
 }
-
-__device__ __forceinline__ float row_min(const Row& v) {
-  float a[8];
+__device__ __forceinline__ float chunk_min(const Chunk& v) {
+  float a[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = fminf(__uint_as_float(v[i]), __uint_as_float(v[i + 8]));
+  for (int i = 0; i < 4; ++i) a[i] = fminf(__uint_as_float(v[i]), __uint_as_float(v[4 + i]));
 #pragma unroll
-  for (int j = 16; j < kTileKeys; j += 16)
+  for (int j = 8; j < 32; j += 8)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      a[i] = fmin3(a[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 8 + i]));
-  return fmin3(fmin3(a[0], a[1], a[2]), fmin3(a[3], a[4], a[5]), fminf(a[6], a[7]));
-}
-
-__device__ __forceinline__ float max4(const float (&e)[kChunks]) {
-  return fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+    for (int i = 0; i < 4; ++i)
+      a[i] = fmin3(a[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 4 + i]));
+  return fminf(fmin3(a[0], a[1], a[2]), a[3]);
 }
 
 // Bits [from, to) of 32, for any from and to.
@@ -82,133 +88,212 @@ __device__ __forceinline__ uint32_t bit_range(int from, int to) {
 
 // What a warp's rows see of a tile, chunk by chunk: bit ch of `partial` set if
 // some row sees some but not every key of it, of `none` if no row sees one.
-// bits: the row's visible keys.  A mask costs only the chunks it cuts, and
-// keys that no row of the warp sees cost nothing.
+// A mask costs only the chunks it cuts, and keys that no row of the warp sees
+// cost nothing.  bits_of(ch): the row's visible keys of chunk ch.
 struct TileMask {
-  uint32_t bits[kChunks];
-  uint32_t partial, none;
+  uint32_t partial = 0u, none = 0u;
+  template <typename BitsOf>
+  __device__ __forceinline__ void classify(BitsOf&& bits_of) {
+#pragma unroll
+    for (int ch = 0; ch < kChunks; ++ch) {
+      const uint32_t bits = bits_of(ch);
+      if (!__any_sync(0xffffffffu, bits != 0u)) none |= 1u << ch;
+      else if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) partial |= 1u << ch;
+    }
+  }
 };
-__device__ __forceinline__ void classify(TileMask& k) {
-  k.partial = k.none = 0u;
+
+// `fill` at the row's masked keys.  Tests of single bits of a word cost one
+// instruction for several predicates, against two comparisons a key.
+__device__ __forceinline__ void mask_chunk(Chunk& v, uint32_t bits, uint32_t fill) {
 #pragma unroll
-  for (int ch = 0; ch < kChunks; ++ch) {
-    if (!__any_sync(0xffffffffu, k.bits[ch] != 0u)) k.none |= 1u << ch;
-    else if (!__all_sync(0xffffffffu, k.bits[ch] == 0xffffffffu)) k.partial |= 1u << ch;
+  for (int e = 0; e < 32; ++e) v[e] = (bits & (1u << e)) ? v[e] : fill;
+}
+
+// How one tile's scores become base-2 logits for one row: x = cap(s) c + off
+// (+ bias), where cap(s) c is cap2 tanh(s |scale| / cap) with a cap and s c
+// without.  c > 0: a negative scale's sign is in the scores (the MMA negates
+// an operand), and a scale of 0 is a c too small to matter.
+template <bool kF16, int MODE>
+struct TileScore {
+  float c;                // |scale| * log2(e)
+  float off;              // constant part of the bias
+  const CapArgs* cap;
+  float slope2, d0;       // both_sides: - slope2 |d0 + e|
+  bool both_sides;
+  const float* strip;     // learned bias of the tile's first key for this row, or null: off has it
+  float strip_lo;         // least bias of the head
+  bool strip_close;       // the head's biases lie within kSpread of each other
+
+  // How far a lower bound of the row max may be off: P then reaches
+  // 2^(kMaxSlack + this), which has to stay a finite 16-bit value.
+  static constexpr float kSpread = kF16 ? 7.f : 64.f;
+
+  // cap(s) c of one score
+  __device__ __forceinline__ float raw(float s) const {
+    if constexpr (mode_cap(MODE)) return fmaf(cap_r(s, cap->c1), -2.f * cap->cap2, cap->cap2);
+    else return s * c;
   }
-}
 
-// `fill` at the row's masked keys of chunk ch.  Tests of single bits of a word
-// cost one instruction for several predicates, against two comparisons a key.
-__device__ __forceinline__ void mask_chunk(Row& v, int ch, uint32_t bits, uint32_t fill) {
+  // One tile of the row: S at s_addr becomes P = 2^(x - m) in 16 bits over its
+  // first 64 columns.  Moves m, publishes the factor of the accumulator by
+  // publish(alpha) as soon as it is known, and updates l.
+  template <typename BitsOf, typename Publish>
+  __device__ __forceinline__ void tile(uint32_t s_addr, bool masked, const TileMask& k, BitsOf&& bits_of,
+                                       float& m, float& l, Publish&& publish) const {
+    Row v;
+    float top[kChunks];
+    load_row(s_addr, v, top);
+    if (masked) {
+      // Masked scores, which may hold anything: out of the max, and 0 where
+      // scores share a reciprocal.
 #pragma unroll
-  for (int e = 0; e < 32; ++e) v[ch * 32 + e] = (bits & (1u << e)) ? v[ch * 32 + e] : fill;
-}
-
-// -inf at masked keys; keeps ext in step.
-__device__ __forceinline__ void apply_mask(Row& v, float (&ext)[kChunks], const TileMask& k) {
+      for (int ch = 0; ch < kChunks; ++ch) {
+        if ((k.partial >> ch) & 1u) {
+          const uint32_t bits = bits_of(ch);
+          mask_chunk(v[ch], bits, kMinusInf);
+          top[ch] = chunk_max(v[ch]);
+          if constexpr (mode_cap(MODE)) mask_chunk(v[ch], bits, 0u);
+        }
+        if ((k.none >> ch) & 1u) {
+          top[ch] = -INFINITY;
+          if constexpr (mode_cap(MODE)) {
 #pragma unroll
-  for (int ch = 0; ch < kChunks; ++ch) {
-    if ((k.none >> ch) & 1u) ext[ch] = -INFINITY;
-    if ((k.partial >> ch) & 1u) {
-      mask_chunk(v, ch, k.bits[ch], kMinusInf);
-      ext[ch] = chunk_max(v, ch);
-    }
-  }
-}
-
-__device__ __forceinline__ void scale_row(Row& v, float (&ext)[kChunks], float c) {
-  const uint64_t c2 = f2_pack(c, c);
-#pragma unroll
-  for (int e = 0; e < kTileKeys; e += 2) set_pair(v, e, f2_mul(pair_of(v, e), c2));
-#pragma unroll
-  for (int ch = 0; ch < kChunks; ++ch) ext[ch] = chunk_max(v, ch);
-}
-
-// Raw scores to capped base-2 logits, cap2 tanh(y / cap), and ext with them.
-// Where every |y / cap| of the warp's rows is at most 0.6 (the usual case: a
-// cap is far above most scores) the tanh is an odd polynomial of degree 9 in
-// s (mod_common.cuh), 3 instructions a score and nothing for the
-// multifunction unit.  Otherwise cap2 - 2 cap2 / (1 + E) with one reciprocal
-// for four scores, 1 + E kept below 2^30 so that four multiply without
-// overflow (the tanh is 1 to the last bit long before).
-// Masked scores, which may hold anything, are set to 0 first.
-__device__ __forceinline__ void cap_row(Row& v, float (&ext)[kChunks], const CapArgs& cap, bool masked,
-                                        const TileMask& k) {
-  if (masked) {
-#pragma unroll
-    for (int ch = 0; ch < kChunks; ++ch)
-      if (((k.partial | k.none) >> ch) & 1u) {
-        mask_chunk(v, ch, k.bits[ch], 0u);
-        ext[ch] = chunk_max(v, ch);
+            for (int e = 0; e < 32; ++e) v[ch][e] = 0u;
+          }
+        }
       }
-  }
-  if (__all_sync(0xffffffffu, max4(ext) <= cap.s_max && row_min(v) >= -cap.s_max)) {
-    const uint64_t k0 = f2_pack(cap.k[0], cap.k[0]), k1 = f2_pack(cap.k[1], cap.k[1]),
-                   k2 = f2_pack(cap.k[2], cap.k[2]), k3 = f2_pack(cap.k[3], cap.k[3]),
-                   k4 = f2_pack(cap.k[4], cap.k[4]);
-#pragma unroll
-    for (int e = 0; e < kTileKeys; e += 2) {
-      const uint64_t s = pair_of(v, e), u = f2_mul(s, s);
-      const uint64_t q = f2_fma(f2_fma(f2_fma(f2_fma(k4, u, k3), u, k2), u, k1), u, k0);
-      set_pair(v, e, f2_mul(q, s));
     }
+    const float best_raw = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    bool direct = true;  // uniform over the warp
+    if constexpr (MODE == kModCap)
+      direct = __all_sync(0xffffffffu, best_raw <= cap->s_max &&
+                                           fminf(fminf(chunk_min(v[0]), chunk_min(v[1])),
+                                                 fminf(chunk_min(v[2]), chunk_min(v[3]))) >= -cap->s_max);
+    if constexpr (MODE == kModSlopes) direct = !both_sides;
+    if constexpr (MODE == kModCapSlopes) direct = false;
+    if constexpr (mode_rel(MODE)) direct = strip == nullptr;
+    float m_new, sum;
+    if (direct) {
+      m_new = next_max(m, best_raw == -INFINITY ? -INFINITY : raw(best_raw) + off);
+      publish(m_new == m ? 1.f : ex2_approx(m - m_new));
+      // a row with no key so far has m_new = -inf and every x = -inf: against
+      // 0 each p is exactly 0
+      const float n = off - (m_new == -INFINITY ? 0.f : m_new);
+      sum = masked ? exps<true, true>(s_addr, v, k, bits_of, n) : exps<false, true>(s_addr, v, k, bits_of, n);
+    } else if constexpr (MODE != kModPlain) {
+      float best = -INFINITY;
+      const bool bound = mode_rel(MODE) && strip_close;
+      if (bound && best_raw != -INFINITY) best = raw(best_raw) + strip_lo;
 #pragma unroll
-    for (int ch = 0; ch < kChunks; ++ch) ext[ch] = cap_small(ext[ch], cap);
-  } else {
-    const uint64_t c1 = f2_pack(cap.c1, cap.c1), one = f2_pack(1.f, 1.f);
-    const uint64_t mul = f2_pack(-2.f * cap.cap2, -2.f * cap.cap2), add = f2_pack(cap.cap2, cap.cap2);
-#pragma unroll
-    for (int e = 0; e < kTileKeys; e += 4) {
-      float z0, z1, z2, z3, px, py;
-      f2_unpack(f2_mul(pair_of(v, e), c1), z0, z1);
-      f2_unpack(f2_mul(pair_of(v, e + 2), c1), z2, z3);
-      const uint64_t ua = f2_add(f2_pack(ex2_approx(min30(z0)), ex2_approx(min30(z1))), one);
-      const uint64_t ub = f2_add(f2_pack(ex2_approx(min30(z2)), ex2_approx(min30(z3))), one);
-      f2_unpack(f2_mul(ua, ub), px, py);  // u0 u2, u1 u3
-      const float q = rcp_approx(px * py);
-      const uint64_t r = f2_mul(f2_pack(q, q), f2_pack(py, px));  // 1 / (u0 u2), 1 / (u1 u3)
-      set_pair(v, e, f2_fma(f2_mul(r, ub), mul, add));
-      set_pair(v, e + 2, f2_fma(f2_mul(r, ua), mul, add));
+      for (int ch = 0; ch < kChunks; ++ch) {
+        if ((k.none >> ch) & 1u) continue;
+        logits(v[ch], ch);
+        if (mode_cap(MODE) && ((k.partial >> ch) & 1u)) mask_chunk(v[ch], bits_of(ch), kMinusInf);
+        if (!bound) best = fmaxf(best, chunk_max(v[ch]));
+      }
+      m_new = next_max(m, best);
+      publish(m_new == m ? 1.f : ex2_approx(m - m_new));
+      sum = exps<true, false>(s_addr, v, k, bits_of, m_new == -INFINITY ? 0.f : -m_new);
     }
-#pragma unroll
-    for (int ch = 0; ch < kChunks; ++ch) ext[ch] = chunk_max(v, ch);
+    l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
+    m = m_new;
   }
-}
 
-// P = 2^(v cm + neg) in 16 bits over the first 64 columns of the row's scores,
-// and its sum.  Chunks of `none` are zeros.
-template <bool kF16>
-__device__ __forceinline__ float exp_row(const Row& v, float cm, float neg, uint32_t s_addr, uint32_t none) {
-  const uint64_t cm2 = f2_pack(cm, cm), nm2 = f2_pack(neg, neg);
-  uint64_t rs_a = 0, rs_b = 0;  // packed partial sums (bit pattern 0 = 0.0f)
+  // x in place of the 32 scores of chunk ch (tiles that are not direct).
+  __device__ __forceinline__ void logits(Chunk& v, int ch) const {
+    if constexpr (mode_cap(MODE)) {
+      // cap2 - 2 cap2 / (1 + E): one reciprocal for four scores, 1 + E kept
+      // below 2^30 so that four multiply without overflow (the tanh is 1 to
+      // the last bit long before)
+      const CapArgs& a = *cap;
+      const uint64_t c1 = f2_pack(a.c1, a.c1), one = f2_pack(1.f, 1.f);
+      const uint64_t mul = f2_pack(-2.f * a.cap2, -2.f * a.cap2), n = f2_pack(a.cap2, a.cap2);
 #pragma unroll
-  for (int ch = 0; ch < kChunks; ++ch) {
-    uint32_t pk[16];
-    if ((none >> ch) & 1u) {
+      for (int e = 0; e < 32; e += 4) {
+        float z0, z1, z2, z3, px, py;
+        f2_unpack(f2_mul(pair_of(v, e), c1), z0, z1);
+        f2_unpack(f2_mul(pair_of(v, e + 2), c1), z2, z3);
+        const uint64_t ua = f2_add(f2_pack(ex2_approx(min30(z0)), ex2_approx(min30(z1))), one);
+        const uint64_t ub = f2_add(f2_pack(ex2_approx(min30(z2)), ex2_approx(min30(z3))), one);
+        f2_unpack(f2_mul(ua, ub), px, py);  // u0 u2, u1 u3
+        const float q = rcp_approx(px * py);
+        const uint64_t r = f2_mul(f2_pack(q, q), f2_pack(py, px));  // 1 / (u0 u2), 1 / (u1 u3)
+        set_pair(v, e, f2_fma(f2_mul(r, ub), mul, n));
+        set_pair(v, e + 2, f2_fma(f2_mul(r, ua), mul, n));
+      }
+    } else if constexpr (mode_rel(MODE)) {
+      const float* at = strip + ch * 32;
+      const uint64_t c2 = f2_pack(c, c);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) pk[e] = 0u;
+      for (int e = 0; e < 32; e += 2) set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(at[e], at[e + 1])));
+    }
+    if constexpr (mode_slopes(MODE)) {
+      const float f0 = d0 + static_cast<float>(ch * 32), mul = mode_cap(MODE) ? 1.f : c;
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        v[e] = __float_as_uint(fmaf(-slope2, fabsf(f0 + static_cast<float>(e)), __uint_as_float(v[e]) * mul));
+    }
+  }
+
+  // x + n of two raw scores (direct tiles); n2: n twice, with off in it.
+  __device__ __forceinline__ uint64_t direct_pair(uint64_t s, uint64_t n2) const {
+    if constexpr (MODE == kModCap) {
+      const uint64_t u = f2_mul(s, s);
+      const uint64_t k0 = f2_pack(cap->k[0], cap->k[0]), k1 = f2_pack(cap->k[1], cap->k[1]),
+                     k2 = f2_pack(cap->k[2], cap->k[2]), k3 = f2_pack(cap->k[3], cap->k[3]);
+      return f2_fma(f2_fma(f2_fma(f2_fma(k3, u, k2), u, k1), u, k0), s, n2);
     } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float x0, x1;
-        f2_unpack(f2_fma(pair_of(v, ch * 32 + 2 * e), cm2, nm2), x0, x1);
-        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        const uint64_t pp = f2_pack(p0, p1);
-        if (e & 1)
-          rs_b = f2_add(rs_b, pp);
-        else
-          rs_a = f2_add(rs_a, pp);
-        if constexpr (kF16) pk[e] = pack_f16x2(p0, p1);
-        else pk[e] = pack_bf16x2(p0, p1);
-      }
+      return f2_fma(s, f2_pack(c, c), n2);
     }
-    tmem_st_32x32b_x16(s_addr + ch * 16, pk);
   }
-  float r0, r1, r2, r3;
-  f2_unpack(rs_a, r0, r1);
-  f2_unpack(rs_b, r2, r3);
-  return (r0 + r1) + (r2 + r3);
-}
+
+  // P in 16 bits over the first 64 columns of the row's scores, and the sum:
+  // 2^(x + n) from raw scores (kDirect, n with off), or 2^(v + n).  kMasked:
+  // chunks that no row of the warp sees are zeros.
+  template <bool kMasked, bool kDirect, typename BitsOf>
+  __device__ __forceinline__ float exps(uint32_t s_addr, const Row& v, const TileMask& k, BitsOf&& bits_of,
+                                        float n) const {
+    uint64_t rs_a = 0, rs_b = 0;  // packed partial sums (bit pattern 0 = 0.0f)
+    const uint64_t n2 = f2_pack(n, n);
+#pragma unroll
+    for (int ch = 0; ch < kChunks; ++ch) {
+      uint32_t pk[16];
+      if (kMasked && ((k.none >> ch) & 1u)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pk[e] = 0u;
+      } else {
+        // capped scores: a masked one was set to 0, not -inf
+        constexpr bool kCut = kMasked && kDirect && MODE == kModCap;
+        uint32_t bits = 0u;
+        if constexpr (kCut) bits = ((k.partial >> ch) & 1u) ? bits_of(ch) : 0xffffffffu;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t s = pair_of(v[ch], 2 * e);
+          float x0, x1;
+          f2_unpack(kDirect ? direct_pair(s, n2) : f2_add(s, n2), x0, x1);
+          if constexpr (kCut) {
+            x0 = (bits & (1u << (2 * e))) ? x0 : -INFINITY;
+            x1 = (bits & (2u << (2 * e))) ? x1 : -INFINITY;
+          }
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          const uint64_t pp = f2_pack(p0, p1);
+          if (e & 1)
+            rs_b = f2_add(rs_b, pp);
+          else
+            rs_a = f2_add(rs_a, pp);
+          if constexpr (kF16) pk[e] = pack_f16x2(p0, p1);
+          else pk[e] = pack_bf16x2(p0, p1);
+        }
+      }
+      tmem_st_32x32b_x16(s_addr + ch * 16, pk);
+    }
+    float r0, r1, r2, r3;
+    f2_unpack(rs_a, r0, r1);
+    f2_unpack(rs_b, r2, r3);
+    return (r0 + r1) + (r2 + r3);
+  }
+};
 
 // Writes 32 16-bit values of a row, from column col0 (a multiple of 8), into a
 // 128-row tile in shared memory in the layout of 64-column TMA boxes with the
