@@ -5,7 +5,6 @@
 namespace osattn {
 namespace bwdmod {
 template cudaError_t prepare<128, true>();
-template cudaError_t launch<128, true>(const ModArgs&, const CUtensorMap&, const CUtensorMap&,
-                                    const CUtensorMap&, const CUtensorMap&);
+template cudaError_t launch<128, true>(const ModArgs&, const BwdModMaps&);
 }  // namespace bwdmod
 }  // namespace osattn

@@ -5,7 +5,6 @@
 namespace osattn {
 namespace bwdmod {
 template cudaError_t prepare<64, false>();
-template cudaError_t launch<64, false>(const ModArgs&, const CUtensorMap&, const CUtensorMap&,
-                                    const CUtensorMap&, const CUtensorMap&);
+template cudaError_t launch<64, false>(const ModArgs&, const BwdModMaps&);
 }  // namespace bwdmod
 }  // namespace osattn

@@ -38,6 +38,7 @@
 #include "mod_common.cuh"
 #include "mod_internal.h"
 #include "sm100_ptx.cuh"
+#include "softmax_tile.cuh"
 #include "tc_attn_mma.cuh"
 
 namespace osattn {
@@ -50,24 +51,35 @@ constexpr uint32_t kCols = 512;
 
 enum : uint32_t { kSiteLoad = 61, kSiteMma = 62, kSiteElem = 63, kSiteEpi = 64, kSiteSync = 65 };
 
+// Sums of dY by distance: entry distance + R + kSumPad, padded so that a whole
+// 128 x 128 tile that overlaps (-R, R) is indexed without clamping.
+constexpr int kSumPad = 255;
+__host__ __device__ constexpr int sum_entries(int R) { return 2 * (R + kSumPad) + 1; }
+
 template <int HD, int MODE>
 struct Cfg {
   static constexpr int kTileBytes = kT * HD * 2;
-  static constexpr int kRelBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16 : 0;
+  // table of learned biases, or the slope operands
+  static constexpr int kTableBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16
+                                                    : (MODE == kModSlopes ? kSlopeKBytes + 4 * kSlopeQBytes : 0);
   // dkdv: K, V, kStages stages of (Q_i, dO_i), then per stage LSE, D, lo, hi
   static constexpr int kStages = HD == 128 ? 2 : 4;
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kDkdvRows = 2 * kTileBytes + kStages * kStageBytes;
-  static constexpr int kDkdvRel = kDkdvRows + kStages * kT * 16;
-  static constexpr int kDkdvRegion = kDkdvRel + kRelBytes;
+  static constexpr int kDkdvTable = kDkdvRows + kStages * kT * 16;
+  static constexpr int kDkdvRegion = kDkdvTable + kTableBytes;
   // dq: Q, dO, kKSlots K tiles, kVSlots V tiles (K_j is read until dQ_j, V_j
-  // until dP_j); with a learned bias the table, its sums by distance and the
-  // warps' diagonal strips take the place of the third K tile at d = 128.
+  // until dP_j); with a learned bias the table, the sums by distance and the
+  // warps' diagonal strips take the place of the third K tile at d = 128.  The
+  // slopes' key operand has 64 rows here, used for each half of a tile.
   static constexpr int kKSlots = HD == 128 ? (mode_rel(MODE) ? 2 : 3) : 4;
   static constexpr int kVSlots = HD == 128 ? 2 : 4;
-  static constexpr int kDqRel = (2 + kKSlots + kVSlots) * kTileBytes;
+  static constexpr int kDqTable = (2 + kKSlots + kVSlots) * kTileBytes;
+  static constexpr int kDqTableBytes = MODE == kModSlopes ? kSlopeKBytes / 2 + kSlopeQBytes : kTableBytes;
+  static constexpr int kDqSums = kDqTable + kDqTableBytes;
+  static constexpr int kSumBytes = mode_rel(MODE) ? (sum_entries(kMaxRelRange) * 4 + 15) / 16 * 16 : 0;
   static constexpr int kStripBytes = mode_rel(MODE) ? 2 * 8 * 96 * 4 : 0;
-  static constexpr int kDqRegion = kDqRel + 2 * kRelBytes + kStripBytes;
+  static constexpr int kDqRegion = kDqSums + kSumBytes + kStripBytes;
   static constexpr uint32_t kColAcc0 = 256;       // dV
   static constexpr uint32_t kColAcc1 = 256 + HD;  // dK
 };
@@ -85,27 +97,25 @@ struct __align__(16) Bars {
   uint64_t mma_drain;
   uint64_t d_full;
   uint64_t elem;
+  uint64_t staged[2];             // an output tile is in shared memory (dq: 256, dkdv: 128 arrivals)
   uint32_t tmem_base;
   int abort_flag;
   int it_lo, it_hi;
+  int side[4];                    // dkdv: slope_side of the stage's query tile, 0 if not linear
   float d_part[2][kT];
   float far_part[2][8];
 };
 
 template <int HD, int MODE>
 constexpr int dkdv_smem_bytes() {
-  return Cfg<HD, MODE>::kDkdvRegion + static_cast<int>(sizeof(Bars)) + 1024;
+  return Cfg<HD, MODE>::kDkdvRegion + static_cast<int>(sizeof(Bars));
 }
 template <int HD, int MODE>
 constexpr int dq_smem_bytes() {
-  return Cfg<HD, MODE>::kDqRegion + static_cast<int>(sizeof(Bars)) + 1024;
+  return Cfg<HD, MODE>::kDqRegion + static_cast<int>(sizeof(Bars));
 }
 
 struct Params {
-  uint16_t* dQ;
-  uint16_t* dK;
-  uint16_t* dV;
-  long long dq_s[3], dk_s[3], dv_s[3];
   const float* LSE;
   float* D;
   const uint16_t* O;
@@ -118,7 +128,7 @@ struct Params {
   int group_heads;  // heads per last-tile-first (dq) or first-tile-first (dkdv) group of CTAs
   float scale;
   float scale_log2;
-  float cap_c1, cap2;
+  CapArgs cap;
   const float* slopes;
   RelArgs rel;
   float* rel_part;
@@ -174,8 +184,11 @@ __device__ __forceinline__ void unit_of(const Params& p, int& bh, int& rank) {
   rank = r / gsize;
 }
 
+// NC fp32 tensor-memory columns of one tile row, starting at taddr, times
+// `mul`, as 16-bit values into an output tile in shared memory from column
+// col0 (zeros when has_acc is false).
 template <int NC, bool kF16>
-__device__ __forceinline__ void write_row(uint16_t* dst, uint32_t taddr, bool has_acc, bool store,
+__device__ __forceinline__ void stage_out(uint8_t* tile, int row, int col0, uint32_t taddr, bool has_acc,
                                           float mul) {
 #pragma unroll
   for (int ch = 0; ch < NC / 32; ++ch) {
@@ -192,11 +205,7 @@ __device__ __forceinline__ void write_row(uint16_t* dst, uint32_t taddr, bool ha
 #pragma unroll
     for (int e = 0; e < 16; ++e)
       pk[e] = pack2<kF16>(__uint_as_float(r[2 * e]) * mul, __uint_as_float(r[2 * e + 1]) * mul);
-    if (store) {
-      uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-    }
+    stage_row32(tile, row, col0 + ch * 32, pk);
   }
 }
 
@@ -209,64 +218,109 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int cb, int row) {
 
 // P part over the 64 columns of this thread's group at tile column c0:
 // P = 2^(x - LSE log2 e) with x the modified score; kMask selects 0 where
-// vis(column) is false.  nl2of4(column): -LSE log2 e of 4 columns.
-// dist(column) = key position less query position of that entry (slopes),
-// bias(column) = the learned bias in base-2 units.  kWriteP writes the 16-bit
-// P over columns c0 .. c0 + 31.  On return pr holds what dS is made of:
-// P, times 1 - tanh^2 = 4 r (1 - r) where scores are capped.
-template <bool kF16, int MODE, bool kWriteP, bool kMask, typename Vis, typename L2of4, typename Dist,
+// vis(column) is false.  nl2of4(column): -LSE log2 e of 4 columns, with the
+// constant part of the bias.  kBias adds bias(column), score by score.
+// kWriteP writes the 16-bit P over columns c0 .. c0 + 31.  On return pr holds
+// what dS is made of: P, times 1 - tanh^2 where scores are capped.  (A cap
+// takes the polynomial where the 32 scores at hand allow it, see CapArgs.)
+template <bool kF16, int MODE, bool kWriteP, bool kMask, bool kBias, typename Vis, typename L2of4,
           typename Bias>
-__device__ __forceinline__ void p_part(uint32_t s_addr, int c0, const Params& p, float slope2, Vis&& vis,
-                                       L2of4&& nl2of4, Dist&& dist, Bias&& bias, float (&pr)[64]) {
-  uint32_t sa[32], sb[32];
-  tmem_ld_32x32b_x32(s_addr + c0, sa);
+__device__ __forceinline__ void p_part(uint32_t s_addr, int c0, const Params& p, Vis&& vis, L2of4&& nl2of4,
+                                       Bias&& bias, float (&pr)[64]) {
+  constexpr bool kCap = mode_cap(MODE);
+  Chunk sa, sb;
+  float ta = 0.f, tb = 0.f;
+  if constexpr (kCap) tmem_ld_red_32x32b_x32<true>(s_addr + c0, sa, ta);
+  else tmem_ld_32x32b_x32(s_addr + c0, sa);
   tmem_ld_wait();
   reg_fence32(sa);
-  tmem_ld_32x32b_x32(s_addr + c0 + 32, sb);
-  auto half = [&](const uint32_t(&sv)[32], int h) {
+  asm volatile("" : "+f"(ta));
+  if constexpr (kCap) tmem_ld_red_32x32b_x32<true>(s_addr + c0 + 32, sb, tb);
+  else tmem_ld_32x32b_x32(s_addr + c0 + 32, sb);
+  const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+  auto half = [&](Chunk& sv, float top, int h) {
     uint32_t pk[16];
+    bool small = true;
+    if constexpr (kCap) {
+      if constexpr (kMask) {  // masked scores, which may hold anything, take no part in the choice
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      const float4 L = nl2of4(c0 + 32 * h + 4 * g);
-      const float nl[4] = {L.x, L.y, L.z, L.w};
-      float e[4], f[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int col = c0 + 32 * h + 4 * g + u;
-        const float s = __uint_as_float(sv[4 * g + u]);
-        float x = nl[u];
-        if constexpr (mode_slopes(MODE)) x = fmaf(-slope2, fabsf(dist(col)), x);
-        if constexpr (mode_rel(MODE)) x += bias(col);
-        if constexpr (mode_cap(MODE)) {
-          const float r = cap_r(s, p.cap_c1);
-          x += fmaf(r, -2.f * p.cap2, p.cap2);
-          f[u] = 4.f * r * (1.f - r);
-        } else {
-          x = fmaf(s, p.scale_log2, x);
-        }
-        e[u] = ex2_approx(x);
-        if constexpr (kMask) e[u] = vis(col) ? e[u] : 0.f;
+        for (int e = 0; e < 32; ++e) sv[e] = vis(c0 + 32 * h + e) ? sv[e] : 0u;
+        top = chunk_max(sv);
       }
-      if constexpr (kWriteP) {
-        pk[2 * g] = pack2<kF16>(e[0], e[1]);
-        pk[2 * g + 1] = pack2<kF16>(e[2], e[3]);
+      small = __all_sync(0xffffffffu, top <= p.cap.s_max && chunk_min(sv) >= -p.cap.s_max);
+    }
+    auto finish = [&](int x, uint64_t a2, uint64_t f2) {  // entries x, x + 1 of the half: exponent, factor
+      const int col = c0 + 32 * h + x;
+      if constexpr (kBias) a2 = f2_add(a2, f2_pack(bias(col), bias(col + 1)));
+      float a0, a1;
+      f2_unpack(a2, a0, a1);
+      float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
+      if constexpr (kMask) {
+        e0 = vis(col) ? e0 : 0.f;
+        e1 = vis(col + 1) ? e1 : 0.f;
       }
+      if constexpr (kWriteP) pk[x / 2] = pack2<kF16>(e0, e1);
+      if constexpr (kCap) f2_unpack(f2_mul(f2_pack(e0, e1), f2), e0, e1);
+      pr[32 * h + x] = e0;
+      pr[32 * h + x + 1] = e1;
+    };
+    if (!kCap || small) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float v = e[u];
-        if constexpr (mode_cap(MODE)) {
-          v = e[u] * f[u];
-          if constexpr (kMask) v = e[u] == 0.f ? 0.f : v;  // a masked score may be NaN
+      for (int g = 0; g < 8; ++g) {
+        const float4 L = nl2of4(c0 + 32 * h + 4 * g);
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          const int x = 4 * g + u;
+          const uint64_t s2 = pair_of(sv, x), n2 = u == 0 ? f2_pack(L.x, L.y) : f2_pack(L.z, L.w);
+          if constexpr (kCap) {
+            const CapArgs& a = p.cap;
+            const uint64_t w = f2_mul(s2, s2);
+            const uint64_t q = f2_fma(f2_fma(f2_fma(f2_pack(a.k[3], a.k[3]), w, f2_pack(a.k[2], a.k[2])), w,
+                                             f2_pack(a.k[1], a.k[1])),
+                                      w, f2_pack(a.k[0], a.k[0]));
+            const uint64_t y = f2_mul(q, s2);  // cap2 tanh
+            finish(x, f2_add(y, n2), f2_fma(f2_mul(y, y), f2_pack(-a.inv2, -a.inv2), f2_pack(1.f, 1.f)));
+          } else {
+            finish(x, f2_fma(s2, c2, n2), 0ull);
+          }
         }
-        pr[32 * h + 4 * g + u] = v;
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float4 L = nl2of4(c0 + 32 * h + 4 * g);
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          const int x = 4 * g + u;
+          const float r0 = cap_r(__uint_as_float(sv[x]), p.cap.c1), r1 = cap_r(__uint_as_float(sv[x + 1]), p.cap.c1);
+          const uint64_t r = f2_pack(r0, r1), n2 = u == 0 ? f2_pack(L.x, L.y) : f2_pack(L.z, L.w);
+          const uint64_t y = f2_fma(r, f2_pack(-2.f * p.cap.cap2, -2.f * p.cap.cap2), f2_pack(p.cap.cap2, p.cap.cap2));
+          // 1 - tanh^2 = 4 r (1 - r)
+          const uint64_t f = f2_mul(f2_mul(r, f2_pack(4.f, 4.f)), f2_fma(r, f2_pack(-1.f, -1.f), f2_pack(1.f, 1.f)));
+          finish(x, f2_add(y, n2), f);
+        }
       }
     }
     if constexpr (kWriteP) tmem_st_32x32b_x16(s_addr + c0 + 16 * h, pk);
   };
-  half(sa, 0);
+  half(sa, ta, 0);
   tmem_ld_wait();
   reg_fence32(sb);
-  half(sb, 1);
+  asm volatile("" : "+f"(tb));
+  half(sb, tb, 1);
+}
+
+// P of a group that no row of the warp sees: zeros.
+template <bool kWriteP>
+__device__ __forceinline__ void p_none(uint32_t s_addr, int c0, float (&pr)[64]) {
+#pragma unroll
+  for (int x = 0; x < 64; ++x) pr[x] = 0.f;
+  if constexpr (kWriteP) {
+    uint32_t z[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) z[e] = 0u;
+    tmem_st_32x32b_x32(s_addr + c0, z);
+  }
 }
 
 // dS part over the same 64 columns of the dP tile: dS = pr (dP - D), in 16
@@ -325,13 +379,27 @@ __device__ __forceinline__ void mma_groups(uint32_t d_tmem, uint32_t a_tmem, uin
                       sdesc_add(b_desc, static_cast<uint32_t>((kk * 2048) >> 4)), id);
 }
 
-// Whether a learned bias is one value over a tile of keys k0 .. k0 + 127 and
-// queries at positions p0 .. p0 + 127: -1 (all at or below -R), 1 (at or above R), 0.
-__device__ __forceinline__ int far_side(int k0, int p0, int R) {
-  const int first = k0 - p0;
-  if (first + kT - 1 <= -R) return -1;
-  if (first - (kT - 1) >= R) return 1;
-  return 0;
+// Whether a learned bias is one value over distances first .. last: -1 (all at
+// or below -R), 1 (all at or above R), 0.
+__device__ __forceinline__ int far_side(int first, int last, int R) {
+  return last <= -R ? -1 : (first >= R ? 1 : 0);
+}
+
+// The slope's share of a score tile: one more step of 16 inner elements, q_at
+// and k_at the operands.  Transposed tile (128 keys by 128 queries):
+template <bool kF16>
+__device__ __forceinline__ void add_slope_t(uint32_t s_col, uint32_t q_at, uint32_t k_at, int side) {
+  if (side == 0) return;
+  mma_ss_k<1, true>(s_col, slope_k_desc(k_at), slope_q_desc(q_at),
+                    idesc_f16_f32(128, 128, 0, kF16) | (side < 0 ? kIdescNegA : 0u));
+}
+// 128 queries by two halves of 64 keys, each counted from its own first key:
+template <bool kF16>
+__device__ __forceinline__ void add_slope(uint32_t s_col, uint32_t q_at, uint32_t k_at, int side) {
+  if (side == 0) return;
+  const uint32_t id = idesc_f16_f32(128, 64, 0, kF16) | (side < 0 ? kIdescNegA : 0u);
+  mma_ss_k<1, true>(s_col, slope_q_desc(q_at), slope_k_desc(k_at), id);
+  mma_ss_k<1, true>(s_col + 64, slope_q_desc(q_at), slope_k_desc(k_at), id);
 }
 
 // ------------------------------------------------------------------ dK, dV
@@ -339,11 +407,14 @@ template <int HD, bool kF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
                 const Params p) {
   using C = Cfg<HD, MODE>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // see fwd_mod_kernel
+    if (threadIdx.x == 0) atomicExch(p.status, 3u /* OSATTN_ERR_CUDA */);
+    return;
+  }
   uint8_t* sK = smem;
   uint8_t* sV = smem + C::kTileBytes;
   uint8_t* ring = smem + 2 * C::kTileBytes;  // stage s: Q_i at +0, dO_i at +kTileBytes
@@ -351,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* dsum = lse2 + C::kStages * kT;                         //   -D
   int* slo = reinterpret_cast<int*>(dsum + C::kStages * kT);    //   lo, hi of the query
   int* shi = slo + C::kStages * kT;
-  float* bias_all = reinterpret_cast<float*>(smem + C::kDkdvRel);
+  float* bias_all = reinterpret_cast<float*>(smem + C::kDkdvTable);  // or the slope operands
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kDkdvRegion);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -374,6 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->acc_full, 1);
     mbar_init(&bars->mma_drain, 1);
     mbar_init(&bars->elem, 256);
+    mbar_init(&bars->staged[0], 128);
+    mbar_init(&bars->staged[1], 128);
     bars->abort_flag = 0;
     bars->it_lo = p.q_tiles;
     bars->it_hi = 0;
@@ -382,6 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, kCols);
     tmem_relinquish();
+  }
+  if constexpr (MODE == kModSlopes) {
+    if (threadIdx.x < kT) slope_fill_k<kF16>(reinterpret_cast<uint8_t*>(bias_all), threadIdx.x);
+    fence_proxy_async();
   }
   __syncthreads();
   // Query tiles [it_lo, it_hi) hold every row that sees one of these keys.
@@ -415,8 +492,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; it < n_it; ++it) {
         const int s = it % C::kStages;
         const int h = hk * p.group + it / cnt;
-        const int q0 = (it_lo + it % cnt) * kT;
+        const int qt = it_lo + it % cnt, q0 = qt * kT;
         const long long rowbase = (static_cast<long long>(b) * p.H + h) * p.Nq;
+        [[maybe_unused]] float slope = 0.f, lin = 0.f;
+        [[maybe_unused]] int side = 0;
+        if constexpr (MODE == kModSlopes) {
+          slope = p.slopes[h];
+          if (slope_linear(slope, p.scale))
+            side = slope_side(k0, q0 + p.q_offset, plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv).left);
+          lin = slope * kModLog2e * static_cast<float>(side);  // what is left: lin (k0 - position)
+        }
         // per-query values, read before the wait for the stage
         float l2[kT / 32], dd[kT / 32];
         int2 see[kT / 32];
@@ -425,10 +510,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int q = q0 + lane + 32 * r;
           l2[r] = -INFINITY;
           dd[r] = 0.f;
-          see[r] = plan_row(p.plan, b, p.Nq, q, p.Nkv);
+          // (rows past the last see what it sees, with P = 2^-inf: lo and hi keep their order)
+          see[r] = plan_row(p.plan, b, p.Nq, min(q, p.Nq - 1), p.Nkv);
           if (q < p.Nq && see[r].x < see[r].y) {
             const float L = p.LSE[rowbase + q];
             l2[r] = (L == -INFINITY) ? -INFINITY : -(L * kModLog2e);
+            if constexpr (MODE == kModSlopes) l2[r] = fmaf(lin, static_cast<float>(k0 - (q + p.q_offset)), l2[r]);
             dd[r] = -p.D[rowbase + q];
           }
         }
@@ -462,6 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           slo[x] = see[r].x;
           shi[x] = see[r].y;
         }
+        if constexpr (MODE == kModSlopes) {
+          if (lane < 8)
+            slope_fill_q<kF16>(reinterpret_cast<uint8_t*>(bias_all) + kSlopeKBytes + s * kSlopeQBytes, lane,
+                               slope, p.scale);
+          if (lane == 0) bars->side[s] = side;
+          fence_proxy_async();
+        }
         __syncwarp();
         if (lane == 0) {
 #pragma unroll
@@ -488,6 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         const uint32_t sq = smem_u32(ring), sdo = sq + C::kTileBytes;
         mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(sq, 16, 1024));
+        if constexpr (MODE == kModSlopes)
+          add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeKBytes, smem_u32(bias_all), bars->side[0]);
         mma_commit<true>(&bars->s_full[0]);
         mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(sdo, 16, 1024));
         mma_commit<true>(&bars->dp_full);
@@ -507,6 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after_sync();
           mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(nq, 16, 1024));
+          if constexpr (MODE == kModSlopes)
+            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeKBytes + s1 * kSlopeQBytes,
+                                   smem_u32(bias_all), bars->side[s1]);
           mma_commit<true>(&bars->s_full[0]);
         }
         ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
@@ -568,34 +667,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int d0 = kabs - p0;  // distance to the tile's first query
       auto vis = [&](int col) { return lo[col] <= kabs && kabs < hi[col]; };
       auto l2of4 = [&](int col) { return l2[col >> 2]; };
-      auto dist = [&](int col) { return static_cast<float>(d0 - col); };
-      const float* bt = nullptr;
-      float far = 0.f;
-      int side = 0;
-      if constexpr (mode_rel(MODE)) {
-        side = far_side(k0, p0, p.rel.range);
-        far = side < 0 ? bias_all[0] : bias_all[rel_entries(p.rel.range) - 1];
-        bt = bias_all + (d0 + p.rel.range + kRelPad);
+      // The group's columns for this warp's rows: all visible, none, or some.
+      // lo and hi do not fall from one query to the next that sees a key, so
+      // the first and last column decide, in tiles where every query does.
+      bool none = false, full = pt.lo_max <= k0 && pt.hi_min >= k0 + kT;
+      if (!full && pt.hi_min > 0) {
+        full = __all_sync(0xffffffffu, lo[c0 + 63] <= kabs && kabs < hi[c0]);
+        none = __all_sync(0xffffffffu, kabs < lo[c0] || kabs >= hi[c0 + 63]);
       }
       float pr[64];
-      // Every key of the tile visible to every query: no per-entry mask.
-      // (Uniform over the CTA.)
-      const bool full = pt.lo_max <= k0 && pt.hi_min >= k0 + kT;
       auto part = [&](auto mask) {
         constexpr bool kMask = decltype(mask)::value;
         if constexpr (mode_rel(MODE)) {
+          // distances of the warp's 32 keys to the group's 64 queries
+          const int first = k0 + 32 * (warp & 3) - p0 - c0 - 63, R = p.rel.range;
+          const int side = far_side(first, first + 94, R);
           if (side != 0) {
-            p_part<kF16, MODE, true, kMask>(lane_base, c0, p, slope2, vis, l2of4, dist,
-                                            [&](int) { return far; }, pr);
-            return;
+            const float far = bias_all[side < 0 ? 0 : rel_entries(R) - 1];
+            p_part<kF16, MODE, true, kMask, true>(lane_base, c0, p, vis, l2of4, [&](int) { return far; }, pr);
+          } else {
+            const float* bt = bias_all + (d0 + R + kRelPad);
+            p_part<kF16, MODE, true, kMask, true>(lane_base, c0, p, vis, l2of4,
+                                                  [&](int col) { return bt[-col]; }, pr);
           }
+        } else if (mode_slopes(MODE) && (MODE == kModCapSlopes || bars->side[s] == 0)) {
+          const float f0 = static_cast<float>(d0);
+          p_part<kF16, MODE, true, kMask, true>(
+              lane_base, c0, p, vis, l2of4,
+              [&](int col) { return -slope2 * fabsf(f0 - static_cast<float>(col)); }, pr);
+        } else {
+          p_part<kF16, MODE, true, kMask, false>(lane_base, c0, p, vis, l2of4, [](int) { return 0.f; }, pr);
         }
-        p_part<kF16, MODE, true, kMask>(lane_base, c0, p, slope2, vis, l2of4, dist,
-                                        [&](int col) { return bt[-col]; }, pr);
       };
       bool waited = false;
       if (full) {
         part(std::false_type{});
+      } else if (none) {
+        p_none<true>(lane_base, c0, pr);
       } else {
         part(std::true_type{});
         if (pt.hi_min == 0) {
@@ -642,13 +750,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       has_acc = ok;
     }
     if (ok) {
-      const bool store = kabs < p.Nkv;
-      if (c0 == 0)
-        write_row<HD, kF16>(p.dV + b * p.dv_s[0] + hk * p.dv_s[1] + kabs * p.dv_s[2],
-                            lane_base + C::kColAcc0, has_acc, store, 1.f);
-      else
-        write_row<HD, kF16>(p.dK + b * p.dk_s[0] + hk * p.dk_s[1] + kabs * p.dk_s[2],
-                            lane_base + C::kColAcc1, has_acc, store, p.scale);
+      // over V and K, whose last readers are done
+      const int w = warp >> 2;
+      uint8_t* out = w == 0 ? sV : sK;
+      stage_out<HD, kF16>(out, row, 0, lane_base + (w == 0 ? C::kColAcc0 : C::kColAcc1), has_acc,
+                          w == 0 ? 1.f : p.scale);
+      fence_proxy_async();
+      mbar_arrive(&bars->staged[w]);
+      if ((warp & 3) == 0) {
+        ok = mbar_wait(&bars->staged[w], 0, wc, kSiteEpi);
+        if (ok && lane == 0) {
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb)
+            tma_store_4d(w == 0 ? &tmdV : &tmdK, out + cb * kT * 128, cb * 64, k0, hk, b);
+          tma_store_drain();
+        }
+        __syncwarp();
+      }
     }
   }
 
@@ -670,18 +788,20 @@ template <int HD, bool kF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
-              const Params p) {
+              const __grid_constant__ CUtensorMap tmdQ, const Params p) {
   using C = Cfg<HD, MODE>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // see fwd_mod_kernel
+    if (threadIdx.x == 0) atomicExch(p.status, 3u /* OSATTN_ERR_CUDA */);
+    return;
+  }
   uint8_t* sQ = smem;
   uint8_t* sdO = smem + C::kTileBytes;
   uint8_t* kring = smem + 2 * C::kTileBytes;
   uint8_t* vring = kring + C::kKSlots * C::kTileBytes;
-  float* bias = reinterpret_cast<float*>(smem + C::kDqRel);
-  float* dsum = reinterpret_cast<float*>(smem + C::kDqRel + C::kRelBytes);  // sums of dY by distance
-  float* strips = reinterpret_cast<float*>(smem + C::kDqRel + 2 * C::kRelBytes);  // [2][8][96]
+  float* bias = reinterpret_cast<float*>(smem + C::kDqTable);  // or the slope operands
+  float* dsum = reinterpret_cast<float*>(smem + C::kDqSums);   // sums of dY by distance
+  float* strips = reinterpret_cast<float*>(smem + C::kDqSums + C::kSumBytes);  // [2][8][96]
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kDqRegion);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -709,6 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->mma_drain, 1);
     mbar_init(&bars->d_full, 256);
     mbar_init(&bars->elem, 256);
+    mbar_init(&bars->staged[0], 256);
     bars->abort_flag = 0;
     fence_barrier_init();
   }
@@ -718,7 +839,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if constexpr (mode_rel(MODE)) {
     rel_fill<kF16>(bias, p.rel, p.H, h);
-    for (int x = threadIdx.x; x < rel_entries(p.rel.range); x += kThreads) dsum[x] = 0.f;
+    for (int x = threadIdx.x; x < sum_entries(p.rel.range); x += kThreads) dsum[x] = 0.f;
+  }
+  [[maybe_unused]] bool linear = false;
+  if constexpr (MODE == kModSlopes) {
+    linear = slope_linear(p.slopes[h], p.scale);
+    uint8_t* at = reinterpret_cast<uint8_t*>(bias);
+    if (threadIdx.x < kT / 2) slope_fill_k<kF16>(at, threadIdx.x);
+    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeKBytes / 2, threadIdx.x, p.slopes[h], p.scale);
+    fence_proxy_async();
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -762,11 +891,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n_kt > 0) {
       const uint64_t qA = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dA = sdesc_sw128(smem_u32(sdO), 16, 1024);
+      [[maybe_unused]] auto slope_step = [&](uint32_t s_col, int j) {
+        add_slope<kF16>(s_col, smem_u32(bias) + kSlopeKBytes / 2, smem_u32(bias),
+                        linear ? slope_side((kt0 + j) * kT, q0 + p.q_offset, pt.left) : 0);
+      };
       bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);
       if (ok) ok = warp_wait(&bars->full[0], 0, wc, kSiteMma);
       if (ok) {
         tc_fence_after_sync();
         mma_abt<128, HD, kF16, true>(tmem, qA, sdesc_sw128(smem_u32(kring), 16, 1024));
+        if constexpr (MODE == kModSlopes) slope_step(tmem, 0);
         mma_commit<true>(&bars->s_full[0]);
         mma_abt<128, HD, kF16, true>(tmem + kDqColDP, dA, sdesc_sw128(smem_u32(vring), 16, 1024));
         mma_commit<true>(&bars->dp_full);
@@ -783,6 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after_sync();
           mma_abt<128, HD, kF16, true>(tmem + 128 * ((j + 1) & 1), qA, sdesc_sw128(nk, 16, 1024));
+          if constexpr (MODE == kModSlopes) slope_step(tmem + 128 * ((j + 1) & 1), j + 1);
           mma_commit<true>(&bars->s_full[(j + 1) & 1]);
         }
         ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(j) & 1u, wc, kSiteMma);
@@ -828,7 +963,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int v = 0; v < kNv; ++v) ov[v] = orow[v];
     }
-    const float4 l2v = make_float4(l2, l2, l2, l2);
     float4 dv4 = make_float4(0.f, 0.f, 0.f, 0.f);  // -D
     if (n_kt == 0 && g == 0 && in) p.D[rix] = 0.f;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -842,34 +976,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after_sync();
       const int kx = (kt0 + j) * kT;
       const int d0 = kx - (q + p.q_offset);
-      auto vis = [&](int col) { return kx + col >= see.x && kx + col < see.y; };
-      auto l2of4 = [&](int) { return l2v; };
-      auto dist = [&](int col) { return static_cast<float>(d0 + col); };
-      const float* bt = nullptr;
-      float far = 0.f;
-      int side = 0;
-      if constexpr (mode_rel(MODE)) {
-        side = far_side(kx, p0, p.rel.range);
-        far = side < 0 ? bias[0] : bias[rel_entries(p.rel.range) - 1];
-        bt = bias + (d0 + p.rel.range + kRelPad);
+      // the row's visible keys of the group, as bits
+      const int from = see.x - kx - c0, to = see.y - kx - c0;
+      const bool full = __all_sync(0xffffffffu, from <= 0 && to >= 64);
+      const bool none = __all_sync(0xffffffffu, max(from, 0) >= min(to, 64));
+      const uint32_t bits[2] = {bit_range(from, to), bit_range(from - 32, to - 32)};
+      auto vis = [&](int col) { return (bits[(col - c0) >> 5] & (1u << ((col - c0) & 31))) != 0u; };
+      float nl = l2;
+      [[maybe_unused]] int sside = 0;
+      if constexpr (MODE == kModSlopes) {
+        sside = linear ? slope_side(kx, p0, pt.left) : 0;
+        nl = fmaf(slope2 * static_cast<float>(sside), static_cast<float>(d0 + c0), nl);
       }
-      const bool full = pt.lo_max <= kx && pt.hi_min >= kx + kT;
+      [[maybe_unused]] int side = 0;  // learned bias: distances of the warp's 32 queries to the group's 64 keys
+      if constexpr (mode_rel(MODE)) {
+        const int first = kx + c0 - p0 - 32 * (warp & 3) - 31;
+        side = far_side(first, first + 94, p.rel.range);
+        if (side != 0) nl += bias[side < 0 ? 0 : rel_entries(p.rel.range) - 1];
+      }
+      const float4 l2v = make_float4(nl, nl, nl, nl);
+      auto l2of4 = [&](int) { return l2v; };
       const uint32_t s_addr = lane_base + 128 * (j & 1);
       float pr[64];
       auto part = [&](auto mask) {
         constexpr bool kMask = decltype(mask)::value;
         if constexpr (mode_rel(MODE)) {
           if (side != 0) {
-            p_part<kF16, MODE, false, kMask>(s_addr, c0, p, slope2, vis, l2of4, dist,
-                                             [&](int) { return far; }, pr);
-            return;
+            p_part<kF16, MODE, false, kMask, false>(s_addr, c0, p, vis, l2of4, [](int) { return 0.f; }, pr);
+          } else {
+            const float* bt = bias + (d0 + p.rel.range + kRelPad);
+            p_part<kF16, MODE, false, kMask, true>(s_addr, c0, p, vis, l2of4,
+                                                   [&](int col) { return bt[col]; }, pr);
           }
+        } else if (mode_slopes(MODE) && sside == 0) {
+          const float f0 = static_cast<float>(d0);
+          p_part<kF16, MODE, false, kMask, true>(
+              s_addr, c0, p, vis, l2of4,
+              [&](int col) { return -slope2 * fabsf(f0 + static_cast<float>(col)); }, pr);
+        } else {
+          p_part<kF16, MODE, false, kMask, false>(s_addr, c0, p, vis, l2of4, [](int) { return 0.f; }, pr);
         }
-        p_part<kF16, MODE, false, kMask>(s_addr, c0, p, slope2, vis, l2of4, dist,
-                                         [&](int col) { return bt[col]; }, pr);
       };
       if (full)
         part(std::false_type{});
+      else if (none)
+        p_none<false>(s_addr, c0, pr);
       else
         part(std::true_type{});
       if (kx < pt.lo || min(kx + kT, p.Nkv) > pt.hi) {
@@ -925,28 +1076,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before_sync();
       mbar_arrive(&bars->ds_full);
       if constexpr (mode_rel(MODE)) {
-        if (side != 0) {
+        // A block of 32 queries and 64 keys beyond the range goes to one
+        // distance.  Otherwise sums along its diagonals: a running sum moves
+        // one lane up with every column, so that it stays on one distance;
+        // lane 31 stores the diagonals that end there.  Strip entry u holds
+        // distance (c0 - 32 quarter) + u - 31 within the tile.
+        const bool tile_far = far_side(kx - p0 - 127, kx - p0 + 127, p.rel.range) != 0;
+        if (side != 0 && !none) {
           float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int x = 0; x < 64; ++x) a[x & 3] += pr[x];
           const float sum = (a[0] + a[1]) + (a[2] + a[3]);
           if (side < 0) far_lo += sum;
           else far_hi += sum;
-        } else {
-          // Sums along the diagonals of the warp's 32 x 64 block: a running
-          // sum moves one lane up with every column, so that it stays on one
-          // distance; lane 31 stores the diagonals that end there.  Strip
-          // entry u holds distance (c0 - 32 quarter) + u - 31 within the tile.
+        }
+        if (!tile_far) {
           const int buf = sync_phase & 1;
           float* strip = strips + buf * 8 * 96 + warp * 96;
-          float acc = 0.f;
+          if (side != 0 || none) {
 #pragma unroll
-          for (int x = 0; x < 64; ++x) {
-            acc = __shfl_up_sync(0xffffffffu, acc, 1);
-            acc = (lane == 0 ? 0.f : acc) + pr[x];
-            if (lane == 31) strip[x] = acc;
+            for (int x = 0; x < 3; ++x) strip[32 * x + lane] = 0.f;
+          } else {
+            float acc = 0.f;
+#pragma unroll
+            for (int x = 0; x < 64; ++x) {
+              acc = __shfl_up_sync(0xffffffffu, acc, 1);
+              acc = (lane == 0 ? 0.f : acc) + pr[x];
+              if (lane == 31) strip[x] = acc;
+            }
+            if (lane < 31) strip[94 - lane] = acc;
           }
-          if (lane < 31) strip[94 - lane] = acc;
           if (!(ok = elem_sync(bars, sync_phase, wc))) break;
           // thread u adds distance u - 127 of the tile to the sums
           const int u = threadIdx.x;
@@ -957,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int at = (u - 127) - 64 * (w >> 2) + 32 * (w & 3) + 31;
               if (at >= 0 && at < 95) add += strips[buf * 8 * 96 + w * 96 + at];
             }
-            dsum[kx - p0 + (u - 127) + p.rel.range + kRelPad] += add;
+            dsum[kx - p0 + (u - 127) + p.rel.range + kSumPad] += add;
           }
         }
       }
@@ -969,9 +1128,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) tc_fence_after_sync();
       has_acc = ok;
     }
-    if (ok)
-      write_row<HD / 2, kF16>(p.dQ + b * p.dq_s[0] + h * p.dq_s[1] + q * p.dq_s[2] + c0 * HD / 128,
-                              lane_base + kDqColAcc + c0 * HD / 128, has_acc, in, p.scale);
+    if (ok) {
+      // over Q, whose last reader is done
+      stage_out<HD / 2, kF16>(sQ, row, c0 * HD / 128, lane_base + kDqColAcc + c0 * HD / 128, has_acc, p.scale);
+      fence_proxy_async();
+      mbar_arrive(&bars->staged[0]);
+      if (warp == 0) {
+        ok = mbar_wait(&bars->staged[0], 0, wc, kSiteEpi);
+        if (ok && lane == 0) {
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb) tma_store_4d(&tmdQ, sQ + cb * kT * 128, cb * 64, q0, h, b);
+          tma_store_drain();
+        }
+        __syncwarp();
+      }
+    }
     if constexpr (mode_rel(MODE)) {
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) {
@@ -999,11 +1170,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int R = p.rel.range;
     float* out = p.rel_part + (static_cast<long long>(bh) * p.num_tiles + qt) * (2 * R + 1);
     for (int x = threadIdx.x; x < 2 * R + 1; x += kThreads)
-      if (x != 0 && x != 2 * R) out[x] = dsum[x + kRelPad];
+      if (x != 0 && x != 2 * R) out[x] = dsum[x + kSumPad];
     if (warp < 2) {  // distance -R (warp 0), R (warp 1)
-      const float* pad = dsum + (warp == 0 ? 0 : 2 * R + kRelPad);
+      const float* pad = dsum + (warp == 0 ? 0 : 2 * R + kSumPad);
       float v = 0.f;
-      for (int x = lane; x <= kRelPad; x += 32) v += pad[x];
+      for (int x = lane; x <= kSumPad; x += 32) v += pad[x];
       if (lane < 8) v += bars->far_part[warp][lane];
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -1012,34 +1183,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The table's gradient: one block per head sums the partials of its query
-// tiles over batch entries and tiles in a fixed order, then each warp its
-// buckets over the distances.  Bound by latency at usual ranges (2 R + 1 = 257
-// floats a tile).
+// The table's gradient: one block per head.  Each warp sums a share of the
+// query tiles' partials over batch entries and tiles, lanes along the
+// distances; the warps' sums are added in order, then each warp sums the
+// distances of its buckets.  Bound by latency: 2 R + 1 floats a tile.
 template <bool kF16>
 __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restrict__ part,
                                                           uint16_t* __restrict__ out, RelArgs rel, int B,
                                                           int H, int q_tiles) {
+  constexpr int kX = 4;  // blocks of 32 distances a warp takes at a time
+  __shared__ float warp_sum[32][32 * kX];
   __shared__ float sums[2 * kMaxRelRange + 1];
   __shared__ int map[2 * kMaxRelRange + 1];
-  const int h = blockIdx.x, n = 2 * rel.range + 1;
-  for (int x = threadIdx.x; x < n; x += blockDim.x) {
-    map[x] = rel.map[x];
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int b = 0; b < B; ++b) {
-      const float* src = part + (static_cast<long long>(b) * H + h) * q_tiles * n + x;
-      int t = 0;
-      for (; t + 4 <= q_tiles; t += 4) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) a[u] += src[static_cast<long long>(t + u) * n];
-      }
-      for (; t < q_tiles; ++t) a[0] += src[static_cast<long long>(t) * n];
-    }
-    sums[x] = (a[0] + a[1]) + (a[2] + a[3]);
-  }
-  __syncthreads();
+  const int h = blockIdx.x, n = 2 * rel.range + 1, rows = B * q_tiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int k = warp; k < rel.num; k += blockDim.x / 32) {
+  for (int x = threadIdx.x; x < n; x += 1024) map[x] = rel.map[x];
+  for (int x0 = 0; x0 < n; x0 += 32 * kX) {
+    float a[kX];
+#pragma unroll
+    for (int u = 0; u < kX; ++u) a[u] = 0.f;
+#pragma unroll 4
+    for (int r = warp; r < rows; r += 32) {
+      const int b = r / q_tiles, t = r - b * q_tiles;
+      const float* src = part + ((static_cast<long long>(b) * H + h) * q_tiles + t) * n + x0 + lane;
+#pragma unroll
+      for (int u = 0; u < kX; ++u)
+        if (x0 + lane + 32 * u < n) a[u] += src[32 * u];
+    }
+#pragma unroll
+    for (int u = 0; u < kX; ++u) warp_sum[warp][32 * u + lane] = a[u];
+    __syncthreads();
+    if (threadIdx.x < 32 * kX && x0 + threadIdx.x < n) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 32; ++w) v += warp_sum[w][threadIdx.x];
+      sums[x0 + threadIdx.x] = v;
+    }
+    __syncthreads();
+  }
+  for (int k = warp; k < rel.num; k += 32) {
     float v = 0.f;
     for (int x = lane; x < n; x += 32) v += map[x] == k ? sums[x] : 0.f;
 #pragma unroll
@@ -1073,13 +1255,12 @@ cudaError_t prepare() {
 
 template <int HD, bool kF16, int MODE>
 cudaError_t launch_mode(const ModArgs& a, const Params& pq, const Params& pk, unsigned gq, unsigned gk,
-                        const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                        const CUtensorMap& g) {
+                        const BwdModMaps& m) {
   // dQ first: it writes D, which the dK/dV kernel reads
-  dq_kernel<HD, kF16, MODE><<<gq, kThreads, dq_smem_bytes<HD, MODE>(), a.stream>>>(q, k, v, g, pq);
+  dq_kernel<HD, kF16, MODE><<<gq, kThreads, dq_smem_bytes<HD, MODE>(), a.stream>>>(m.q, m.k, m.v, m.g, m.dq, pq);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dkdv_kernel<HD, kF16, MODE><<<gk, kThreads, dkdv_smem_bytes<HD, MODE>(), a.stream>>>(q, k, v, g, pk);
+  dkdv_kernel<HD, kF16, MODE><<<gk, kThreads, dkdv_smem_bytes<HD, MODE>(), a.stream>>>(m.q, m.k, m.v, m.g, m.dk, m.dv, pk);
   e = cudaGetLastError();
   if (e != cudaSuccess || !mode_rel(MODE)) return e;
   rel_reduce_kernel<kF16><<<a.H, 1024, 0, a.stream>>>(a.rel_part, static_cast<uint16_t*>(a.dRel), a.rel,
@@ -1088,18 +1269,9 @@ cudaError_t launch_mode(const ModArgs& a, const Params& pq, const Params& pk, un
 }
 
 template <int HD, bool kF16>
-cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                   const CUtensorMap& g) {
+cudaError_t launch(const ModArgs& a, const BwdModMaps& m) {
   Params p;
-  p.dQ = static_cast<uint16_t*>(a.dQ);
-  p.dK = static_cast<uint16_t*>(a.dK);
-  p.dV = static_cast<uint16_t*>(a.dV);
-  for (int i = 0; i < 3; ++i) {
-    p.dq_s[i] = a.dq_s[i];
-    p.dk_s[i] = a.dk_s[i];
-    p.dv_s[i] = a.dv_s[i];
-    p.o_s[i] = a.o_s[i];
-  }
+  for (int i = 0; i < 3; ++i) p.o_s[i] = a.o_s[i];
   p.LSE = a.LSE;
   p.D = a.D;
   p.O = static_cast<const uint16_t*>(a.O_in);
@@ -1114,8 +1286,7 @@ cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k,
   p.Nkv = a.Nkv;
   p.scale = a.scale;
   p.scale_log2 = a.scale * kModLog2e;
-  p.cap_c1 = a.softcap > 0.f ? 2.f * a.scale * kModLog2e / a.softcap : 0.f;
-  p.cap2 = a.softcap * kModLog2e;
+  p.cap = make_cap(a.scale, a.softcap);
   p.slopes = a.slopes;
   p.rel = a.rel;
   p.rel_part = a.rel_part;
@@ -1139,11 +1310,11 @@ cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k,
   if (gk > 0x7fffffffLL || gq > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned uq = static_cast<unsigned>(gq), uk = static_cast<unsigned>(gk);
   switch (mod_score_mode(a)) {
-    case kModCap: return launch_mode<HD, kF16, kModCap>(a, pq, pk, uq, uk, q, k, v, g);
-    case kModSlopes: return launch_mode<HD, kF16, kModSlopes>(a, pq, pk, uq, uk, q, k, v, g);
-    case kModCapSlopes: return launch_mode<HD, kF16, kModCapSlopes>(a, pq, pk, uq, uk, q, k, v, g);
-    case kModRel: return launch_mode<HD, kF16, kModRel>(a, pq, pk, uq, uk, q, k, v, g);
-    default: return launch_mode<HD, kF16, kModPlain>(a, pq, pk, uq, uk, q, k, v, g);
+    case kModCap: return launch_mode<HD, kF16, kModCap>(a, pq, pk, uq, uk, m);
+    case kModSlopes: return launch_mode<HD, kF16, kModSlopes>(a, pq, pk, uq, uk, m);
+    case kModCapSlopes: return launch_mode<HD, kF16, kModCapSlopes>(a, pq, pk, uq, uk, m);
+    case kModRel: return launch_mode<HD, kF16, kModRel>(a, pq, pk, uq, uk, m);
+    default: return launch_mode<HD, kF16, kModPlain>(a, pq, pk, uq, uk, m);
   }
 }
 

@@ -68,14 +68,16 @@ template <int HD, int MODE>
 struct Cfg {
   static constexpr int kTileBytes = BN * HD * 2;
   static constexpr int kQBytes = BM * HD * 2;
-  // The learned-bias table (10 KB) or the slope operands (12 KB) take the
-  // place of one stage (32 KB at d = 128, 16 KB at d = 64).
-  static constexpr bool kTable = mode_rel(MODE) || MODE == kModSlopes;
-  static constexpr int kStages = HD == 128 ? (kTable ? 4 : 5) : (kTable ? 11 : 12);
+  // Table of learned biases: ranges up to kSmallRel leave all five stages at d =
+  // 128; wider ones (kModRelWide) take one (32 KB; a step with four stages
+  // waits for its loads, 20 % slower).  At d = 64 the twelfth stage of 16 KB
+  // makes room for any range.
+  static constexpr int kTableBytes =
+      mode_rel(MODE) ? (rel_entries(HD == 64 || MODE == kModRelWide ? kMaxRelRange : kSmallRel) * 4 + 15) / 16 * 16
+                     : (MODE == kModSlopes ? kSlopeKBytes + kSlopeQBytes : 0);
+  static constexpr int kStages = HD == 128 ? (MODE == kModRelWide ? 4 : 5) : (mode_rel(MODE) ? 11 : 12);
   static constexpr int kIters = HD == 128 ? 4 : 8;  // > kStages / 2 + 1
   static constexpr int kTileRegion = kQTiles * kQBytes + kStages * kTileBytes;
-  static constexpr int kTableBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16
-                                                    : (MODE == kModSlopes ? kSlopeBytes : 0);
   static constexpr uint32_t kOCol0 = 256;
 };
 
@@ -91,7 +93,7 @@ struct __align__(16) Bars {
   uint64_t mma_drain;
   uint32_t tmem_base;
   int abort_flag;
-  float alpha[kQTiles][BM];
+  uint16_t alpha[kQTiles][BM];  // alpha_bits
   float rel_lo, rel_hi;  // least and greatest learned bias of the head
 };
 
@@ -170,6 +172,8 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
   }
   if constexpr (mode_rel(MODE)) {
     ts.strip_lo = bars->rel_lo;
+    ts.far_lo = bias[0];
+    ts.far_hi = bias[rel_entries(p.rel.range) - 1];
     ts.strip_close = bars->rel_hi - bars->rel_lo <= ts.kSpread;
   }
   float m = -INFINITY, l = 0.f;
@@ -198,9 +202,12 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
       const int first = k0 - p0;  // distances of the whole tile: first - 127 .. first + 127
       const bool far = first + BN - 1 <= -R || first - (BM - 1) >= R;
       ts.strip = far ? nullptr : bias + (k0 - pos + R + kRelPad);
-      ts.off = far ? bias[first <= 0 ? 0 : rel_entries(R) - 1] : 0.f;
+      ts.off = far ? (first <= 0 ? ts.far_lo : ts.far_hi) : 0.f;
+      // a chunk of this warp's 32 rows has distances x + first - 32 quarter - 31 .. + 31
+      ts.near_lo = -R - 31 - first + 32 * quarter;
+      ts.near_hi = R + 31 - first + 32 * quarter;
     }
-    ts.tile(s_addr, masked, mk, bits_of, m, l, [&](float alpha) {
+    ts.tile(s_addr, masked, mk, bits_of, m, l, [&](uint16_t alpha) {
       bars->alpha[t][row] = alpha;
       mbar_arrive(&bars->alpha_full[t]);
     });
@@ -265,7 +272,7 @@ __device__ __forceinline__ void correction_tile(Bars* bars, uint32_t lane_base, 
   ok = mbar_wait(&bars->alpha_full[t], static_cast<uint32_t>(j) & 1u, wc, kSiteAlpha);
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) return;
-  const float alpha = bars->alpha[t][row];
+  const float alpha = alpha_of(bars->alpha[t][row]);
   if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
     tc_fence_after_sync();
     const uint64_t a2 = f2_pack(alpha, alpha);
@@ -403,8 +410,8 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
     if (slope_tiles == 0) return;
     const int side = slope_side((kt0 + j) * BN, pt, left);
     if (side == 0) return;
-    mma_ss_k<1, true>(s_col, sdesc_plain(slope_tiles + (side < 0 ? kSlopeTileBytes : 0)),
-                      sdesc_plain(slope_tiles + 2 * kSlopeTileBytes), idesc_f16_f32(128, 128, 0, kF16));
+    mma_ss_k<1, true>(s_col, slope_q_desc(slope_tiles + kSlopeKBytes), slope_k_desc(slope_tiles),
+                      idesc_f16_f32(128, 128, 0, kF16) | (side < 0 ? kIdescNegA : 0u));
   };
   bool ok = true;
 
@@ -527,8 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if constexpr (mode_rel(MODE)) rel_fill<kF16>(bias, p.rel, p.H, h);
   if constexpr (MODE == kModSlopes) {
-    if (threadIdx.x < BN)
-      slope_fill_row<kF16>(reinterpret_cast<uint8_t*>(bias), threadIdx.x, p.slopes[h], p.scale);
+    uint8_t* at = reinterpret_cast<uint8_t*>(bias);
+    if (threadIdx.x < BN) slope_fill_k<kF16>(at, threadIdx.x);
+    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeKBytes, threadIdx.x, p.slopes[h], p.scale);
     fence_proxy_async();
   }
   tc_fence_before_sync();
@@ -611,6 +619,8 @@ cudaError_t prepare() {
   if ((e = set_attrs<HD, kF16, kModCap>()) != cudaSuccess) return e;
   if ((e = set_attrs<HD, kF16, kModSlopes>()) != cudaSuccess) return e;
   if ((e = set_attrs<HD, kF16, kModCapSlopes>()) != cudaSuccess) return e;
+  if constexpr (HD == 128)
+    if ((e = set_attrs<HD, kF16, kModRelWide>()) != cudaSuccess) return e;
   return set_attrs<HD, kF16, kModRel>();
 }
 
@@ -658,7 +668,10 @@ cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k,
     case kModCap: return launch_mode<HD, kF16, kModCap>(g, a.stream, q, k, v, o, p);
     case kModSlopes: return launch_mode<HD, kF16, kModSlopes>(g, a.stream, q, k, v, o, p);
     case kModCapSlopes: return launch_mode<HD, kF16, kModCapSlopes>(g, a.stream, q, k, v, o, p);
-    case kModRel: return launch_mode<HD, kF16, kModRel>(g, a.stream, q, k, v, o, p);
+    case kModRel:
+      if constexpr (HD == 128)
+        if (a.rel.range > kSmallRel) return launch_mode<HD, kF16, kModRelWide>(g, a.stream, q, k, v, o, p);
+      return launch_mode<HD, kF16, kModRel>(g, a.stream, q, k, v, o, p);
     default: return launch_mode<HD, kF16, kModPlain>(g, a.stream, q, k, v, o, p);
   }
 }

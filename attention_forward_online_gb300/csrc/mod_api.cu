@@ -24,8 +24,7 @@ namespace bwdmod {
 template <int HD, bool kF16>
 cudaError_t prepare();
 template <int HD, bool kF16>
-cudaError_t launch(const ModArgs&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                   const CUtensorMap&);
+cudaError_t launch(const ModArgs&, const BwdModMaps&);
 }  // namespace bwdmod
 
 int mod_score_mode(const ModArgs& a) {
@@ -226,23 +225,17 @@ int osattn_bwd_mod(const void* Q, const void* K, const void* V, const void* O, c
   common_args(&a, B, H, Hkv, Nq, Nkv, d, scale, score, plan, dtype, stream, dev);
   a.O_in = O;
   a.LSE = const_cast<float*>(LSE);
-  a.dQ = dQ;
-  a.dK = dK;
-  a.dV = dV;
   a.dRel = dRel;
-  for (int i = 0; i < 3; ++i) {
-    a.o_s[i] = st[3][i];
-    a.dq_s[i] = st[5][i];
-    a.dk_s[i] = st[6][i];
-    a.dv_s[i] = st[7][i];
-  }
+  for (int i = 0; i < 3; ++i) a.o_s[i] = st[3][i];
   a.D = static_cast<float*>(workspace);
   a.rel_part = a.D + static_cast<size_t>(B) * H * Nq;
-  CUtensorMap tq, tk, tv, tg;
-  if (api_encode_map(&tq, Q, a.fp16, d, Nq, H, B, st[0], kBoxRows) != OSATTN_OK ||
-      api_encode_map(&tk, K, a.fp16, d, Nkv, Hkv, B, st[1], kBoxRows) != OSATTN_OK ||
-      api_encode_map(&tv, V, a.fp16, d, Nkv, Hkv, B, st[2], kBoxRows) != OSATTN_OK ||
-      api_encode_map(&tg, dO, a.fp16, d, Nq, H, B, st[4], kBoxRows) != OSATTN_OK)
+  BwdModMaps maps;
+  auto encode = [&](CUtensorMap* map, const void* base, int i, bool kv) {
+    return api_encode_map(map, base, a.fp16, d, kv ? Nkv : Nq, kv ? Hkv : H, B, st[i], kBoxRows) == OSATTN_OK;
+  };
+  if (!encode(&maps.q, Q, 0, false) || !encode(&maps.k, K, 1, true) || !encode(&maps.v, V, 2, true) ||
+      !encode(&maps.g, dO, 4, false) || !encode(&maps.dq, dQ, 5, false) || !encode(&maps.dk, dK, 6, true) ||
+      !encode(&maps.dv, dV, 7, true))
     return OSATTN_ERR_CUDA;
   const int slot = (d == 128 ? 2 : 0) + a.fp16;
   cudaError_t (*const prep[4])() = {bwdmod::prepare<64, false>, bwdmod::prepare<64, true>,
@@ -251,10 +244,10 @@ int osattn_bwd_mod(const void* Q, const void* K, const void* V, const void* O, c
   if (rc != OSATTN_OK) return rc;
   cudaError_t e;
   switch (slot) {
-    case 0: e = bwdmod::launch<64, false>(a, tq, tk, tv, tg); break;
-    case 1: e = bwdmod::launch<64, true>(a, tq, tk, tv, tg); break;
-    case 2: e = bwdmod::launch<128, false>(a, tq, tk, tv, tg); break;
-    default: e = bwdmod::launch<128, true>(a, tq, tk, tv, tg); break;
+    case 0: e = bwdmod::launch<64, false>(a, maps); break;
+    case 1: e = bwdmod::launch<64, true>(a, maps); break;
+    case 2: e = bwdmod::launch<128, false>(a, maps); break;
+    default: e = bwdmod::launch<128, true>(a, maps); break;
   }
   return e == cudaSuccess ? OSATTN_OK : OSATTN_ERR_CUDA;
 }

@@ -24,10 +24,18 @@ constexpr float kModLog2e = 1.4426950408889634f;
 // each pair that a call can ask for; a cap together with a learned bias is
 // refused by the entry points (its backward pass would have to hold two
 // factors per score in registers).
-enum ScoreMode : int { kModPlain = 0, kModCap = 1, kModSlopes = 2, kModCapSlopes = 3, kModRel = 4 };
+enum ScoreMode : int {
+  kModPlain = 0,
+  kModCap = 1,
+  kModSlopes = 2,
+  kModCapSlopes = 3,
+  kModRel = 4,
+  kModRelWide = 5  // forward at d = 128: ranges above kSmallRel
+};
+constexpr int kSmallRel = 128;
 __host__ __device__ constexpr bool mode_cap(int m) { return m == kModCap || m == kModCapSlopes; }
 __host__ __device__ constexpr bool mode_slopes(int m) { return m == kModSlopes || m == kModCapSlopes; }
-__host__ __device__ constexpr bool mode_rel(int m) { return m == kModRel; }
+__host__ __device__ constexpr bool mode_rel(int m) { return m == kModRel || m == kModRelWide; }
 
 // Mask plan: per 128-row query tile {smallest lo, largest hi, largest lo,
 // smallest hi} (the first two over the rows that see a key, 0 and 0 if none
@@ -80,23 +88,26 @@ __device__ __forceinline__ float cap_r(float s, float c1) { return rcp_approx(1.
 // 3: coefficients fitted here for the least relative error on that range
 // (2^-23.3, reweighted least squares on Chebyshev points).  k[n] carries
 // cap2 (scale / cap)^(2 n + 1), so that the polynomial is in the raw score:
-// cap2 tanh = s (k0 + s^2 (k1 + ...)).  s_max = 0.4 cap / scale, or -1 where
-// scale / cap is not in [2^-12, 2^12] (products could leave fp32's range):
+// cap2 tanh = s (k0 + s^2 (k1 + ...)).  s_max = 0.4 cap / |scale|, or -1 where
+// |scale| / cap is not in [2^-12, 2^12] (products could leave fp32's range):
 // then the other form is used.
 struct CapArgs {
   float c1, cap2, s_max;  // c1 = 2 scale log2(e) / cap
+  float inv2;             // 1 / cap2^2
   float k[4];
 };
 inline CapArgs make_cap(float scale, float softcap) {
   CapArgs c{};
   if (!(softcap > 0.f)) return c;
-  const double a = static_cast<double>(scale) / softcap;  // scale >= 0
+  const double a = static_cast<double>(scale) / softcap;  // the tanh is odd: either sign
   const double cap2 = static_cast<double>(softcap) * 1.4426950408889634;
   c.c1 = static_cast<float>(2.0 * a * 1.4426950408889634);
   c.cap2 = static_cast<float>(cap2);
+  c.inv2 = static_cast<float>(1.0 / (cap2 * cap2));
   const double t[4] = {0.9999999019, -0.3333136247, 0.1327097680, -0.0475536037};
-  const bool ok = a >= 1.0 / 4096 && a <= 4096.0;
-  c.s_max = ok ? static_cast<float>(0.4 / a) : -1.f;
+  const double size = a < 0 ? -a : a;
+  const bool ok = size >= 1.0 / 4096 && size <= 4096.0;
+  c.s_max = ok ? static_cast<float>(0.4 / size) : -1.f;
   double pw = a;
   for (int n = 0; n < 4; ++n, pw *= a * a) c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;
   return c;
@@ -139,20 +150,27 @@ __device__ __forceinline__ void mma_abt_id(uint32_t d_tmem, uint64_t a_desc, uin
 // step), e < 128 is exact, and the products are summed in fp32 as s is.
 // Tiles with keys on both sides of a row that sees them get the bias score
 // by score instead.
-// The operands: 128 rows of 16 elements as 8 x 16-byte core matrices, the two
-// of a row group 128 bytes apart, row groups 256 bytes apart, no swizzle.
-constexpr int kSlopeTileBytes = 128 * 32;
-constexpr int kSlopeBytes = 3 * kSlopeTileBytes;  // + pieces, - pieces, e
-constexpr float kSlopeMax = 16384.f;              // |slope / scale| beyond: score by score
+// The operands are made of 8 x 16-byte core matrices without swizzle.  All
+// query rows are alike: one core matrix of (hi, mid, lo, 0 ...) rows and one of
+// zeros for the other 8 inner elements, with a stride of 0 between row groups.
+// Key rows (e, e, e, 0 ...): 16 core matrices, read again for the other 8
+// inner elements (stride 0), where they meet the zeros.
+constexpr int kSlopeQBytes = 256;
+constexpr int kSlopeKBytes = 128 * 16;
+constexpr float kSlopeMax = 16384.f;  // |slope / scale| beyond: score by score
 
-__device__ __forceinline__ uint64_t sdesc_plain(uint32_t smem_addr) {
+// Shared-memory descriptor without swizzle; lbo: to the next 8 inner elements,
+// sbo: to the next 8 rows.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(128u >> 4) << 16;  // next core matrix along the inner axis
-  d |= static_cast<uint64_t>(256u >> 4) << 32;  // next 8 rows
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(sbo >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   return d;
 }
+__device__ __forceinline__ uint64_t slope_q_desc(uint32_t at) { return sdesc_plain(at, 128, 0); }
+__device__ __forceinline__ uint64_t slope_k_desc(uint32_t at) { return sdesc_plain(at, 0, 128); }
 
 __device__ __forceinline__ bool slope_linear(float slope, float scale) {
   return fabsf(slope / scale) <= kSlopeMax;
@@ -169,27 +187,26 @@ __device__ __forceinline__ float from_16(uint16_t w) {
   else return __bfloat162float(__ushort_as_bfloat16(w));
 }
 
-// Writes row `row` of the three operand tiles; the caller orders the writes
-// before the MMAs (fence_proxy_async and a barrier).
+// Write the operands with 8 threads (x: 0 .. 7) and 128 threads (x: 0 .. 127);
+// the caller orders the writes before the MMAs (fence_proxy_async, then a
+// barrier).
 template <bool kF16>
-__device__ __forceinline__ void slope_fill_row(uint8_t* tiles, int row, float slope, float scale) {
-  const float q = slope_linear(slope, scale) ? slope / scale : 0.f;
+__device__ __forceinline__ void slope_fill_q(uint8_t* at, int x, float slope, float scale) {
   uint16_t w[3];
-  float rest = q;
+  float rest = slope_linear(slope, scale) ? slope / scale : 0.f;
 #pragma unroll
-  for (int x = 0; x < 3; ++x) {
-    w[x] = to_16<kF16>(rest);
-    rest -= from_16<kF16>(w[x]);
+  for (int i = 0; i < 3; ++i) {
+    w[i] = to_16<kF16>(rest);
+    rest -= from_16<kF16>(w[i]);
   }
-  const uint32_t e = to_16<kF16>(static_cast<float>(row));
-  uint8_t* at = tiles + (row / 8) * 256 + (row % 8) * 16;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  *reinterpret_cast<uint4*>(at) = make_uint4(w[0] | (static_cast<uint32_t>(w[1]) << 16), w[2], 0u, 0u);
-  *reinterpret_cast<uint4*>(at + kSlopeTileBytes) =
-      make_uint4((w[0] ^ 0x8000u) | ((static_cast<uint32_t>(w[1]) ^ 0x8000u) << 16), w[2] ^ 0x8000u, 0u, 0u);
-  *reinterpret_cast<uint4*>(at + 2 * kSlopeTileBytes) = make_uint4(e | (e << 16), e, 0u, 0u);
-#pragma unroll
-  for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(at + t * kSlopeTileBytes + 128) = zero;
+  uint4* q = reinterpret_cast<uint4*>(at) + x;
+  q[0] = make_uint4(w[0] | (static_cast<uint32_t>(w[1]) << 16), w[2], 0u, 0u);
+  q[8] = make_uint4(0u, 0u, 0u, 0u);
+}
+template <bool kF16>
+__device__ __forceinline__ void slope_fill_k(uint8_t* at, int x) {
+  const uint32_t e = to_16<kF16>(static_cast<float>(x));
+  reinterpret_cast<uint4*>(at)[x] = make_uint4(e | (e << 16), e, 0u, 0u);
 }
 
 // Which side of a tile's rows its keys k0 .. k0 + 127 lie on: 1 before or at
@@ -201,9 +218,9 @@ __device__ __forceinline__ int slope_side(int k0, int p0, bool left) {
 }
 
 // Bias by distance in shared memory, in base-2 units: entry j - p + R + kRelPad
-// holds table[map[clamp(j - p)]][h] * log2 e.  The pad lets a thread index a
-// whole 128-key tile that overlaps (-R, R) without clamping.
-constexpr int kRelPad = 255;
+// holds table[map[clamp(j - p)]][h] * log2 e.  The pad lets a warp's 32 rows
+// index a block of 64 keys that overlaps (-R, R) without clamping.
+constexpr int kRelPad = 95;
 __host__ __device__ constexpr int rel_entries(int R) { return 2 * (R + kRelPad) + 1; }
 
 template <bool kF16>

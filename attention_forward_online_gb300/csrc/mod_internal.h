@@ -43,14 +43,15 @@ struct ModArgs {
   float* LSE;  // written by the forward pass, read by the backward pass
   // backward
   const void* O_in;
-  void* dQ;
-  void* dK;
-  void* dV;
-  long long o_s[3];  // element strides of the b, h and row axes
-  long long dq_s[3], dk_s[3], dv_s[3];
+  long long o_s[3];  // its element strides of the b, h and row axes
   float* D;         // workspace [B, H, Nq]
   float* rel_part;  // workspace [B, H, query tiles, 2 range + 1]
   void* dRel;       // [num, H] or null
+};
+
+// Tensor maps of the backward pass; g: dO.
+struct BwdModMaps {
+  CUtensorMap q, k, v, g, dq, dk, dv;
 };
 
 int mod_score_mode(const ModArgs& a);

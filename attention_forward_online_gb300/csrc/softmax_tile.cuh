@@ -26,8 +26,14 @@ constexpr uint32_t kMinusInf = 0xff800000u;
 // this (log2 units), so that the accumulator in tensor memory is left alone on
 // almost every tile.  P may then exceed 1, by 2^8 and by as much as the max was
 // a lower bound only: fp32 sums and 16-bit P keep their relative precision.
+// It is kept a whole number, so that the factor of the accumulator is a power
+// of two, exact in the upper 16 bits of an fp32.
 constexpr float kMaxSlack = 8.f;
-__device__ __forceinline__ float next_max(float m, float mx) { return mx > m + kMaxSlack ? mx : m; }
+__device__ __forceinline__ float next_max(float m, float mx) { return mx > m + kMaxSlack ? ceilf(mx) : m; }
+__device__ __forceinline__ uint16_t alpha_bits(float m, float m_new) {
+  return static_cast<uint16_t>(__float_as_uint(m_new == m ? 1.f : ex2_approx(m - m_new)) >> 16);
+}
+__device__ __forceinline__ float alpha_of(uint16_t bits) { return __uint_as_float(static_cast<uint32_t>(bits) << 16); }
 
 using Chunk = uint32_t[32];
 
@@ -124,6 +130,9 @@ struct TileScore {
   const float* strip;     // learned bias of the tile's first key for this row, or null: off has it
   float strip_lo;         // least bias of the head
   bool strip_close;       // the head's biases lie within kSpread of each other
+  int near_lo, near_hi;   // first keys x of chunks, from the tile's first, with near_lo < x < near_hi
+                          // have distances within (-R, R): the strip; others one bias per side
+  float far_lo, far_hi;
 
   // How far a lower bound of the row max may be off: P then reaches
   // 2^(kMaxSlack + this), which has to stay a finite 16-bit value.
@@ -137,7 +146,7 @@ struct TileScore {
 
   // One tile of the row: S at s_addr becomes P = 2^(x - m) in 16 bits over its
   // first 64 columns.  Moves m, publishes the factor of the accumulator by
-  // publish(alpha) as soon as it is known, and updates l.
+  // publish(alpha_bits) as soon as it is known, and updates l.
   template <typename BitsOf, typename Publish>
   __device__ __forceinline__ void tile(uint32_t s_addr, bool masked, const TileMask& k, BitsOf&& bits_of,
                                        float& m, float& l, Publish&& publish) const {
@@ -176,7 +185,7 @@ struct TileScore {
     float m_new, sum;
     if (direct) {
       m_new = next_max(m, best_raw == -INFINITY ? -INFINITY : raw(best_raw) + off);
-      publish(m_new == m ? 1.f : ex2_approx(m - m_new));
+      publish(alpha_bits(m, m_new));
       // a row with no key so far has m_new = -inf and every x = -inf: against
       // 0 each p is exactly 0
       const float n = off - (m_new == -INFINITY ? 0.f : m_new);
@@ -193,7 +202,7 @@ struct TileScore {
         if (!bound) best = fmaxf(best, chunk_max(v[ch]));
       }
       m_new = next_max(m, best);
-      publish(m_new == m ? 1.f : ex2_approx(m - m_new));
+      publish(alpha_bits(m, m_new));
       sum = exps<true, false>(s_addr, v, k, bits_of, m_new == -INFINITY ? 0.f : -m_new);
     }
     l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
@@ -223,10 +232,17 @@ struct TileScore {
         set_pair(v, e + 2, f2_fma(f2_mul(r, ua), mul, n));
       }
     } else if constexpr (mode_rel(MODE)) {
-      const float* at = strip + ch * 32;
       const uint64_t c2 = f2_pack(c, c);
+      if (ch * 32 > near_lo && ch * 32 < near_hi) {
+        const float* at = strip + ch * 32;
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(at[e], at[e + 1])));
+        for (int e = 0; e < 32; e += 2) set_pair(v, e, f2_fma(pair_of(v, e), c2, f2_pack(at[e], at[e + 1])));
+      } else {
+        const float far = ch * 32 <= near_lo ? far_lo : far_hi;
+        const uint64_t b2 = f2_pack(far, far);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) set_pair(v, e, f2_fma(pair_of(v, e), c2, b2));
+      }
     }
     if constexpr (mode_slopes(MODE)) {
       const float f0 = d0 + static_cast<float>(ch * 32), mul = mode_cap(MODE) ? 1.f : c;
