@@ -642,14 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (mode_rel(MODE)) {
           // everyone is done with the last head's table
           if (h_of >= 0 && !(ok = elem_sync(bars, sync_phase, wc))) break;
-          for (int x = threadIdx.x; x < rel_entries(p.rel.range); x += 256) {
-            const int bucket = __ldg(p.rel.map + min(max(x - kRelPad, 0), 2 * p.rel.range));
-            float v = 0.f;
-            if (bucket >= 0 && bucket < p.rel.num)
-              v = load_16<kF16>(static_cast<const uint16_t*>(p.rel.table) +
-                                static_cast<long long>(bucket) * p.H + h);
-            bias_all[x] = v * kModLog2e;
-          }
+          float least, most;
+          rel_fill<kF16>(bias_all, p.rel, p.H, h, threadIdx.x, 256, least, most);
           if (!(ok = elem_sync(bars, sync_phase, wc))) break;
         }
         h_of = h;
@@ -809,6 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   unit_of(p, bh, rank);
   const int qt = p.num_tiles - 1 - rank;
   const int b = bh / p.H, h = bh % p.H, hk = h / p.group;
+  [[maybe_unused]] float slope = 0.f;
+  if constexpr (mode_slopes(MODE)) slope = __ldg(p.slopes + h);
   const int q0 = qt * kT;
   const PlanTile pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
   const int kt0 = pt.lo / kT;
@@ -838,15 +834,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if constexpr (mode_rel(MODE)) {
-    rel_fill<kF16>(bias, p.rel, p.H, h);
     for (int x = threadIdx.x; x < sum_entries(p.rel.range); x += kThreads) dsum[x] = 0.f;
   }
   [[maybe_unused]] bool linear = false;
   if constexpr (MODE == kModSlopes) {
-    linear = slope_linear(p.slopes[h], p.scale);
+    linear = slope_linear(slope, p.scale);
     uint8_t* at = reinterpret_cast<uint8_t*>(bias);
     if (threadIdx.x < kT / 2) slope_fill_k<kF16>(at, threadIdx.x);
-    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeKBytes / 2, threadIdx.x, p.slopes[h], p.scale);
+    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeKBytes / 2, threadIdx.x, slope, p.scale);
     fence_proxy_async();
   }
   tc_fence_before_sync();
@@ -945,8 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool row_live = see.x < see.y;
     const long long rix = static_cast<long long>(bh) * p.Nq + q;
     const int p0 = q0 + p.q_offset;
-    float slope2 = 0.f;
-    if constexpr (mode_slopes(MODE)) slope2 = p.slopes[h] * kModLog2e;
+    const float slope2 = slope * kModLog2e;
     float l2 = -INFINITY;  // -LSE log2 e
     // D of this row: warpgroup g takes columns g d/2 .. (g + 1) d/2 - 1, O
     // from global memory (loaded now), dO from the resident tile
@@ -967,8 +961,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n_kt == 0 && g == 0 && in) p.D[rix] = 0.f;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     float far_lo = 0.f, far_hi = 0.f;  // sums of dY at distances <= -R and >= R
-    [[maybe_unused]] uint32_t sync_phase = 0;  // = near tiles so far
+    [[maybe_unused]] uint32_t sync_phase = 0;
     bool ok = true;
+    if constexpr (mode_rel(MODE)) {  // while the first loads and products run
+      float least, most;
+      rel_fill<kF16>(bias, p.rel, p.H, h, threadIdx.x, 256, least, most);
+      ok = elem_sync(bars, sync_phase, wc);
+    }
     for (int j = 0; ok && j < n_kt; ++j) {
       ok = mbar_wait(&bars->s_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, wc, kSiteElem);
       ok = __all_sync(0xffffffffu, ok);

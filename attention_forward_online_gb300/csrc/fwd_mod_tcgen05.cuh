@@ -61,7 +61,8 @@ enum : uint32_t {
   kSiteAlpha = 46,
   kSiteO = 48,
   kSiteZero = 49,
-  kSiteStage = 50
+  kSiteStage = 50,
+  kSiteTable = 51
 };
 
 template <int HD, int MODE>
@@ -72,8 +73,10 @@ struct Cfg {
   // 128; wider ones (kModRelWide) take one (32 KB; a step with four stages
   // waits for its loads, 20 % slower).  At d = 64 the twelfth stage of 16 KB
   // makes room for any range.
+  // (kRangeBytes: the least and greatest that each filling warp wrote.)
+  static constexpr int kRangeBytes = 12 * 8;
   static constexpr int kTableBytes =
-      mode_rel(MODE) ? (rel_entries(HD == 64 || MODE == kModRelWide ? kMaxRelRange : kSmallRel) * 4 + 15) / 16 * 16
+      mode_rel(MODE) ? kRangeBytes + (rel_entries(HD == 64 || MODE == kModRelWide ? kMaxRelRange : kSmallRel) * 4 + 15) / 16 * 16
                      : (MODE == kModSlopes ? kSlopeKBytes + kSlopeQBytes : 0);
   static constexpr int kStages = HD == 128 ? (MODE == kModRelWide ? 4 : 5) : (mode_rel(MODE) ? 11 : 12);
   static constexpr int kIters = HD == 128 ? 4 : 8;  // > kStages / 2 + 1
@@ -90,11 +93,11 @@ struct __align__(16) Bars {
   uint64_t p_full[kQTiles];      // softmax and correction, 256 arrivals
   uint64_t o_full[kQTiles];
   uint64_t staged[kQTiles];      // O_t is in shared memory, 128 arrivals
+  uint64_t table;                // the learned biases are in shared memory, 384 arrivals
   uint64_t mma_drain;
   uint32_t tmem_base;
   int abort_flag;
   uint16_t alpha[kQTiles][BM];  // alpha_bits
-  float rel_lo, rel_hi;  // least and greatest learned bias of the head
 };
 
 template <int HD, int MODE>
@@ -146,11 +149,28 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
   }
 }
 
+// The head's learned biases, written by the softmax and correction warps while
+// the first loads and products run.
+template <int HD, bool kF16, int MODE>
+__device__ __forceinline__ bool fill_table(const Params& p, Bars* bars, float* bias, int h, const WaitCtl& wc) {
+  float lo, hi;
+  float2* range = reinterpret_cast<float2*>(bias) - 12;
+  rel_fill<kF16>(bias, p.rel, p.H, h, threadIdx.x, kProducerWarp * 32, lo, hi);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  }
+  if ((threadIdx.x & 31) == 0) range[threadIdx.x >> 5] = make_float2(lo, hi);
+  mbar_arrive(&bars->table);
+  return __all_sync(0xffffffffu, mbar_wait(&bars->table, 0u, wc, kSiteTable));
+}
+
 // ------------------------------------------------------------------ softmax
 template <int HD, bool kF16, int MODE>
 __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Params& p, Bars* bars,
-                                             const float* bias, uint8_t* sQt, uint32_t tmem, int t, int b,
-                                             int h, int q0, Range rg, const PlanTile& tile, int kt0,
+                                             float* bias, uint8_t* sQt, uint32_t tmem, int t, int b, int h,
+                                             float slope, int q0, Range rg, const PlanTile& tile, int kt0,
                                              WaitCtl wc) {
   using C = Cfg<HD, MODE>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -167,17 +187,26 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
   ts.cap = &p.cap;
   [[maybe_unused]] bool linear = false;
   if constexpr (mode_slopes(MODE)) {
-    ts.slope2 = p.slopes[h] * kModLog2e;
-    linear = MODE == kModSlopes && slope_linear(p.slopes[h], p.scale);
-  }
-  if constexpr (mode_rel(MODE)) {
-    ts.strip_lo = bars->rel_lo;
-    ts.far_lo = bias[0];
-    ts.far_hi = bias[rel_entries(p.rel.range) - 1];
-    ts.strip_close = bars->rel_hi - bars->rel_lo <= ts.kSpread;
+    ts.slope2 = slope * kModLog2e;
+    linear = MODE == kModSlopes && slope_linear(slope, p.scale);
   }
   float m = -INFINITY, l = 0.f;
   bool ok = true;
+  if constexpr (mode_rel(MODE)) {
+    ok = fill_table<HD, kF16, MODE>(p, bars, bias, h, wc);
+    if (!ok) return;
+    float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 12; ++w) {
+      const float2 r = reinterpret_cast<const float2*>(bias)[w - 12];
+      lo = fminf(lo, r.x);
+      hi = fmaxf(hi, r.y);
+    }
+    ts.strip_lo = lo;
+    ts.strip_close = hi - lo <= ts.kSpread;
+    ts.far_lo = bias[0];
+    ts.far_hi = bias[rel_entries(p.rel.range) - 1];
+  }
 
   for (int j = 0; j < rg.n; ++j) {
     ok = mbar_wait(&bars->s_full[t], static_cast<uint32_t>(j) & 1u, wc, kSiteS);
@@ -474,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + kQTiles * C::kQBytes;
-  float* bias = reinterpret_cast<float*>(smem + C::kTileRegion);
+  float* bias = reinterpret_cast<float*>(smem + C::kTileRegion + (mode_rel(MODE) ? C::kRangeBytes : 0));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kTileRegion + C::kTableBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -488,6 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int bh = g0 + rank % gsize;
   const int qb = nqb - 1 - rank / gsize;
   const int b = bh / p.H, h = bh % p.H;
+  float slope = 0.f;
+  if constexpr (mode_slopes(MODE)) slope = __ldg(p.slopes + h);
   const int q0 = qb * (kQTiles * BM);
   const int t0 = qb * kQTiles;
   const PlanTile pt0 = plan_tile(p.plan, b, p.n_tiles, t0, p.Nkv);
@@ -519,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->kv_full[i], 1);
       mbar_init(&bars->kv_empty[i], 1);
     }
+    mbar_init(&bars->table, kProducerWarp * 32);
     mbar_init(&bars->mma_drain, 1);
     bars->abort_flag = 0;
     fence_barrier_init();
@@ -532,35 +564,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if constexpr (mode_rel(MODE)) rel_fill<kF16>(bias, p.rel, p.H, h);
   if constexpr (MODE == kModSlopes) {
     uint8_t* at = reinterpret_cast<uint8_t*>(bias);
     if (threadIdx.x < BN) slope_fill_k<kF16>(at, threadIdx.x);
-    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeKBytes, threadIdx.x, p.slopes[h], p.scale);
+    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeKBytes, threadIdx.x, slope, p.scale);
     fence_proxy_async();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if constexpr (mode_rel(MODE)) {
-    if (warp == 0) {  // the range of the head's biases, for the softmax's bounds
-      float a = INFINITY, z = -INFINITY;
-      for (int x = lane + kRelPad; x <= 2 * p.rel.range + kRelPad; x += 32) {
-        a = fminf(a, bias[x]);
-        z = fmaxf(z, bias[x]);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, off));
-        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, off));
-      }
-      if (lane == 0) {
-        bars->rel_lo = a;
-        bars->rel_hi = z;
-      }
-    }
-    __syncthreads();
-  }
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
 
@@ -568,10 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kCorrWarp0) {
     regs_inc<184>();
     const int t = warp >> 2;
-    softmax_role<HD, kF16, MODE>(&tmO, p, bars, bias, sQ + t * C::kQBytes, tmem, t, b, h, q0 + t * BM,
+    softmax_role<HD, kF16, MODE>(&tmO, p, bars, bias, sQ + t * C::kQBytes, tmem, t, b, h, slope, q0 + t * BM,
                                  t ? r1 : r0, t ? pt1 : pt0, kt0, wc);
   } else if (warp < kProducerWarp) {
     regs_dec<88>();
+    if constexpr (mode_rel(MODE)) fill_table<HD, kF16, MODE>(p, bars, bias, h, wc);
     correction_role<HD, MODE>(bars, sKV, tmem, r0, r1, n, kt0, lo, hi, p.Nkv, wc);
   } else {
     regs_dec<56>();
@@ -580,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == kMmaWarp && n > 0) {
       uint32_t slope_tiles = 0;
       if constexpr (MODE == kModSlopes)
-        if (slope_linear(p.slopes[h], p.scale)) slope_tiles = smem_u32(bias);
+        if (slope_linear(slope, p.scale)) slope_tiles = smem_u32(bias);
       mma_role<HD, kF16, MODE>(bars, tmem, sQ, sKV, r0, r1, n, kt0, slope_tiles, q0 + p.q_offset, pt0.left,
                                pt1.left, p.neg_q, wc);
     }

@@ -230,17 +230,23 @@ __device__ __forceinline__ float load_16(const uint16_t* p) {
   else return __bfloat162float(__ushort_as_bfloat16(w));
 }
 
-// Fills bias[] with all threads of the block; a bucket outside [0, num) adds
-// nothing.
+// Fills bias[] with n threads (x0: 0 .. n - 1); a bucket outside [0, num) adds
+// nothing.  lo, hi: the least and greatest bias this thread wrote.
 template <bool kF16>
-__device__ __forceinline__ void rel_fill(float* bias, const RelArgs& r, int H, int h) {
-  for (int x = threadIdx.x; x < rel_entries(r.range); x += blockDim.x) {
+__device__ __forceinline__ void rel_fill(float* bias, const RelArgs& r, int H, int h, int x0, int n, float& lo,
+                                         float& hi) {
+  lo = INFINITY;
+  hi = -INFINITY;
+  for (int x = x0; x < rel_entries(r.range); x += n) {
     const int at = min(max(x - kRelPad, 0), 2 * r.range);
     const int bucket = __ldg(r.map + at);
     float v = 0.f;
     if (bucket >= 0 && bucket < r.num)
       v = load_16<kF16>(static_cast<const uint16_t*>(r.table) + static_cast<long long>(bucket) * H + h);
-    bias[x] = v * kModLog2e;
+    v *= kModLog2e;
+    bias[x] = v;
+    lo = v == v ? fminf(lo, v) : -INFINITY;  // NaN: no bound holds
+    hi = v == v ? fmaxf(hi, v) : INFINITY;
   }
 }
 

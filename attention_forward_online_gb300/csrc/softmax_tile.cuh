@@ -333,9 +333,10 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
                "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
                : "memory");
 }
-// The stores issued by this thread are done.
+// The stores issued by this thread have read their shared memory, which may
+// then be given up; they land before the kernel ends.
 __device__ __forceinline__ void tma_store_drain() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 }  // namespace osattn
