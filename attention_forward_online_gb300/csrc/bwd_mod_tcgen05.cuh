@@ -61,7 +61,7 @@ struct Cfg {
   static constexpr int kTileBytes = kT * HD * 2;
   // table of learned biases, or the slope operands
   static constexpr int kTableBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16
-                                                    : (MODE == kModSlopes ? kSlopeKBytes + 4 * kSlopeQBytes : 0);
+                                                    : (MODE == kModSlopes ? kSlopeRowsBytes + 4 * kSlopeQBytes : 0);
   // dkdv: K, V, kStages stages of (Q_i, dO_i), then per stage LSE, D, lo, hi
   static constexpr int kStages = HD == 128 ? 2 : 4;
   static constexpr int kStageBytes = 2 * kTileBytes;
@@ -75,7 +75,7 @@ struct Cfg {
   static constexpr int kKSlots = HD == 128 ? (mode_rel(MODE) ? 2 : 3) : 4;
   static constexpr int kVSlots = HD == 128 ? 2 : 4;
   static constexpr int kDqTable = (2 + kKSlots + kVSlots) * kTileBytes;
-  static constexpr int kDqTableBytes = MODE == kModSlopes ? kSlopeKBytes / 2 + kSlopeQBytes : kTableBytes;
+  static constexpr int kDqTableBytes = MODE == kModSlopes ? kSlopeRowsBytes / 2 + kSlopeQBytes : kTableBytes;
   static constexpr int kDqSums = kDqTable + kDqTableBytes;
   static constexpr int kSumBytes = mode_rel(MODE) ? (sum_entries(kMaxRelRange) * 4 + 15) / 16 * 16 : 0;
   static constexpr int kStripBytes = mode_rel(MODE) ? 2 * 8 * 96 * 4 : 0;
@@ -390,7 +390,7 @@ __device__ __forceinline__ int far_side(int first, int last, int R) {
 template <bool kF16>
 __device__ __forceinline__ void add_slope_t(uint32_t s_col, uint32_t q_at, uint32_t k_at, int side) {
   if (side == 0) return;
-  mma_ss_k<1, true>(s_col, slope_k_desc(k_at), slope_q_desc(q_at),
+  mma_ss_k<1, true>(s_col, slope_rows_desc(k_at), slope_q_desc(q_at),
                     idesc_f16_f32(128, 128, 0, kF16) | (side < 0 ? kIdescNegA : 0u));
 }
 // 128 queries by two halves of 64 keys, each counted from its own first key:
@@ -398,8 +398,8 @@ template <bool kF16>
 __device__ __forceinline__ void add_slope(uint32_t s_col, uint32_t q_at, uint32_t k_at, int side) {
   if (side == 0) return;
   const uint32_t id = idesc_f16_f32(128, 64, 0, kF16) | (side < 0 ? kIdescNegA : 0u);
-  mma_ss_k<1, true>(s_col, slope_q_desc(q_at), slope_k_desc(k_at), id);
-  mma_ss_k<1, true>(s_col + 64, slope_q_desc(q_at), slope_k_desc(k_at), id);
+  mma_ss_k<1, true>(s_col, slope_q_desc(q_at), slope_rows_desc(k_at), id);
+  mma_ss_k<1, true>(s_col + 64, slope_q_desc(q_at), slope_rows_desc(k_at), id);
 }
 
 // ------------------------------------------------------------------ dK, dV
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if constexpr (MODE == kModSlopes) {
           if (lane < 8)
-            slope_fill_q<kF16>(reinterpret_cast<uint8_t*>(bias_all) + kSlopeKBytes + s * kSlopeQBytes, lane,
+            slope_fill_q<kF16>(reinterpret_cast<uint8_t*>(bias_all) + kSlopeRowsBytes + s * kSlopeQBytes, lane,
                                slope, p.scale);
           if (lane == 0) bars->side[s] = side;
           fence_proxy_async();
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sq = smem_u32(ring), sdo = sq + C::kTileBytes;
         mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(sq, 16, 1024));
         if constexpr (MODE == kModSlopes)
-          add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeKBytes, smem_u32(bias_all), bars->side[0]);
+          add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes, smem_u32(bias_all), bars->side[0]);
         mma_commit<true>(&bars->s_full[0]);
         mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(sdo, 16, 1024));
         mma_commit<true>(&bars->dp_full);
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
           mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(nq, 16, 1024));
           if constexpr (MODE == kModSlopes)
-            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeKBytes + s1 * kSlopeQBytes,
+            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + s1 * kSlopeQBytes,
                                    smem_u32(bias_all), bars->side[s1]);
           mma_commit<true>(&bars->s_full[0]);
         }
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear = slope_linear(slope, p.scale);
     uint8_t* at = reinterpret_cast<uint8_t*>(bias);
     if (threadIdx.x < kT / 2) slope_fill_k<kF16>(at, threadIdx.x);
-    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeKBytes / 2, threadIdx.x, slope, p.scale);
+    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeRowsBytes / 2, threadIdx.x, slope, p.scale);
     fence_proxy_async();
   }
   tc_fence_before_sync();
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qA = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dA = sdesc_sw128(smem_u32(sdO), 16, 1024);
       [[maybe_unused]] auto slope_step = [&](uint32_t s_col, int j) {
-        add_slope<kF16>(s_col, smem_u32(bias) + kSlopeKBytes / 2, smem_u32(bias),
+        add_slope<kF16>(s_col, smem_u32(bias) + kSlopeRowsBytes / 2, smem_u32(bias),
                         linear ? slope_side((kt0 + j) * kT, q0 + p.q_offset, pt.left) : 0);
       };
       bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);

@@ -77,7 +77,7 @@ struct Cfg {
   static constexpr int kRangeBytes = 12 * 8;
   static constexpr int kTableBytes =
       mode_rel(MODE) ? kRangeBytes + (rel_entries(HD == 64 || MODE == kModRelWide ? kMaxRelRange : kSmallRel) * 4 + 15) / 16 * 16
-                     : (MODE == kModSlopes ? kSlopeKBytes + kSlopeQBytes : 0);
+                     : (MODE == kModSlopes ? kSlopeRowsBytes + kSlopeQBytes : 0);
   static constexpr int kStages = HD == 128 ? (MODE == kModRelWide ? 4 : 5) : (mode_rel(MODE) ? 11 : 12);
   static constexpr int kIters = HD == 128 ? 4 : 8;  // > kStages / 2 + 1
   static constexpr int kTileRegion = kQTiles * kQBytes + kStages * kTileBytes;
@@ -236,7 +236,7 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
       ts.near_lo = -R - 31 - first + 32 * quarter;
       ts.near_hi = R + 31 - first + 32 * quarter;
     }
-    ts.tile(s_addr, masked, mk, bits_of, m, l, [&](uint16_t alpha) {
+    ts.tile(s_addr, masked, mk, bits_of, ts.by_place(), m, l, [&](uint16_t alpha) {
       bars->alpha[t][row] = alpha;
       mbar_arrive(&bars->alpha_full[t]);
     });
@@ -439,7 +439,7 @@ __device__ __forceinline__ void mma_role(Bars* bars, uint32_t tmem, uint8_t* sQ,
     if (slope_tiles == 0) return;
     const int side = slope_side((kt0 + j) * BN, pt, left);
     if (side == 0) return;
-    mma_ss_k<1, true>(s_col, slope_q_desc(slope_tiles + kSlopeKBytes), slope_k_desc(slope_tiles),
+    mma_ss_k<1, true>(s_col, slope_q_desc(slope_tiles + kSlopeRowsBytes), slope_rows_desc(slope_tiles),
                       idesc_f16_f32(128, 128, 0, kF16) | (side < 0 ? kIdescNegA : 0u));
   };
   bool ok = true;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (MODE == kModSlopes) {
     uint8_t* at = reinterpret_cast<uint8_t*>(bias);
     if (threadIdx.x < BN) slope_fill_k<kF16>(at, threadIdx.x);
-    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeKBytes, threadIdx.x, slope, p.scale);
+    if (threadIdx.x < 8) slope_fill_q<kF16>(at + kSlopeRowsBytes, threadIdx.x, slope, p.scale);
     fence_proxy_async();
   }
   tc_fence_before_sync();

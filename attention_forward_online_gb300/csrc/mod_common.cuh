@@ -141,36 +141,31 @@ __device__ __forceinline__ void mma_abt_id(uint32_t d_tmem, uint64_t a_desc, uin
 }
 
 // Slopes on the tensor cores.  For keys on one side of a query,
-// -slope |j - p| = +-slope (j - p) is linear in the key's place e in its
-// tile; with one more MMA step of 16 inner elements, whose operands hold
-// (hi, mid, lo, 0 ...) of +-slope / scale in every query row and (e, e, e,
-// 0 ...) in key row e, the scores come out as s +- (slope / scale) e and what
-// is left of the bias is one constant per row and tile.  hi + mid + lo carry
-// slope / scale to 2^-24 in bf16 (three 8-bit pieces; fp16: to its smallest
-// step), e < 128 is exact, and the products are summed in fp32 as s is.
-// Tiles with keys on both sides of a row that sees them get the bias score
-// by score instead.
-// The operands are made of 8 x 16-byte core matrices without swizzle.  All
-// query rows are alike: one core matrix of (hi, mid, lo, 0 ...) rows and one of
-// zeros for the other 8 inner elements, with a stride of 0 between row groups.
-// Key rows (e, e, e, 0 ...): 16 core matrices, read again for the other 8
-// inner elements (stride 0), where they meet the zeros.
-constexpr int kSlopeQBytes = 256;
-constexpr int kSlopeKBytes = 128 * 16;
-constexpr float kSlopeMax = 16384.f;  // |slope / scale| beyond: score by score
+// -slope |j - p| = +-slope (j - p) is linear in the key's place e in its tile;
+// with one more MMA step of 16 inner elements, whose operands hold (hi, mid,
+// lo, 0 ...) of slope / (2 scale) in each query row and (e, e, e, 0 ...) in key
+// row e, twice, the scores come out as s +- (slope / scale) e and what is left
+// of the bias is one constant per row and tile.  hi + mid + lo carry the
+// quotient to 2^-24 in bf16 (three 8-bit pieces; fp16: to its smallest step),
+// e < 128 is exact, and the products are summed in fp32 as s is.  Tiles with
+// keys on both sides of a row that sees them get the bias score by score.
+// The operands are 8 x 16-byte core matrices without swizzle; the other 8
+// inner elements read the same matrix again (stride 0, hence the half), and
+// so do all row groups where every query row is alike.
+constexpr int kSlopeQBytes = 128;       // alike query rows: one core matrix
+constexpr int kSlopeRowsBytes = 128 * 16;  // 128 different rows, of queries or keys
+constexpr float kSlopeMax = 16384.f;    // |slope / scale| beyond: score by score
 
-// Shared-memory descriptor without swizzle; lbo: to the next 8 inner elements,
-// sbo: to the next 8 rows.
-__device__ __forceinline__ uint64_t sdesc_plain(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
+// Descriptor of rows of 8 elements read twice; sbo: to the next 8 rows.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t smem_addr, uint32_t sbo) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(lbo >> 4) << 16;
   d |= static_cast<uint64_t>(sbo >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   return d;
 }
-__device__ __forceinline__ uint64_t slope_q_desc(uint32_t at) { return sdesc_plain(at, 128, 0); }
-__device__ __forceinline__ uint64_t slope_k_desc(uint32_t at) { return sdesc_plain(at, 0, 128); }
+__device__ __forceinline__ uint64_t slope_q_desc(uint32_t at) { return sdesc_plain(at, 0); }
+__device__ __forceinline__ uint64_t slope_rows_desc(uint32_t at) { return sdesc_plain(at, 128); }
 
 __device__ __forceinline__ bool slope_linear(float slope, float scale) {
   return fabsf(slope / scale) <= kSlopeMax;
@@ -187,26 +182,24 @@ __device__ __forceinline__ float from_16(uint16_t w) {
   else return __bfloat162float(__ushort_as_bfloat16(w));
 }
 
-// Write the operands with 8 threads (x: 0 .. 7) and 128 threads (x: 0 .. 127);
-// the caller orders the writes before the MMAs (fence_proxy_async, then a
-// barrier).
+// Write one row of a query or key operand (row 0 .. 7 where query rows are
+// alike); the caller orders the writes before the MMAs (fence_proxy_async, then
+// a barrier).
 template <bool kF16>
-__device__ __forceinline__ void slope_fill_q(uint8_t* at, int x, float slope, float scale) {
+__device__ __forceinline__ void slope_fill_q(uint8_t* at, int row, float slope, float scale) {
   uint16_t w[3];
-  float rest = slope_linear(slope, scale) ? slope / scale : 0.f;
+  float rest = slope_linear(slope, scale) ? 0.5f * (slope / scale) : 0.f;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     w[i] = to_16<kF16>(rest);
     rest -= from_16<kF16>(w[i]);
   }
-  uint4* q = reinterpret_cast<uint4*>(at) + x;
-  q[0] = make_uint4(w[0] | (static_cast<uint32_t>(w[1]) << 16), w[2], 0u, 0u);
-  q[8] = make_uint4(0u, 0u, 0u, 0u);
+  reinterpret_cast<uint4*>(at)[row] = make_uint4(w[0] | (static_cast<uint32_t>(w[1]) << 16), w[2], 0u, 0u);
 }
 template <bool kF16>
-__device__ __forceinline__ void slope_fill_k(uint8_t* at, int x) {
-  const uint32_t e = to_16<kF16>(static_cast<float>(x));
-  reinterpret_cast<uint4*>(at)[x] = make_uint4(e | (e << 16), e, 0u, 0u);
+__device__ __forceinline__ void slope_fill_k(uint8_t* at, int row) {
+  const uint32_t e = to_16<kF16>(static_cast<float>(row));
+  reinterpret_cast<uint4*>(at)[row] = make_uint4(e | (e << 16), e, 0u, 0u);
 }
 
 // Which side of a tile's rows its keys k0 .. k0 + 127 lie on: 1 before or at

@@ -125,7 +125,7 @@ struct TileScore {
   float c;                // |scale| * log2(e)
   float off;              // constant part of the bias
   const CapArgs* cap;
-  float slope2, d0;       // both_sides: - slope2 |d0 + e|
+  float slope2, d0;       // both_sides: - slope2 |d0 + e| (or another distance)
   bool both_sides;
   const float* strip;     // learned bias of the tile's first key for this row, or null: off has it
   float strip_lo;         // least bias of the head
@@ -138,6 +138,12 @@ struct TileScore {
   // 2^(kMaxSlack + this), which has to stay a finite 16-bit value.
   static constexpr float kSpread = kF16 ? 7.f : 64.f;
 
+  // Distances that grow by one from key to key.
+  __device__ __forceinline__ auto by_place() const {
+    const float d = d0;
+    return [d](int e) { return d + static_cast<float>(e); };
+  }
+
   // cap(s) c of one score
   __device__ __forceinline__ float raw(float s) const {
     if constexpr (mode_cap(MODE)) return fmaf(cap_r(s, cap->c1), -2.f * cap->cap2, cap->cap2);
@@ -147,9 +153,10 @@ struct TileScore {
   // One tile of the row: S at s_addr becomes P = 2^(x - m) in 16 bits over its
   // first 64 columns.  Moves m, publishes the factor of the accumulator by
   // publish(alpha_bits) as soon as it is known, and updates l.
-  template <typename BitsOf, typename Publish>
+  // gap(e): the distance of key e of the tile, for both_sides.
+  template <typename BitsOf, typename Gap, typename Publish>
   __device__ __forceinline__ void tile(uint32_t s_addr, bool masked, const TileMask& k, BitsOf&& bits_of,
-                                       float& m, float& l, Publish&& publish) const {
+                                       Gap&& gap, float& m, float& l, Publish&& publish) const {
     Row v;
     float top[kChunks];
     load_row(s_addr, v, top);
@@ -197,7 +204,7 @@ struct TileScore {
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) {
         if ((k.none >> ch) & 1u) continue;
-        logits(v[ch], ch);
+        logits(v[ch], ch, gap);
         if (mode_cap(MODE) && ((k.partial >> ch) & 1u)) mask_chunk(v[ch], bits_of(ch), kMinusInf);
         if (!bound) best = fmaxf(best, chunk_max(v[ch]));
       }
@@ -210,7 +217,8 @@ struct TileScore {
   }
 
   // x in place of the 32 scores of chunk ch (tiles that are not direct).
-  __device__ __forceinline__ void logits(Chunk& v, int ch) const {
+  template <typename Gap>
+  __device__ __forceinline__ void logits(Chunk& v, int ch, Gap&& gap) const {
     if constexpr (mode_cap(MODE)) {
       // cap2 - 2 cap2 / (1 + E): one reciprocal for four scores, 1 + E kept
       // below 2^30 so that four multiply without overflow (the tanh is 1 to
@@ -245,10 +253,10 @@ struct TileScore {
       }
     }
     if constexpr (mode_slopes(MODE)) {
-      const float f0 = d0 + static_cast<float>(ch * 32), mul = mode_cap(MODE) ? 1.f : c;
+      const float mul = mode_cap(MODE) ? 1.f : c;
 #pragma unroll
       for (int e = 0; e < 32; ++e)
-        v[e] = __float_as_uint(fmaf(-slope2, fabsf(f0 + static_cast<float>(e)), __uint_as_float(v[e]) * mul));
+        v[e] = __float_as_uint(fmaf(-slope2, fabsf(gap(ch * 32 + e)), __uint_as_float(v[e]) * mul));
     }
   }
 

@@ -20,9 +20,11 @@
 //     softmax warpgroups work while the tensor core fills the other's scores;
 //     the two states are merged once at the segment's end.
 //
-// Warps 0-3 and 4-7: softmax of the even and odd tiles, one row a thread; 8-11
-// rescale O; 12 TMA producer (lane x loads box x of a tile, a box lying in one
-// page); 13 MMA issue.  Tensor memory: S0, S1 (P in 16 bits over them), O0, O1.
+// Warps 0-3 and 4-7: softmax of the even and odd tiles, one row a thread (a
+// warp whose 32 rows hold no token only keeps the barriers' count: a decode
+// step fills a few rows of the 128); 8-11 rescale O; 12 and 14 TMA producers of
+// Q and K, and of V (lane x loads box x of a tile, a box lying in one page);
+// 13 MMA issue.  Tensor memory: S0, S1 (P in 16 bits over them), O0, O1.
 #pragma once
 
 #include <cmath>
@@ -32,6 +34,7 @@
 
 #include "mod_common.cuh"
 #include "sm100_ptx.cuh"
+#include "softmax_tile.cuh"
 #include "tc_attn_mma.cuh"
 #include "tree_internal.h"
 
@@ -41,7 +44,7 @@ namespace tree {
 constexpr int BM = 128;
 constexpr int BN = 128;
 constexpr int kThreads = 512;
-constexpr int kCorrWarp0 = 8, kProducerWarp = 12, kMmaWarp = 13;
+constexpr int kCorrWarp0 = 8, kProducerWarp = 12, kMmaWarp = 13, kProducerVWarp = 14;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol0 = 256;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -63,14 +66,16 @@ enum : uint32_t {
   kSiteZero = 93
 };
 
-template <int HD>
+template <int HD, int MODE>
 struct Cfg {
   static constexpr int kTileBytes = BN * HD * 2;
-  // K_i is read until S_i, two tiles ahead of the product with V_i, so V needs
-  // the deeper ring where not both fit.
-  static constexpr int kKSlots = HD == 128 ? 2 : 6;
+  // slots of K tiles, and as many of V tiles; the slopes' operands take the
+  // place of one K tile at d = 128 (at d = 64 there is room)
+  static constexpr int kKSlots = HD == 128 ? (MODE == kModSlopes ? 2 : 3) : 6;
   static constexpr int kVSlots = HD == 128 ? 3 : 6;
   static constexpr int kTileRegion = (1 + kKSlots + kVSlots) * kTileBytes;
+  // the key rows' operand, then the query rows' (the heads of a group differ)
+  static constexpr int kTableBytes = MODE == kModSlopes ? 2 * kSlopeRowsBytes : 0;
 };
 
 struct __align__(16) Bars {
@@ -87,13 +92,13 @@ struct __align__(16) Bars {
   int abort_flag;
   int start_b, start_base, total;
   int warp_sum[16];
-  float alpha[2][BM];
-  float2 state[2][2][BM];  // [segment parity][accumulator][row]: m, l
+  uint16_t alpha[2][BM];  // alpha_bits
+  float2 state[2][BM];    // [accumulator][row]: m, l
 };
 
-template <int HD>
+template <int HD, int MODE>
 constexpr int smem_bytes() {
-  return Cfg<HD>::kTileRegion + static_cast<int>(sizeof(Bars)) + 1024;
+  return Cfg<HD, MODE>::kTileRegion + Cfg<HD, MODE>::kTableBytes + static_cast<int>(sizeof(Bars));
 }
 
 struct Params {
@@ -109,7 +114,9 @@ struct Params {
   int max_pages, page, num_pages;
   int box_rows;   // keys of one TMA box: min(page, 128)
   int window;
-  float scale_log2, cap_c1, cap2;
+  float scale, scale_log2;  // |scale|, |scale| * log2(e) (positive_scale)
+  uint32_t neg_q;           // kIdescNegA if the scale is negative
+  CapArgs cap;
   const float* slopes;
   float* o_part;    // [2 grid][slot_rows][d]
   float* lse_part;  // [2 grid][slot_rows]
@@ -142,18 +149,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
   }
 }
 
-__device__ __forceinline__ float max128(const uint32_t* v) {
-  float a[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 8]));
-#pragma unroll
-  for (int j = 16; j < BN; j += 16)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      a[i] = fmax3(a[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 8 + i]));
-  return fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
-}
-
 // Cached keys of a sequence, kept within its page table.
 __device__ __forceinline__ int ctx_of(const Params& p, int b) {
   const long long room = static_cast<long long>(p.max_pages) * p.page - p.T;
@@ -181,6 +176,13 @@ __device__ __forceinline__ unsigned long long mask_of(const Params& p, int b, in
 // A draft's place behind the context: how many other drafts lie on its line.
 __device__ __forceinline__ int depth_of(unsigned long long mask) {
   return mask ? __popcll(mask) - 1 : 0;
+}
+
+// Whether the slopes of a key head's query heads all go through the MMA step.
+__device__ __forceinline__ bool slopes_linear(const Params& p, int hk) {
+  bool ok = true;
+  for (int g = 0; g < p.group; ++g) ok = ok && slope_linear(__ldg(p.slopes + hk * p.group + g), p.scale);
+  return ok;
 }
 
 // Shares of a list of `total` key tiles: no share is empty.
@@ -242,29 +244,35 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t s_addr = lane_base + static_cast<uint32_t>(t * BN);
   const int tl = row / p.group, g = row - tl * p.group;
-  const float c = p.scale_log2;
+  TileScore<kF16, MODE> ts;
+  ts.c = p.scale_log2;
+  ts.off = 0.f;
+  ts.cap = &p.cap;
   uint32_t s_phase = 0, seg = 0;
   bool ok = true;
   for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
     const int tok = w.rt * p.tok_tile + tl;
     const bool live = tl < p.tok_tile && tok < p.T;
+    const bool warp_live = __any_sync(0xffffffffu, live);
     const int h = w.hk * p.group + g;
     unsigned long long mask = live ? mask_of(p, w.b, tok) : 0ull;
+    const bool sees = mask != 0ull;  // a padding token sees nothing: its row is zeroed at the end
     const int depth = depth_of(mask);
-    int lo = w.ctx + p.T;  // first key of the row's context; a padding row sees nothing
-    if (mask) {
-      lo = 0;
-      if (p.window > 0) {
-        lo = max(0, w.ctx + depth - p.window + 1);
-        if (p.T > p.window) {  // drafts of its line that are a window away
-          for (int u = 0; u < p.T; ++u)
-            if (((mask >> u) & 1) && abs(depth - depth_of(mask_of(p, w.b, u))) >= p.window)
-              mask &= ~(1ull << u);
-        }
+    int lo = 0;  // first key of the row's context
+    if (p.window > 0) {
+      lo = max(0, w.ctx + depth - p.window + 1);
+      if (sees && p.T > p.window) {  // drafts of its line that are a window away
+        for (int u = 0; u < p.T; ++u)
+          if (((mask >> u) & 1) && abs(depth - depth_of(mask_of(p, w.b, u))) >= p.window)
+            mask &= ~(1ull << u);
       }
     }
-    [[maybe_unused]] float slope2 = 0.f;
-    if constexpr (mode_slopes(MODE)) slope2 = live ? __ldg(p.slopes + h) * kModLog2e : 0.f;
+    [[maybe_unused]] bool linear = false;
+    if constexpr (mode_slopes(MODE)) {
+      const float slope = live ? __ldg(p.slopes + h) : 0.f;
+      ts.slope2 = slope * kModLog2e;
+      linear = MODE == kModSlopes && slopes_linear(p, w.hk);
+    }
     const int tile_lo = p.window > 0 ? max(0, w.ctx + p.T - p.window) : 0;  // every row's context starts at or before it
     float m = -INFINITY, l = 0.f;
     for (int i = t; ok && i < w.n; i += 2) {
@@ -273,116 +281,67 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
       if (!ok) break;
       ++s_phase;
       tc_fence_after_sync();
-      uint32_t v[BN];
-#pragma unroll
-      for (int ch = 0; ch < BN / 32; ++ch) tmem_ld_32x32b_x32(s_addr + ch * 32, v + ch * 32);
-      tmem_ld_wait();
-#pragma unroll
-      for (int ch = 0; ch < BN / 32; ++ch) reg_fence32(v + ch * 32);
+      auto publish = [&](uint16_t alpha) {
+        bars->alpha[t][row] = alpha;
+        mbar_arrive(&bars->alpha_full[t]);
+      };
+      if (!warp_live) {
+        publish(0x3f80);  // 1: nothing to rescale
+        tc_fence_before_sync();
+        mbar_arrive(&bars->p_full[t]);
+        continue;
+      }
       const int k0 = (w.tile0 + i) * BN;
       const bool tail = k0 + BN > w.ctx;  // holds drafts or keys behind them
-#pragma unroll
-      for (int e = 0; e < BN; ++e) {
-        const float s = __uint_as_float(v[e]);
-        float x;
-        if constexpr (mode_cap(MODE))
-          x = fmaf(cap_r(s, p.cap_c1), -2.f * p.cap2, p.cap2);
-        else
-          x = s * c;
-        v[e] = __float_as_uint(x);
-      }
+      const bool masked = tail || k0 < tile_lo;
+      // visible keys of a chunk: context keys [lo, ctx), then the mask
+      auto bits_of = [&](int ch) {
+        const int c0 = k0 + 32 * ch;
+        uint32_t bits = bit_range(lo - c0, w.ctx - c0);
+        const int sh = w.ctx - c0;  // where draft 0 falls
+        if (sh >= 0 && sh < 32) bits |= static_cast<uint32_t>(mask << sh);
+        else if (sh < 0 && sh > -64) bits |= static_cast<uint32_t>(mask >> -sh);
+        return bits;
+      };
+      TileMask mk;
+      if (masked) mk.classify(bits_of);
       if constexpr (mode_slopes(MODE)) {
-        const float d0 = static_cast<float>(w.ctx + depth - k0);  // distance of the tile's first key
-        if (!tail) {
-#pragma unroll
-          for (int e = 0; e < BN; ++e)
-            v[e] = __float_as_uint(fmaf(-slope2, d0 - static_cast<float>(e), __uint_as_float(v[e])));
-        } else {
-#pragma unroll
-          for (int e = 0; e < BN; ++e) {
+        // distances fall along the context; drafts are at the distance of
+        // their depths
+        ts.d0 = static_cast<float>(k0 - (w.ctx + depth));
+        ts.both_sides = !linear || tail;
+        ts.off = ts.both_sides ? 0.f : ts.slope2 * ts.d0;
+        if (tail) {
+          auto gap = [&](int e) {
             const int u = k0 + e - w.ctx;
-            float dist = d0 - static_cast<float>(e);
-            if (u >= 0) dist = u < p.T ? fabsf(static_cast<float>(depth - depth_of(mask_of(p, w.b, u)))) : 0.f;
-            v[e] = __float_as_uint(fmaf(-slope2, dist, __uint_as_float(v[e])));
-          }
+            const float dist = ts.d0 + static_cast<float>(e);
+            if (u < 0) return dist;
+            return u < p.T ? static_cast<float>(depth_of(mask_of(p, w.b, u)) - depth) : 0.f;
+          };
+          ts.tile(s_addr, masked, mk, bits_of, gap, m, l, publish);
         }
       }
-      if (tail || k0 < tile_lo) {
-        // visible keys of the tile as 128 bits: context keys [lo, ctx), then the mask
-        const int nc = w.ctx - k0;  // keys of the tile before the drafts (may be negative or > 128)
-        const int from = lo - k0;
-        unsigned long long bits[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int a = 64 * x;  // bits a .. a + 63
-          const int up = min(max(nc - a, 0), 64), dn = min(max(from - a, 0), 64);
-          unsigned long long cb = up >= 64 ? ~0ull : (1ull << up) - 1;
-          cb &= dn >= 64 ? 0ull : ~0ull << dn;
-          const int sh = nc - a;  // where draft 0 falls
-          unsigned long long db = 0ull;
-          if (sh >= 0 && sh < 64) db = mask << sh;
-          else if (sh < 0 && sh > -64) db = mask >> -sh;
-          bits[x] = cb | db;
-        }
-#pragma unroll
-        for (int e = 0; e < BN; ++e)
-          if (!((bits[e >> 6] >> (e & 63)) & 1ull)) v[e] = __float_as_uint(-INFINITY);
-      } else if (!live) {
-#pragma unroll
-        for (int e = 0; e < BN; ++e) v[e] = __float_as_uint(-INFINITY);
-      } else if (!mask) {
-#pragma unroll
-        for (int e = 0; e < BN; ++e) v[e] = __float_as_uint(-INFINITY);
-      }
-      const float m_new = fmaxf(m, max128(v));
-      const float alpha = (m_new == m) ? 1.f : ex2_approx(m - m_new);
-      bars->alpha[t][row] = alpha;
-      mbar_arrive(&bars->alpha_full[t]);
-      const float neg_m = (m_new == -INFINITY) ? 0.f : -m_new;
-      const uint64_t nm2 = f2_pack(neg_m, neg_m);
-      uint64_t rs_a = 0, rs_b = 0;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int x = half * 64 + 2 * e;
-          float x0, x1;
-          f2_unpack(f2_add(f2_pack(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), nm2), x0, x1);
-          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          const uint64_t pp = f2_pack(p0, p1);
-          if (e & 1)
-            rs_b = f2_add(rs_b, pp);
-          else
-            rs_a = f2_add(rs_a, pp);
-          pk[e] = pack2<kF16>(p0, p1);
-        }
-        tmem_st_32x32b_x32(s_addr + half * 32, pk);
-      }
-      float r0, r1, r2, r3;
-      f2_unpack(rs_a, r0, r1);
-      f2_unpack(rs_b, r2, r3);
-      l = fmaf(l, alpha, (r0 + r1) + (r2 + r3));
-      m = m_new;
+      if (!mode_slopes(MODE) || !tail) ts.tile(s_addr, masked, mk, bits_of, ts.by_place(), m, l, publish);
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&bars->p_full[t]);
     }
     if (!ok) break;
     // ---- merge the two states; warpgroup t finishes columns t d/2 .. of both
-    bars->state[seg & 1][t][row] = make_float2(m, l);
+    if (seg > 0) ok = mbar_wait(&bars->o_empty, (seg - 1) & 1u, wc, kSiteOEmpty);  // the last states have been read
+    bars->state[t][row] = make_float2(m, l);
     mbar_arrive(&bars->merge);
-    ok = mbar_wait(&bars->merge, seg & 1u, wc, kSiteMerge);
+    if (ok) ok = mbar_wait(&bars->merge, seg & 1u, wc, kSiteMerge);
     if (ok) ok = mbar_wait(&bars->o_full, seg & 1u, wc, kSiteO);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     tc_fence_after_sync();
-    const float2 s0 = bars->state[seg & 1][0][row], s1 = bars->state[seg & 1][1][row];
+    const float2 s0 = bars->state[0][row], s1 = bars->state[1][row];
     const float M = fmaxf(s0.x, s1.x);
     const float f0 = s0.x == -INFINITY ? 0.f : ex2_approx(s0.x - M);
     const float f1 = s1.x == -INFINITY ? 0.f : ex2_approx(s1.x - M);
     const float L = fmaf(s0.y, f0, s1.y * f1);
-    const bool empty = L == 0.f;
+    const bool empty = L == 0.f || !sees;
     const float inv = empty ? 0.f : 1.f / L;
     const float g0 = f0 * inv, g1 = f1 * inv;
     const bool whole = !w.head_cut && !w.tail_cut;
@@ -394,6 +353,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
     float* part = p.o_part + prow * HD + t * kHalf;
 #pragma unroll
     for (int ch = 0; ch < kHalf / 32; ++ch) {
+      if (!warp_live) break;
       uint32_t a0[32], a1[32];
       tmem_ld_32x32b_x32(o_addr + ch * 32, a0);
       if (w.n > 1) tmem_ld_32x32b_x32(o_addr + HD + ch * 32, a1);
@@ -434,10 +394,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
 }
 
 // ------------------------------------------------------------------ correction
-template <int HD>
+template <int HD, int MODE>
 __device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uint8_t* sV, uint32_t tmem,
                                                 WaitCtl wc) {
-  using C = Cfg<HD>;
+  using C = Cfg<HD, MODE>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;
   const int row = quarter * 32 + lane;
@@ -476,7 +436,7 @@ __device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uin
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ++a_phase[t];
-      const float alpha = bars->alpha[t][row];
+      const float alpha = alpha_of(bars->alpha[t][row]);
       // the accumulator's earlier products are done: S_t of this tile was
       // issued after them
       if (i >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -506,40 +466,56 @@ __device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uin
   }
 }
 
-// ------------------------------------------------------------------ producer
-// The whole warp: lane x loads box x of each tile.  A box that holds no
-// visible key, or whose page number is not one of the pool's, is read from
-// behind the pool, which fills it with zeros; the latter also sets the status.
-template <int HD>
-__device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
-                                              const CUtensorMap* tmV, const Params& p, Bars* bars,
-                                              uint8_t* sQ, uint8_t* sK, uint8_t* sV, WaitCtl wc) {
-  using C = Cfg<HD>;
+// ------------------------------------------------------------------ producers
+// One warp loads Q and K, another V; lane x loads box x of each tile.  A box
+// that holds no visible key, or whose page number is not one of the pool's, is
+// read from behind the pool, which fills it with zeros; the latter also sets
+// the status.
+template <int HD, bool kF16, int MODE, bool kV>
+__device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmKV, const Params& p,
+                                              Bars* bars, uint8_t* sQ, uint8_t* ring, uint8_t* slopes,
+                                              WaitCtl wc) {
+  using C = Cfg<HD, MODE>;
+  constexpr int kSlots = kV ? C::kVSlots : C::kKSlots;
+  uint64_t* const full = kV ? bars->v_full : bars->k_full;
+  uint64_t* const empty = kV ? bars->v_empty : bars->k_empty;
   const int lane = threadIdx.x & 31;
   const int boxes = BN / p.box_rows;
   const uint32_t q_bytes = static_cast<uint32_t>(p.tok_tile * p.group * HD * 2);
-  uint32_t kc = 0, seg = 0;  // key tiles and segments so far
+  uint32_t n = 0, seg = 0;  // tiles and segments so far
   bool ok = true;
   for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
-    if (seg > 0) {
-      ok = warp_wait(&bars->q_empty, (seg - 1) & 1u, wc, kSiteQEmpty);
-      if (!ok) break;
-    }
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&bars->q_full, q_bytes);
+    if constexpr (!kV) {
+      if (seg > 0) {
+        ok = warp_wait(&bars->q_empty, (seg - 1) & 1u, wc, kSiteQEmpty);
+        if (!ok) break;
+      }
+      if constexpr (MODE == kModSlopes) {
+        if (slopes_linear(p, w.hk)) {
+          for (int row = lane; row < 128; row += 32) {
+            const int tl = row / p.group, tok = w.rt * p.tok_tile + tl;
+            const bool live = tl < p.tok_tile && tok < p.T;
+            const float slope = live ? __ldg(p.slopes + w.hk * p.group + row - tl * p.group) : 0.f;
+            slope_fill_q<kF16>(slopes + kSlopeRowsBytes, row, slope, p.scale);
+          }
+          fence_proxy_async();
+        }
+        __syncwarp();
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars->q_full, q_bytes);
 #pragma unroll
-      for (int cb = 0; cb < HD / 64; ++cb)
-        tma_load_4d(sQ + cb * BM * 128, tmQ, &bars->q_full, cb * 64, w.hk * p.group,
-                    w.rt * p.tok_tile, w.b);
+        for (int cb = 0; cb < HD / 64; ++cb)
+          tma_load_4d(sQ + cb * BM * 128, tmQ, &bars->q_full, cb * 64, w.hk * p.group, w.rt * p.tok_tile, w.b);
+      }
     }
     const int lo = first_key(p, w.ctx), end = w.ctx + p.T;
-    for (int i = 0; ok && i < w.n; ++i, ++kc) {
-      const int s = static_cast<int>(kc % C::kKSlots), sv = static_cast<int>(kc % C::kVSlots);
-      const uint32_t use = kc / C::kKSlots, use_v = kc / C::kVSlots;
-      const int k0 = (w.tile0 + i) * BN;
+    for (int i = 0; ok && i < w.n; ++i) {
+      const int s = static_cast<int>(n % kSlots);
+      const uint32_t use = n / kSlots;
       int page = p.num_pages, in_page = 0;
       if (lane < boxes) {
-        const int key = k0 + lane * p.box_rows;
+        const int key = (w.tile0 + i) * BN + lane * p.box_rows;
         if (key < end && key + p.box_rows > lo) {
           const int at = key / p.page;  // < max_pages: ctx + T fits the table
           in_page = key - at * p.page;
@@ -550,55 +526,45 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUte
           }
         }
       }
-      if (use > 0) ok = warp_wait(&bars->k_empty[s], (use - 1) & 1u, wc, kSiteKEmpty);
+      if (use > 0) ok = warp_wait(&empty[s], (use - 1) & 1u, wc, kV ? kSiteVEmpty : kSiteKEmpty);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[s], C::kTileBytes);
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], C::kTileBytes);
       __syncwarp();
       if (lane < boxes)
 #pragma unroll
         for (int cb = 0; cb < HD / 64; ++cb)
-          tma_load_4d(sK + s * C::kTileBytes + cb * BN * 128 + lane * p.box_rows * 128, tmK,
-                      &bars->k_full[s], cb * 64, in_page, w.hk, page);
-      if (use_v > 0) ok = warp_wait(&bars->v_empty[sv], (use_v - 1) & 1u, wc, kSiteVEmpty);
-      if (!ok) {
-        ++kc;  // this K tile is in flight: the drain below covers it
-        break;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[sv], C::kTileBytes);
-      __syncwarp();
-      if (lane < boxes)
-#pragma unroll
-        for (int cb = 0; cb < HD / 64; ++cb)
-          tma_load_4d(sV + sv * C::kTileBytes + cb * BN * 128 + lane * p.box_rows * 128, tmV,
-                      &bars->v_full[sv], cb * 64, in_page, w.hk, page);
+          tma_load_4d(ring + s * C::kTileBytes + cb * BN * 128 + lane * p.box_rows * 128, tmKV, &full[s],
+                      cb * 64, in_page, w.hk, page);
+      ++n;
     }
-    if (!ok) break;
+    if (!ok) {
+      ++seg;  // its Q is in flight
+      break;
+    }
   }
-  // Let every load of this warp land before the CTA can exit (a V tile that
-  // was not issued makes its wait run into the limit, on the give-up path only).
-  if (lane == 0 && kc > 0) {
-    const uint32_t q_uses = ok ? seg : seg + 1;
-    if (q_uses > 0) drain_wait(&bars->q_full, (q_uses - 1) & 1u, wc.limit_ns);
-    for (uint32_t x = (kc > C::kKSlots ? kc - C::kKSlots : 0); x < kc; ++x)
-      drain_wait(&bars->k_full[x % C::kKSlots], (x / C::kKSlots) & 1u, wc.limit_ns);
-    for (uint32_t x = (kc > C::kVSlots ? kc - C::kVSlots : 0); x < kc; ++x)
-      drain_wait(&bars->v_full[x % C::kVSlots], (x / C::kVSlots) & 1u, wc.limit_ns);
+  // Let every load of this warp land before the CTA can exit.
+  if (lane == 0) {
+    if (!kV && seg > 0) drain_wait(&bars->q_full, (seg - 1) & 1u, wc.limit_ns);
+    for (uint32_t x = (n > kSlots ? n - kSlots : 0); x < n; ++x)
+      drain_wait(&full[x % kSlots], (x / kSlots) & 1u, wc.limit_ns);
   }
   __syncwarp();
 }
 
 // ------------------------------------------------------------------ MMA issuer
-template <int HD, bool kF16>
+template <int HD, bool kF16, int MODE>
 __device__ __forceinline__ void mma_role(const Params& p, Bars* bars, uint32_t tmem, uint8_t* sQ,
-                                         uint8_t* sK, uint8_t* sV, WaitCtl wc) {
-  using C = Cfg<HD>;
+                                         uint8_t* sK, uint8_t* sV, uint8_t* slopes, WaitCtl wc) {
+  using C = Cfg<HD, MODE>;
   const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
   const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);        // slot 0, K-major
   const uint64_t v_desc = sdesc_sw128(smem_u32(sV), BN * 128, 1024);  // slot 0, MN-major
   constexpr uint64_t kStep = static_cast<uint64_t>(C::kTileBytes >> 4);
+  const uint32_t s_id = idesc_f16_f32(128, 128, 0, kF16) | p.neg_q;
   uint32_t kc = 0, vc = 0, seg = 0, p_phase[2] = {0, 0};
   bool ok = true;
   for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
+    [[maybe_unused]] const bool linear = MODE == kModSlopes && slopes_linear(p, w.hk);
     ok = warp_wait(&bars->q_full, seg & 1u, wc, kSiteQ);
     if (!ok) break;
     // scores of tile i into buffer i mod 2
@@ -606,7 +572,12 @@ __device__ __forceinline__ void mma_role(const Params& p, Bars* bars, uint32_t t
       const uint32_t s = kc % C::kKSlots;
       if (!warp_wait(&bars->k_full[s], (kc / C::kKSlots) & 1u, wc, kSiteK)) return false;
       tc_fence_after_sync();
-      mma_abt_128<HD, kF16, true>(tmem + (i & 1) * BN, q_desc, k_desc + s * kStep);
+      mma_abt_id<HD>(tmem + (i & 1) * BN, q_desc, k_desc + s * kStep, s_id);
+      if constexpr (MODE == kModSlopes) {
+        if (linear && (w.tile0 + i + 1) * BN <= w.ctx)  // not where drafts are
+          mma_ss_k<1, true>(tmem + (i & 1) * BN, slope_rows_desc(smem_u32(slopes) + kSlopeRowsBytes),
+                            slope_rows_desc(smem_u32(slopes)), idesc_f16_f32(128, 128, 0, kF16));
+      }
       mma_commit<true>(&bars->s_full[i & 1]);
       mma_commit<true>(&bars->k_empty[s]);
       if (i == w.n - 1) mma_commit<true>(&bars->q_empty);
@@ -698,14 +669,17 @@ template <int HD, bool kF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const Params p) {
-  using C = Cfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  using C = Cfg<HD, MODE>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // see fwd_mod_kernel
+    if (threadIdx.x == 0) atomicExch(p.status, 3u /* OSATTN_ERR_CUDA */);
+    return;
+  }
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::kTileBytes;
   uint8_t* sV = sK + C::kKSlots * C::kTileBytes;
-  Bars* bars = reinterpret_cast<Bars*>(smem + C::kTileRegion);
+  uint8_t* slopes = smem + C::kTileRegion;
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kTileRegion + C::kTableBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -742,9 +716,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  // rows of Q that no load writes (tok_tile * group < 128) stay zero
-  for (int x = threadIdx.x; x < C::kTileBytes / 16; x += kThreads)
-    reinterpret_cast<uint4*>(sQ)[x] = make_uint4(0u, 0u, 0u, 0u);
+  // rows of Q that no load writes stay zero
+  if (p.tok_tile * p.group < BM)
+    for (int x = threadIdx.x; x < C::kTileBytes / 16; x += kThreads)
+      reinterpret_cast<uint4*>(sQ)[x] = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (MODE == kModSlopes) {
+    if (threadIdx.x < BN) slope_fill_k<kF16>(slopes, threadIdx.x);
+  }
   fence_proxy_async();
   __syncthreads();
   find_start(p, bars);
@@ -760,13 +738,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_role<HD, kF16, MODE>(p, bars, tmem, warp >> 2, wc);
   } else if (warp < kProducerWarp) {
     regs_dec<88>();
-    correction_role<HD>(p, bars, sV, tmem, wc);
+    correction_role<HD, MODE>(p, bars, sV, tmem, wc);
   } else {
     regs_dec<56>();
     if (warp == kProducerWarp)
-      producer_role<HD>(&tmQ, &tmK, &tmV, p, bars, sQ, sK, sV, wc);
+      producer_role<HD, kF16, MODE, false>(&tmQ, &tmK, p, bars, sQ, sK, slopes, wc);
+    else if (warp == kProducerVWarp)
+      producer_role<HD, kF16, MODE, true>(&tmQ, &tmV, p, bars, sQ, sV, slopes, wc);
     else if (warp == kMmaWarp)
-      mma_role<HD, kF16>(p, bars, tmem, sQ, sK, sV, wc);
+      mma_role<HD, kF16, MODE>(p, bars, tmem, sQ, sK, sV, slopes, wc);
   }
 
   __syncwarp();
@@ -841,13 +821,13 @@ constexpr int kLaunchRegs = 128;  // the setmaxnreg split above assumes it
 
 template <int HD, bool kF16, int MODE>
 cudaError_t set_attrs() {
-  static_assert(smem_bytes<HD>() <= 232448, "shared memory per CTA");
+  static_assert(smem_bytes<HD, MODE>() <= 232448, "shared memory per CTA");
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, tree_kernel<HD, kF16, MODE>);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(tree_kernel<HD, kF16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smem_bytes<HD>());
+                              smem_bytes<HD, MODE>());
 }
 
 template <int HD, bool kF16>
@@ -862,7 +842,7 @@ cudaError_t prepare() {
 template <int HD, bool kF16, int MODE>
 cudaError_t launch_mode(int grid, cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k,
                         const CUtensorMap& v, const Params& p) {
-  tree_kernel<HD, kF16, MODE><<<grid, kThreads, smem_bytes<HD>(), s>>>(q, k, v, p);
+  tree_kernel<HD, kF16, MODE><<<grid, kThreads, smem_bytes<HD, MODE>(), s>>>(q, k, v, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.row_tiles * ((p.slot_rows + 7) / 8);
@@ -894,9 +874,10 @@ cudaError_t launch(const TreeArgs& a, const CUtensorMap& q, const CUtensorMap& k
   p.num_pages = a.num_pages;
   p.box_rows = a.page < BN ? a.page : BN;
   p.window = a.window;
-  p.scale_log2 = a.scale * kModLog2e;
-  p.cap_c1 = a.softcap > 0.f ? 2.f * a.scale * kModLog2e / a.softcap : 0.f;
-  p.cap2 = a.softcap * kModLog2e;
+  p.scale = positive_scale(a.scale);
+  p.scale_log2 = p.scale * kModLog2e;
+  p.neg_q = a.scale < 0.f ? kIdescNegA : 0u;
+  p.cap = make_cap(p.scale, a.softcap);
   p.slopes = a.slopes;
   p.slot_rows = tree_slot_rows(p.group, a.T);
   const int grid = a.num_sms < kTreeMaxCtas ? a.num_sms : kTreeMaxCtas;

@@ -558,41 +558,40 @@ class MaskPlan:
         self.buffer, self.B, self.Nq, self.Nkv, self.q_offset = buffer, B, Nq, Nkv, q_offset
 
 
-def _int32(t, shape, device, name):
+def _int32(t, shape, index, name):
     import torch
 
     if t is None:
         return None
-    if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape:
+    if t.dtype != torch.int32 or not t.is_cuda or t.shape != shape:
         raise ValueError(f"{name} must be a CUDA int32 tensor of shape {list(shape)}")
-    if t.device != device:
+    if t.get_device() != index:
         raise ValueError(f"{name} is on another device")
     return t.contiguous()
 
 
-def _on(device):
-    """The context of calls for tensors of `device`."""
-    import contextlib
-
+def _raw_stream(index):
+    """Handle of torch's current stream on device `index`."""
     import torch
 
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _stream_for(stream, device):
+def _handle(stream, index):
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _elsewhere(index):
+    """Whether another device than `index` is current."""
     import torch
 
-    return torch.cuda.current_stream(device) if stream is None else stream
+    return torch.cuda.current_device() != index
 
 
-def _keep(stream, device, *tensors):
-    """Temporaries of this call, used on `stream`: not to be handed out again
-    before the work there is done."""
-    import torch
-
-    if stream != torch.cuda.current_stream(device):
+def _keep(stream, index, tensors):
+    """Temporaries of a call that was given `stream`: not to be handed out
+    again before the work there is done."""
+    if stream is not None and stream.cuda_stream != _raw_stream(index):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
@@ -630,37 +629,38 @@ def mask_plan(B: int, Nq: int, Nkv: int, causal: bool = False, window: int = 0, 
     MaskPlan of the same B and Nq to overwrite."""
     import torch
 
-    B, Nq, Nkv, window, q_offset = int(B), int(Nq), int(Nkv), int(window), int(q_offset)
-    for t in (key_len, prefix_len, doc_ids):
-        if t is not None:
-            device = t.device if device is None else torch.device(device)
-            break
-    if device is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    device = torch.device(device)
+    masks = (key_len, prefix_len, doc_ids)
+    for t in masks:
+        if t is not None and device is None:
+            device = t.device
+    device = torch.device("cuda" if device is None else device)
     if device.type != "cuda":
         raise ValueError("a mask plan lives on a CUDA device")
-    if device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    key_len = _int32(key_len, (B,), device, "key_len")
-    prefix_len = _int32(prefix_len, (B,), device, "prefix_len")
-    doc_ids = _int32(doc_ids, (B, Nkv), device, "doc_ids")
-    need = int(lib().osattn_mask_plan_bytes(B, Nq))
-    with _on(device):
-        stream = _stream_for(stream, device)
-        if out is None:
-            buffer = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-            _keep(stream, device, buffer)
-        else:
-            buffer = out.buffer
-            if out.B != B or out.Nq != Nq or buffer.device != device:
-                raise ValueError("out must be a MaskPlan of the same B, Nq and device")
-        st = lib().osattn_mask_plan(buffer.data_ptr(), buffer.numel(), B, Nq, Nkv, q_offset,
-                                    int(bool(causal)), window, *(
-                                        None if t is None else t.data_ptr()
-                                        for t in (key_len, prefix_len, doc_ids)),
-                                    stream.cuda_stream)
-        _keep(stream, device, key_len, prefix_len, doc_ids)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return mask_plan(B, Nq, Nkv, causal, window, q_offset, *masks, device=f"cuda:{index}", out=out,
+                             stream=stream)
+    B, Nq, Nkv, window, q_offset = int(B), int(Nq), int(Nkv), int(window), int(q_offset)
+    key_len = _int32(key_len, (B,), index, "key_len")
+    prefix_len = _int32(prefix_len, (B,), index, "prefix_len")
+    doc_ids = _int32(doc_ids, (B, Nkv), index, "doc_ids")
+    made = [key_len, prefix_len, doc_ids]
+    if out is None:
+        # tiles of 128 rows take 16 bytes each, rows 8
+        need = max(B, 0) * ((max(Nq, 0) + 127) // 128 * 16 + max(Nq, 0) * 8)
+        buffer = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        made.append(buffer)
+    else:
+        buffer = out.buffer
+        if out.B != B or out.Nq != Nq or buffer.get_device() != index:
+            raise ValueError("out must be a MaskPlan of the same B, Nq and device")
+    st = lib().osattn_mask_plan(buffer.data_ptr(), buffer.numel(), B, Nq, Nkv, q_offset,
+                                1 if causal else 0, window,
+                                None if key_len is None else key_len.data_ptr(),
+                                None if prefix_len is None else prefix_len.data_ptr(),
+                                None if doc_ids is None else doc_ids.data_ptr(), _handle(stream, index))
+    _keep(stream, index, made)
     if st != OK:
         raise OsattnError(st, "osattn_mask_plan")
     if out is not None:
@@ -699,47 +699,66 @@ def _mod_shapes(q, k, v):
         raise ValueError("q must be [B, H, Nq, d], k and v [B, Hkv, Nkv, d]")
     B, H, Nq, d = q.shape
     Hkv, Nkv = k.shape[1], k.shape[2]
-    if tuple(k.shape) != (B, Hkv, Nkv, d) or v.shape != k.shape:
+    if k.shape != (B, Hkv, Nkv, d) or v.shape != k.shape:
         raise ValueError("k and v must be [B, Hkv, Nkv, d] matching q")
     if Hkv < 1 or H % Hkv:
         raise ValueError("the number of key/value heads must divide the number of query heads")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must share one dtype")
-    if not (q.is_cuda and k.is_cuda and v.is_cuda):
+    if not q.is_cuda:
         raise ValueError("q, k, v must be CUDA tensors")
-    if k.device != q.device or v.device != q.device:
+    index = q.get_device()
+    if k.get_device() != index or v.get_device() != index:
         raise ValueError("q, k, v must be on one device")
-    return B, H, Hkv, Nq, Nkv, d
+    return B, H, Hkv, Nq, Nkv, d, index
 
 
-def _score(q, plan, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map):
+def _slopes(slopes, H, index):
+    import torch
+
+    if slopes.shape != (H,) or slopes.dtype != torch.float32 or slopes.get_device() != index:
+        raise ValueError("slopes must be an fp32 tensor of shape [H] on q's device")
+    return slopes.contiguous()
+
+
+def _score(q, plan, index, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map):
     """struct osattn_score of a call, and the tensors it points into."""
     import torch
 
-    s = _Score(softcap=float(softcap))
+    s = _Score(softcap)
+    held = []
     if plan is not None:
-        if (plan.B, plan.Nq, plan.Nkv) != (B, Nq, Nkv) or plan.buffer.device != q.device:
+        if (plan.B, plan.Nq, plan.Nkv) != (B, Nq, Nkv) or plan.buffer.get_device() != index:
             raise ValueError("plan was made for other sizes or another device")
         s.q_offset = plan.q_offset
-    held = []
     if slopes is not None:
-        if tuple(slopes.shape) != (H,) or slopes.dtype != torch.float32 or slopes.device != q.device:
-            raise ValueError("slopes must be an fp32 tensor of shape [H] on q's device")
-        held.append(slopes.contiguous())
+        held.append(_slopes(slopes, H, index))
         s.slopes = held[-1].data_ptr()
     if (rel_table is None) != (rel_map is None):
         raise ValueError("rel_table and rel_map go together")
     if rel_table is not None:
         if (rel_table.dim() != 2 or rel_table.shape[1] != H or rel_table.dtype != q.dtype
-                or rel_table.device != q.device):
+                or rel_table.get_device() != index):
             raise ValueError("rel_table must be [buckets, H] with q's dtype and device")
         if (rel_map.dim() != 1 or rel_map.numel() % 2 == 0 or rel_map.dtype != torch.int32
-                or rel_map.device != q.device):
+                or rel_map.get_device() != index):
             raise ValueError("rel_map must be int32 [2 R + 1] on q's device")
         held += [rel_table.contiguous(), rel_map.contiguous()]
         s.rel_table, s.rel_map = held[-2].data_ptr(), held[-1].data_ptr()
         s.rel_num, s.rel_range = rel_table.shape[0], rel_map.numel() // 2
     return s, held
+
+
+def _lse(lse, shape, index, device):
+    """The caller's LSE tensor, or a new one."""
+    import torch
+
+    if lse is None:
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    if (lse.shape != shape or lse.dtype != torch.float32 or not lse.is_contiguous()
+            or lse.get_device() != index):
+        raise ValueError(f"lse must be contiguous fp32 {list(shape)} on q's device")
+    return lse
 
 
 def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0, slopes=None,
@@ -756,34 +775,25 @@ def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0
     no key gets O = 0 and LSE = -inf."""
     import torch
 
-    B, H, Hkv, Nq, Nkv, d = _mod_shapes(q, k, v)
+    B, H, Hkv, Nq, Nkv, d, index = _mod_shapes(q, k, v)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return fwd_mod(q, k, v, scale, plan, softcap, slopes, rel_table, rel_map, out, lse, stream)
     dtype = _dtype_code(q)
-    score, held = _score(q, plan, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    device = q.device
-    with _on(device):
-        stream = _stream_for(stream, device)
-        made = []
-        if out is None:
-            out = torch.empty_like(q)
-            made.append(out)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != device:
-            raise ValueError("out must match q")
-        if lse is None:
-            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=device)
-            made.append(lse)
-        elif (tuple(lse.shape) != (B, H, Nq) or lse.dtype != torch.float32
-              or not lse.is_contiguous() or lse.device != device):
-            raise ValueError("lse must be contiguous fp32 [B, H, Nq] on q's device")
-        st = lib().osattn_fwd_mod(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq,
-            Nkv, d, _view_strides(q, "q"), _view_strides(k, "k"), _view_strides(v, "v"),
-            _view_strides(out, "out"), float(scale), ctypes.byref(score),
-            None if plan is None else plan.buffer.data_ptr(), dtype, stream.cuda_stream)
-        _keep(stream, device, *made, *held)
+    score, held = _score(q, plan, index, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index:
+        raise ValueError("out must match q")
+    lse = _lse(lse, (B, H, Nq), index, q.device)
+    st = lib().osattn_fwd_mod(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, Nkv, d,
+        _view_strides(q, "q"), _view_strides(k, "k"), _view_strides(v, "v"), _view_strides(out, "out"),
+        1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(score),
+        None if plan is None else plan.buffer.data_ptr(), dtype, _handle(stream, index))
     if st != OK:
         raise OsattnError(st, "osattn_fwd_mod")
+    _keep(stream, index, (out, lse, *held))
     return out, lse
 
 
@@ -801,52 +811,49 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
     bwd_mod_workspace_bytes(B, H, Nq, R or 0) bytes) may be given."""
     import torch
 
-    B, H, Hkv, Nq, Nkv, d = _mod_shapes(q, k, v)
+    B, H, Hkv, Nq, Nkv, d, index = _mod_shapes(q, k, v)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return bwd_mod(q, k, v, o, lse, do, scale, plan, softcap, slopes, rel_table, rel_map, dq, dk, dv,
+                           drel, workspace, stream)
     dtype = _dtype_code(q)
-    device = q.device
     for t in (o, do):
-        if t.shape != q.shape or t.dtype != q.dtype or t.device != device:
+        if t.shape != q.shape or t.dtype != q.dtype or t.get_device() != index:
             raise ValueError("o and do must be shaped, typed and placed like q")
-    if (tuple(lse.shape) != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()
-            or lse.device != device):
-        raise ValueError("lse must be contiguous fp32 [B, H, Nq] on q's device")
-    score, held = _score(q, plan, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map)
-    if drel is not None and rel_table is None:
-        raise ValueError("drel needs a rel_table")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with _on(device):
-        stream = _stream_for(stream, device)
-        made = []
-        grads = []
-        for g, ref in ((dq, q), (dk, k), (dv, v), (drel, rel_table)):
-            if g is None and ref is not None:
-                g = torch.empty_like(ref, memory_format=torch.contiguous_format) \
-                    if ref is rel_table else torch.empty_like(ref)
-                made.append(g)
-            elif g is not None and (g.shape != ref.shape or g.dtype != ref.dtype or g.device != device):
-                raise ValueError("gradients must be shaped, typed and placed like their tensors")
-            grads.append(g)
-        dq, dk, dv, drel = grads
-        if drel is not None and not drel.is_contiguous():
+    _lse(lse, (B, H, Nq), index, None)
+    score, held = _score(q, plan, index, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map)
+
+    def grad(g, ref):
+        if g is None:
+            return torch.empty_like(ref)
+        if g.shape != ref.shape or g.dtype != ref.dtype or g.get_device() != index:
+            raise ValueError("gradients must be shaped, typed and placed like their tensors")
+        return g
+
+    dq, dk, dv = grad(dq, q), grad(dk, k), grad(dv, v)
+    if rel_table is not None:
+        drel = grad(drel, held[-2])  # the contiguous table
+        if not drel.is_contiguous():
             raise ValueError("drel must be contiguous")
-        if workspace is None:
-            workspace = torch.empty(bwd_mod_workspace_bytes(B, H, Nq, score.rel_range),
-                                    dtype=torch.uint8, device=device)
-            made.append(workspace)
-        elif not workspace.is_contiguous() or workspace.device != device:
-            raise ValueError("workspace must be contiguous on q's device")
-        names = ("q", "k", "v", "o", "do", "dq", "dk", "dv")
-        ts = (q, k, v, o, do, dq, dk, dv)
-        st = lib().osattn_bwd_mod(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
-            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if drel is None else drel.data_ptr(), B,
-            H, Hkv, Nq, Nkv, d, *(_view_strides(t, n) for t, n in zip(ts, names)), float(scale),
-            ctypes.byref(score), None if plan is None else plan.buffer.data_ptr(), dtype,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream.cuda_stream)
-        _keep(stream, device, *made, *held)
+    elif drel is not None:
+        raise ValueError("drel needs a rel_table")
+    L = lib()
+    if workspace is None:
+        need = L.osattn_bwd_mod_workspace_bytes(B, H, Nq, score.rel_range)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError("workspace must be contiguous on q's device")
+    st = L.osattn_bwd_mod(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if drel is None else drel.data_ptr(), B, H, Hkv,
+        Nq, Nkv, d, _view_strides(q, "q"), _view_strides(k, "k"), _view_strides(v, "v"),
+        _view_strides(o, "o"), _view_strides(do, "do"), _view_strides(dq, "dq"), _view_strides(dk, "dk"),
+        _view_strides(dv, "dv"), 1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(score),
+        None if plan is None else plan.buffer.data_ptr(), dtype, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _handle(stream, index))
     if st != OK:
         raise OsattnError(st, "osattn_bwd_mod")
+    _keep(stream, index, (dq, dk, dv, drel, workspace, *held))
     return (dq, dk, dv) if drel is None else (dq, dk, dv, drel)
 
 
@@ -874,61 +881,52 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
         raise ValueError("q must be [B, H, T, d], k_pages and v_pages [pages, Hkv, page_size, d]")
     B, H, T, d = q.shape
     pages, Hkv, page_size, dk = k_pages.shape
-    device = q.device
     if dk != d or Hkv < 1 or H % Hkv:
         raise ValueError("k_pages must have q's d and a number of heads that divides q's")
     if k_pages.dtype != q.dtype or v_pages.dtype != q.dtype:
         raise TypeError("q, k_pages, v_pages must share one dtype")
-    dtype = _dtype_code(q)
-    if not q.is_cuda or k_pages.device != device or v_pages.device != device:
+    index = q.get_device()
+    if not q.is_cuda or k_pages.get_device() != index or v_pages.get_device() != index:
         raise ValueError("q, k_pages, v_pages must be CUDA tensors on one device")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask, scale, softcap, slopes,
+                             window, out, lse, workspace, stream)
+    dtype = _dtype_code(q)
     max_pages = page_table.shape[1]
-    page_table = _int32(page_table, (B, max_pages), device, "page_table")
-    ctx_len = _int32(ctx_len, (B,), device, "ctx_len")
+    page_table = _int32(page_table, (B, max_pages), index, "page_table")
+    ctx_len = _int32(ctx_len, (B,), index, "ctx_len")
     if tree_mask is not None:
-        if (tree_mask.dtype != torch.int64 or tuple(tree_mask.shape) != (B, T)
-                or tree_mask.device != device):
+        if (tree_mask.dtype != torch.int64 or tree_mask.shape != (B, T)
+                or tree_mask.get_device() != index):
             raise ValueError("tree_mask must be int64 [B, T] on q's device")
         tree_mask = tree_mask.contiguous()
     if slopes is not None:
-        if tuple(slopes.shape) != (H,) or slopes.dtype != torch.float32 or slopes.device != device:
-            raise ValueError("slopes must be an fp32 tensor of shape [H] on q's device")
-        slopes = slopes.contiguous()
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with _on(device):
-        stream = _stream_for(stream, device)
-        made = []
-        if out is None:
-            out = torch.empty_like(q)
-            made.append(out)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != device:
-            raise ValueError("out must match q")
-        if lse is None:
-            lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
-            made.append(lse)
-        elif (tuple(lse.shape) != (B, H, T) or lse.dtype != torch.float32
-              or not lse.is_contiguous() or lse.device != device):
-            raise ValueError("lse must be contiguous fp32 [B, H, T] on q's device")
-        if workspace is None:
-            workspace = torch.empty(max(tree_workspace_bytes(B, H, Hkv, T, d), 16),
-                                    dtype=torch.uint8, device=device)
-            made.append(workspace)
-        elif not workspace.is_contiguous() or workspace.device != device:
-            raise ValueError("workspace must be contiguous on q's device")
-        st = lib().osattn_tree_attn(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-            ctx_len.data_ptr(), None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(),
-            lse.data_ptr(), B, H, Hkv, T, d, pages, page_size, max_pages, _view_strides(q, "q"),
-            _view_strides(k_pages, "k_pages"), _view_strides(v_pages, "v_pages"),
-            _view_strides(out, "out"), float(scale), float(softcap),
-            None if slopes is None else slopes.data_ptr(), int(window), dtype, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), stream.cuda_stream)
-        _keep(stream, device, *made, page_table, ctx_len, tree_mask, slopes)
+        slopes = _slopes(slopes, H, index)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index:
+        raise ValueError("out must match q")
+    lse = _lse(lse, (B, H, T), index, q.device)
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(max(L.osattn_tree_workspace_bytes(B, H, Hkv, T, d), 16),
+                                dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError("workspace must be contiguous on q's device")
+    st = L.osattn_tree_attn(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), ctx_len.data_ptr(),
+        None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, T,
+        d, pages, page_size, max_pages, _view_strides(q, "q"), _view_strides(k_pages, "k_pages"),
+        _view_strides(v_pages, "v_pages"), _view_strides(out, "out"),
+        1.0 / math.sqrt(d) if scale is None else scale, softcap,
+        None if slopes is None else slopes.data_ptr(), int(window), dtype, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _handle(stream, index))
     if st != OK:
         raise OsattnError(st, "osattn_tree_attn")
+    _keep(stream, index, (out, lse, workspace, page_table, ctx_len, tree_mask, slopes))
     return out, lse
 
 
