@@ -16,6 +16,8 @@ import math
 import os
 import threading
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libosattn.so")
 
@@ -548,6 +550,9 @@ def softmax_rows_offload(x_host, out_host=None, lse_host=None, x=None, out=None,
 
 
 # ---------------------------------------------------------------- modified scores
+_CODES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
 class MaskPlan:
     """Which keys each query row sees: what mask_plan() returns and fwd_mod()
     and bwd_mod() take.  `buffer` is private to the library."""
@@ -559,8 +564,6 @@ class MaskPlan:
 
 
 def _int32(t, shape, index, name):
-    import torch
-
     if t is None:
         return None
     if t.dtype != torch.int32 or not t.is_cuda or t.shape != shape:
@@ -572,19 +575,15 @@ def _int32(t, shape, index, name):
 
 def _raw_stream(index):
     """Handle of torch's current stream on device `index`."""
-    import torch
-
     return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _handle(stream, index):
-    return _raw_stream(index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _elsewhere(index):
     """Whether another device than `index` is current."""
-    import torch
-
     return torch.cuda.current_device() != index
 
 
@@ -609,8 +608,9 @@ def _view_strides(t, name):
     b, h, n, one = t.stride()
     if one != 1:
         raise ValueError(f"the last (d) axis of {name} must have stride 1")
-    if min(t.shape) == 1:
-        B, H, N, d = t.shape
+    shape = t.shape
+    if 1 in shape:
+        B, H, N, d = shape
         n = d if N == 1 else n
         h = max(n * N, 8) if H == 1 else h
         b = max(h * H, 8) if B == 1 else b
@@ -627,8 +627,6 @@ def mask_plan(B: int, Nq: int, Nkv: int, causal: bool = False, window: int = 0, 
     |j - p| < window; with doc_ids ([B, Nkv] int32) j and p lie in one run of
     equal, non-negative ids.  key_len, prefix_len: CUDA int32 [B].  `out`: a
     MaskPlan of the same B and Nq to overwrite."""
-    import torch
-
     masks = (key_len, prefix_len, doc_ids)
     for t in masks:
         if t is not None and device is None:
@@ -655,7 +653,7 @@ def mask_plan(B: int, Nq: int, Nkv: int, causal: bool = False, window: int = 0, 
         buffer = out.buffer
         if out.B != B or out.Nq != Nq or buffer.get_device() != index:
             raise ValueError("out must be a MaskPlan of the same B, Nq and device")
-    st = lib().osattn_mask_plan(buffer.data_ptr(), buffer.numel(), B, Nq, Nkv, q_offset,
+    st = (_lib or lib()).osattn_mask_plan(buffer.data_ptr(), buffer.numel(), B, Nq, Nkv, q_offset,
                                 1 if causal else 0, window,
                                 None if key_len is None else key_len.data_ptr(),
                                 None if prefix_len is None else prefix_len.data_ptr(),
@@ -676,8 +674,6 @@ def rel_buckets(num_buckets: int, max_distance: int, bidirectional: bool = True)
     rest share buckets spaced by the logarithm up to max_distance; with
     `bidirectional` one half of the buckets is for keys behind the query,
     otherwise all such keys fall into bucket 0.  A CPU tensor."""
-    import torch
-
     num_buckets, max_distance = int(num_buckets), int(max_distance)
     n = num_buckets // 2 if bidirectional else num_buckets
     small = n // 2
@@ -714,8 +710,6 @@ def _mod_shapes(q, k, v):
 
 
 def _slopes(slopes, H, index):
-    import torch
-
     if slopes.shape != (H,) or slopes.dtype != torch.float32 or slopes.get_device() != index:
         raise ValueError("slopes must be an fp32 tensor of shape [H] on q's device")
     return slopes.contiguous()
@@ -723,8 +717,6 @@ def _slopes(slopes, H, index):
 
 def _score(q, plan, index, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map):
     """struct osattn_score of a call, and the tensors it points into."""
-    import torch
-
     s = _Score(softcap)
     held = []
     if plan is not None:
@@ -749,12 +741,10 @@ def _score(q, plan, index, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map):
     return s, held
 
 
-def _lse(lse, shape, index, device):
+def _lse(lse, shape, index, like):
     """The caller's LSE tensor, or a new one."""
-    import torch
-
     if lse is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
+        return like.new_empty(shape, dtype=torch.float32)
     if (lse.shape != shape or lse.dtype != torch.float32 or not lse.is_contiguous()
             or lse.get_device() != index):
         raise ValueError(f"lse must be contiguous fp32 {list(shape)} on q's device")
@@ -773,20 +763,20 @@ def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0
     (rel_table: [buckets, H] in q's dtype; rel_map: int32 [2 R + 1], see
     rel_buckets()).  plan: a MaskPlan, or None for no mask.  A row that sees
     no key gets O = 0 and LSE = -inf."""
-    import torch
-
     B, H, Hkv, Nq, Nkv, d, index = _mod_shapes(q, k, v)
     if _elsewhere(index):
         with torch.cuda.device(index):
             return fwd_mod(q, k, v, scale, plan, softcap, slopes, rel_table, rel_map, out, lse, stream)
-    dtype = _dtype_code(q)
+    dtype = _CODES.get(q.dtype)
+    if dtype is None:
+        raise TypeError("tensors must be bf16 or fp16")
     score, held = _score(q, plan, index, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map)
     if out is None:
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index:
         raise ValueError("out must match q")
-    lse = _lse(lse, (B, H, Nq), index, q.device)
-    st = lib().osattn_fwd_mod(
+    lse = _lse(lse, (B, H, Nq), index, q)
+    st = (_lib or lib()).osattn_fwd_mod(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, Nkv, d,
         _view_strides(q, "q"), _view_strides(k, "k"), _view_strides(v, "v"), _view_strides(out, "out"),
         1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(score),
@@ -809,14 +799,14 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
     fwd_mod(); dk and dv are summed over the query heads of a key head.
     Outputs and the workspace (a CUDA uint8 tensor of at least
     bwd_mod_workspace_bytes(B, H, Nq, R or 0) bytes) may be given."""
-    import torch
-
     B, H, Hkv, Nq, Nkv, d, index = _mod_shapes(q, k, v)
     if _elsewhere(index):
         with torch.cuda.device(index):
             return bwd_mod(q, k, v, o, lse, do, scale, plan, softcap, slopes, rel_table, rel_map, dq, dk, dv,
                            drel, workspace, stream)
-    dtype = _dtype_code(q)
+    dtype = _CODES.get(q.dtype)
+    if dtype is None:
+        raise TypeError("tensors must be bf16 or fp16")
     for t in (o, do):
         if t.shape != q.shape or t.dtype != q.dtype or t.get_device() != index:
             raise ValueError("o and do must be shaped, typed and placed like q")
@@ -837,10 +827,10 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
             raise ValueError("drel must be contiguous")
     elif drel is not None:
         raise ValueError("drel needs a rel_table")
-    L = lib()
+    L = _lib or lib()
     if workspace is None:
         need = L.osattn_bwd_mod_workspace_bytes(B, H, Nq, score.rel_range)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError("workspace must be contiguous on q's device")
     st = L.osattn_bwd_mod(
@@ -875,8 +865,6 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
     softcap and slopes (fp32 [H]) as in fwd_mod(), with a window keys at a
     distance of at least `window` are hidden; a draft stands behind the
     context by the number of other drafts it sees."""
-    import torch
-
     if q.dim() != 4 or k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("q must be [B, H, T, d], k_pages and v_pages [pages, Hkv, page_size, d]")
     B, H, T, d = q.shape
@@ -894,7 +882,9 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
         with torch.cuda.device(index):
             return tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask, scale, softcap, slopes,
                              window, out, lse, workspace, stream)
-    dtype = _dtype_code(q)
+    dtype = _CODES.get(q.dtype)
+    if dtype is None:
+        raise TypeError("tensors must be bf16 or fp16")
     max_pages = page_table.shape[1]
     page_table = _int32(page_table, (B, max_pages), index, "page_table")
     ctx_len = _int32(ctx_len, (B,), index, "ctx_len")
@@ -909,11 +899,11 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index:
         raise ValueError("out must match q")
-    lse = _lse(lse, (B, H, T), index, q.device)
-    L = lib()
+    lse = _lse(lse, (B, H, T), index, q)
+    L = _lib or lib()
     if workspace is None:
-        workspace = torch.empty(max(L.osattn_tree_workspace_bytes(B, H, Hkv, T, d), 16),
-                                dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(max(L.osattn_tree_workspace_bytes(B, H, Hkv, T, d), 16),
+                                dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError("workspace must be contiguous on q's device")
     st = L.osattn_tree_attn(
