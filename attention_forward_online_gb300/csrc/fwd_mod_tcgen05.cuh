@@ -217,8 +217,6 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
     const bool masked = !(tile.lo_max <= k0 && tile.hi_min >= k0 + BN);
     const int lo = see.x - k0, hi = see.y - k0;
     auto bits_of = [&](int ch) { return bit_range(lo - 32 * ch, hi - 32 * ch); };
-    TileMask mk;
-    if (masked) mk.classify(bits_of);
     if constexpr (mode_slopes(MODE)) {
       const int d0 = k0 - pos;  // distance of the tile's first key
       const int side = linear ? slope_side(k0, p0, tile.left) : 0;
@@ -236,10 +234,17 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
       ts.near_lo = -R - 31 - first + 32 * quarter;
       ts.near_hi = R + 31 - first + 32 * quarter;
     }
-    ts.tile(s_addr, masked, mk, bits_of, ts.by_place(), m, l, [&](uint16_t alpha) {
+    auto publish = [&](uint16_t alpha) {
       bars->alpha[t][row] = alpha;
       mbar_arrive(&bars->alpha_full[t]);
-    });
+    };
+    TileMask mk;
+    if (masked) {
+      mk.classify(bits_of);
+      ts.template tile<true>(s_addr, mk, bits_of, ts.by_place(), m, l, publish);
+    } else {
+      ts.template tile<false>(s_addr, mk, bits_of, ts.by_place(), m, l, publish);
+    }
     tmem_st_wait();
     tc_fence_before_sync();
     mbar_arrive(&bars->p_full[t]);

@@ -154,13 +154,14 @@ struct TileScore {
   // first 64 columns.  Moves m, publishes the factor of the accumulator by
   // publish(alpha_bits) as soon as it is known, and updates l.
   // gap(e): the distance of key e of the tile, for both_sides.
-  template <typename BitsOf, typename Gap, typename Publish>
-  __device__ __forceinline__ void tile(uint32_t s_addr, bool masked, const TileMask& k, BitsOf&& bits_of,
-                                       Gap&& gap, float& m, float& l, Publish&& publish) const {
+  // kMasked: some rows of the warp may not see all of the tile.
+  template <bool kMasked, typename BitsOf, typename Gap, typename Publish>
+  __device__ __forceinline__ void tile(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
+                                       float& m, float& l, Publish&& publish) const {
     Row v;
     float top[kChunks];
     load_row(s_addr, v, top);
-    if (masked) {
+    if constexpr (kMasked) {
       // Masked scores, which may hold anything: out of the max, and 0 where
       // scores share a reciprocal.
 #pragma unroll
@@ -196,27 +197,80 @@ struct TileScore {
       // a row with no key so far has m_new = -inf and every x = -inf: against
       // 0 each p is exactly 0
       const float n = off - (m_new == -INFINITY ? 0.f : m_new);
-      sum = masked ? exps<true, true>(s_addr, v, k, bits_of, n) : exps<false, true>(s_addr, v, k, bits_of, n);
+      sum = exps<kMasked, true>(s_addr, v, k, bits_of, n);
     } else if constexpr (MODE != kModPlain) {
       float best = -INFINITY;
       const bool bound = mode_rel(MODE) && strip_close;
       if (bound && best_raw != -INFINITY) best = raw(best_raw) + strip_lo;
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) {
-        if ((k.none >> ch) & 1u) continue;
+        if (kMasked && ((k.none >> ch) & 1u)) continue;
         logits(v[ch], ch, gap);
-        if (mode_cap(MODE) && ((k.partial >> ch) & 1u)) mask_chunk(v[ch], bits_of(ch), kMinusInf);
+        if (kMasked && mode_cap(MODE) && ((k.partial >> ch) & 1u)) mask_chunk(v[ch], bits_of(ch), kMinusInf);
         if (!bound) best = fmaxf(best, chunk_max(v[ch]));
       }
       m_new = next_max(m, best);
       publish(alpha_bits(m, m_new));
-      sum = exps<true, false>(s_addr, v, k, bits_of, m_new == -INFINITY ? 0.f : -m_new);
+      sum = exps<kMasked, false>(s_addr, v, k, bits_of, m_new == -INFINITY ? 0.f : -m_new);
     }
     l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
     m = m_new;
   }
 
-  // x in place of the 32 scores of chunk ch (tiles that are not direct).
+  // The same for a masked tile by a rolled loop that reads each chunk from
+  // tensor memory twice: a third of the instructions, for tiles that a CTA
+  // meets once or twice, whose code then comes from far.
+  template <typename BitsOf, typename Gap, typename Publish>
+  __device__ __forceinline__ void tile_rolled(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
+                                              float& m, float& l, Publish&& publish) const {
+    auto load = [&](int ch, Chunk& v) {
+      tmem_ld_32x32b_x32(s_addr + ch * 32, v);
+      tmem_ld_wait();
+      reg_fence32(v);
+      const uint32_t bits = bits_of(ch);
+      if constexpr (mode_cap(MODE)) mask_chunk(v, bits, 0u);
+      logits(v, ch, gap);
+      mask_chunk(v, bits, kMinusInf);
+    };
+    float best = -INFINITY;
+#pragma unroll 1
+    for (int ch = 0; ch < kChunks; ++ch) {
+      if ((k.none >> ch) & 1u) continue;
+      Chunk v;
+      load(ch, v);
+      best = fmaxf(best, chunk_max(v));
+    }
+    const float m_new = next_max(m, best);
+    publish(alpha_bits(m, m_new));
+    const float n = m_new == -INFINITY ? 0.f : -m_new;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int ch = 0; ch < kChunks; ++ch) {
+      uint32_t pk[16];
+      if ((k.none >> ch) & 1u) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pk[e] = 0u;
+      } else {
+        Chunk v;
+        load(ch, v);
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float p0 = ex2_approx(__uint_as_float(v[2 * e]) + n), p1 = ex2_approx(__uint_as_float(v[2 * e + 1]) + n);
+          a[(2 * e) & 3] += p0;
+          a[(2 * e + 1) & 3] += p1;
+          if constexpr (kF16) pk[e] = pack_f16x2(p0, p1);
+          else pk[e] = pack_bf16x2(p0, p1);
+        }
+        sum += (a[0] + a[1]) + (a[2] + a[3]);
+      }
+      tmem_st_32x32b_x16(s_addr + ch * 16, pk);
+    }
+    l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
+    m = m_new;
+  }
+
+  // x in place of the 32 scores of chunk ch, less the constant part of the bias.
   template <typename Gap>
   __device__ __forceinline__ void logits(Chunk& v, int ch, Gap&& gap) const {
     if constexpr (mode_cap(MODE)) {
@@ -251,6 +305,11 @@ struct TileScore {
 #pragma unroll
         for (int e = 0; e < 32; e += 2) set_pair(v, e, f2_fma(pair_of(v, e), c2, b2));
       }
+    }
+    if constexpr (MODE == kModPlain) {
+      const uint64_t c2 = f2_pack(c, c);
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) set_pair(v, e, f2_mul(pair_of(v, e), c2));
     }
     if constexpr (mode_slopes(MODE)) {
       const float mul = mode_cap(MODE) ? 1.f : c;

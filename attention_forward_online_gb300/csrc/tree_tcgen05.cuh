@@ -78,6 +78,16 @@ struct Cfg {
   static constexpr int kTableBytes = MODE == kModSlopes ? 2 * kSlopeRowsBytes : 0;
 };
 
+// A share's next segment; every role walks the same ones.
+struct Walk {
+  int at, end;  // list positions
+  int b, base;  // sequence and its first list position
+  int ctx, first, n_b;
+  // the segment
+  int hk, rt, tile0, n;
+  bool head_cut, tail_cut;  // misses the unit's first or last tiles
+};
+
 struct __align__(16) Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
@@ -90,10 +100,15 @@ struct __align__(16) Bars {
   uint64_t mma_drain;
   uint32_t tmem_base;
   int abort_flag;
-  int start_b, start_base, total;
+  Walk start;  // of this CTA's share, before its first segment
   int warp_sum[16];
-  uint16_t alpha[2][BM];  // alpha_bits
-  float2 state[2][BM];    // [accumulator][row]: m, l
+  // Within a segment alpha_bits of the accumulator's rows, [accumulator][row];
+  // at its end the states m, l.
+  union {
+    uint16_t alpha[2][BM];
+    float2 state[2][BM];
+  };
+  Walk walk[8];  // of the softmax warps: their registers hold the scores
 };
 
 template <int HD, int MODE>
@@ -185,32 +200,14 @@ __device__ __forceinline__ bool slopes_linear(const Params& p, int hk) {
   return ok;
 }
 
+// Whether some draft does not see all keys of the tile from k0 on: it holds
+// drafts or keys behind them, or keys before some draft's window.
+__device__ __forceinline__ bool tile_masked(const Params& p, int ctx, int k0) {
+  return k0 + BN > ctx || (p.window > 0 && k0 < ctx + p.T - p.window);
+}
+
 // Shares of a list of `total` key tiles: no share is empty.
 __device__ __forceinline__ int shares(int total, int grid) { return total < grid ? total : grid; }
-
-// A share's next segment; every role walks the same ones.
-struct Walk {
-  int at, end;  // list positions
-  int b, base;  // sequence and its first list position
-  int ctx, first, n_b;
-  // the segment
-  int hk, rt, tile0, n;
-  bool head_cut, tail_cut;  // misses the unit's first or last tiles
-};
-
-__device__ __forceinline__ Walk walk_start(const Params& p, const Bars* bars) {
-  Walk w;
-  const long long total = bars->total, c = blockIdx.x, G = shares(bars->total, gridDim.x);
-  w.at = c < G ? static_cast<int>(c * total / G) : 0;
-  w.end = c < G ? static_cast<int>((c + 1) * total / G) : 0;
-  w.b = bars->start_b;
-  w.base = bars->start_base;
-  if (w.at < w.end) {
-    w.ctx = ctx_of(p, w.b);
-    key_tiles(p, w.ctx, w.first, w.n_b);
-  }
-  return w;
-}
 
 __device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
   if (w.at >= w.end) return false;
@@ -250,32 +247,49 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
   ts.cap = &p.cap;
   uint32_t s_phase = 0, seg = 0;
   bool ok = true;
-  for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
+  Walk& at = bars->walk[warp];
+  if (lane == 0) at = bars->start;
+  __syncwarp();
+  for (; ok; ++seg) {
+    Walk w = at;
+    const bool more = walk_next(p, w);
+    __syncwarp();
+    if (lane == 0) at = w;
+    __syncwarp();
+    if (!more) break;
+    const int ctx = w.ctx, tile0 = w.tile0, n = w.n;
     const int tok = w.rt * p.tok_tile + tl;
     const bool live = tl < p.tok_tile && tok < p.T;
     const bool warp_live = __any_sync(0xffffffffu, live);
-    const int h = w.hk * p.group + g;
-    unsigned long long mask = live ? mask_of(p, w.b, tok) : 0ull;
-    const bool sees = mask != 0ull;  // a padding token sees nothing: its row is zeroed at the end
-    const int depth = depth_of(mask);
-    int lo = 0;  // first key of the row's context
-    if (p.window > 0) {
-      lo = max(0, w.ctx + depth - p.window + 1);
-      if (sees && p.T > p.window) {  // drafts of its line that are a window away
+    // the drafts that the row sees: those of its line, without the ones that
+    // are a window away
+    auto row_mask = [&](int b) {
+      unsigned long long mask = live ? mask_of(p, b, tok) : 0ull;
+      if (p.window > 0 && p.T > p.window) {
+        const int depth = depth_of(mask);
         for (int u = 0; u < p.T; ++u)
-          if (((mask >> u) & 1) && abs(depth - depth_of(mask_of(p, w.b, u))) >= p.window)
-            mask &= ~(1ull << u);
+          if (((mask >> u) & 1) && abs(depth - depth_of(mask_of(p, b, u))) >= p.window) mask &= ~(1ull << u);
       }
+      return mask;
+    };
+    int depth = 0;
+    bool sees = false;  // a padding token sees nothing: its row is zeroed at the end
+    if (live) {
+      const unsigned long long mask = mask_of(p, w.b, tok);
+      sees = mask != 0ull;
+      depth = depth_of(mask);
     }
+    const int lo = p.window > 0 ? max(0, ctx + depth - p.window + 1) : 0;  // first key of the row's context
     [[maybe_unused]] bool linear = false;
     if constexpr (mode_slopes(MODE)) {
-      const float slope = live ? __ldg(p.slopes + h) : 0.f;
+      const float slope = live ? __ldg(p.slopes + w.hk * p.group + g) : 0.f;
       ts.slope2 = slope * kModLog2e;
       linear = MODE == kModSlopes && slopes_linear(p, w.hk);
     }
-    const int tile_lo = p.window > 0 ? max(0, w.ctx + p.T - p.window) : 0;  // every row's context starts at or before it
     float m = -INFINITY, l = 0.f;
-    for (int i = t; ok && i < w.n; i += 2) {
+    // the last segment's states, where alpha goes now, have been read
+    if (seg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_empty, (seg - 1) & 1u, wc, kSiteOEmpty));
+    for (int i = t; ok && i < n; i += 2) {
       ok = mbar_wait(&bars->s_full[t], s_phase & 1u, wc, kSiteS);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -291,48 +305,59 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
         mbar_arrive(&bars->p_full[t]);
         continue;
       }
-      const int k0 = (w.tile0 + i) * BN;
-      const bool tail = k0 + BN > w.ctx;  // holds drafts or keys behind them
-      const bool masked = tail || k0 < tile_lo;
-      // visible keys of a chunk: context keys [lo, ctx), then the mask
-      auto bits_of = [&](int ch) {
-        const int c0 = k0 + 32 * ch;
-        uint32_t bits = bit_range(lo - c0, w.ctx - c0);
-        const int sh = w.ctx - c0;  // where draft 0 falls
-        if (sh >= 0 && sh < 32) bits |= static_cast<uint32_t>(mask << sh);
-        else if (sh < 0 && sh > -64) bits |= static_cast<uint32_t>(mask >> -sh);
-        return bits;
-      };
-      TileMask mk;
-      if (masked) mk.classify(bits_of);
+      const int k0 = (tile0 + i) * BN;
+      const bool tail = k0 + BN > ctx;  // holds drafts or keys behind them
+      const bool masked = tile_masked(p, ctx, k0);
       if constexpr (mode_slopes(MODE)) {
         // distances fall along the context; drafts are at the distance of
         // their depths
-        ts.d0 = static_cast<float>(k0 - (w.ctx + depth));
-        ts.both_sides = !linear || tail;
+        ts.d0 = static_cast<float>(k0 - (ctx + depth));
+        ts.both_sides = !linear || masked;
         ts.off = ts.both_sides ? 0.f : ts.slope2 * ts.d0;
-        if (tail) {
-          auto gap = [&](int e) {
-            const int u = k0 + e - w.ctx;
-            const float dist = ts.d0 + static_cast<float>(e);
-            if (u < 0) return dist;
-            return u < p.T ? static_cast<float>(depth_of(mask_of(p, w.b, u)) - depth) : 0.f;
-          };
-          ts.tile(s_addr, masked, mk, bits_of, gap, m, l, publish);
-        }
       }
-      if (!mode_slopes(MODE) || !tail) ts.tile(s_addr, masked, mk, bits_of, ts.by_place(), m, l, publish);
+      TileMask mk;
+      if (masked) {
+        const unsigned long long mask = tail ? row_mask(at.b) : 0ull;
+        // visible keys of a chunk: context keys [lo, ctx), then the mask
+        auto bits_of = [&](int ch) {
+          const int c0 = k0 + 32 * ch;
+          uint32_t bits = bit_range(lo - c0, sees ? ctx - c0 : 0);
+          const int sh = ctx - c0;  // where draft 0 falls
+          if (sh >= 0 && sh < 32) bits |= static_cast<uint32_t>(mask << sh);
+          else if (sh < 0 && sh > -64) bits |= static_cast<uint32_t>(mask >> -sh);
+          return bits;
+        };
+        mk.classify(bits_of);
+        // lane x holds the depths of drafts x and 32 + x
+        [[maybe_unused]] float dep0 = 0.f, dep1 = 0.f;
+        if constexpr (mode_slopes(MODE)) {
+          if (tail) {
+            if (lane < p.T) dep0 = static_cast<float>(depth_of(mask_of(p, at.b, lane)));
+            if (lane + 32 < p.T) dep1 = static_cast<float>(depth_of(mask_of(p, at.b, lane + 32)));
+          }
+        }
+        auto gap = [&](int e) {
+          const int u = k0 + e - ctx;  // (uniform over the warp)
+          if (u < 0) return ts.d0 + static_cast<float>(e);
+          return __shfl_sync(0xffffffffu, u < 32 ? dep0 : dep1, u & 31) - static_cast<float>(depth);
+        };
+        ts.tile_rolled(s_addr, mk, bits_of, gap, m, l, publish);
+      } else {
+        ts.template tile<false>(s_addr, mk, [](int) { return 0xffffffffu; }, ts.by_place(), m, l, publish);
+      }
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&bars->p_full[t]);
     }
     if (!ok) break;
     // ---- merge the two states; warpgroup t finishes columns t d/2 .. of both
-    if (seg > 0) ok = mbar_wait(&bars->o_empty, (seg - 1) & 1u, wc, kSiteOEmpty);  // the last states have been read
+    // (every alpha of the segment has been used: its products are done)
+    ok = mbar_wait(&bars->o_full, seg & 1u, wc, kSiteO);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
     bars->state[t][row] = make_float2(m, l);
     mbar_arrive(&bars->merge);
-    if (ok) ok = mbar_wait(&bars->merge, seg & 1u, wc, kSiteMerge);
-    if (ok) ok = mbar_wait(&bars->o_full, seg & 1u, wc, kSiteO);
+    ok = mbar_wait(&bars->merge, seg & 1u, wc, kSiteMerge);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     tc_fence_after_sync();
@@ -344,11 +369,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
     const bool empty = L == 0.f || !sees;
     const float inv = empty ? 0.f : 1.f / L;
     const float g0 = f0 * inv, g1 = f1 * inv;
-    const bool whole = !w.head_cut && !w.tail_cut;
-    const int slot = 2 * static_cast<int>(blockIdx.x) + (w.head_cut ? 0 : 1);
+    const bool head_cut = at.head_cut, whole = !head_cut && !at.tail_cut;
+    const int b = at.b, h = at.hk * p.group + g;
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (head_cut ? 0 : 1);
     constexpr int kHalf = HD / 2;
     const uint32_t o_addr = lane_base + kOCol0 + static_cast<uint32_t>(t * kHalf);
-    uint16_t* orow = p.O + w.b * p.o_sb + h * p.o_sh + tok * p.o_sn + t * kHalf;
+    uint16_t* orow = p.O + b * p.o_sb + h * p.o_sh + tok * p.o_sn + t * kHalf;
     const long long prow = static_cast<long long>(slot) * p.slot_rows + row;
     float* part = p.o_part + prow * HD + t * kHalf;
 #pragma unroll
@@ -356,7 +382,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
       if (!warp_live) break;
       uint32_t a0[32], a1[32];
       tmem_ld_32x32b_x32(o_addr + ch * 32, a0);
-      if (w.n > 1) tmem_ld_32x32b_x32(o_addr + HD + ch * 32, a1);
+      if (n > 1) tmem_ld_32x32b_x32(o_addr + HD + ch * 32, a1);
       tmem_ld_wait();
       reg_fence32(a0);
       reg_fence32(a1);
@@ -364,7 +390,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         o[e] = __uint_as_float(a0[e]) * g0;
-        if (w.n > 1) o[e] = fmaf(__uint_as_float(a1[e]), g1, o[e]);
+        if (n > 1) o[e] = fmaf(__uint_as_float(a1[e]), g1, o[e]);
         if (empty) o[e] = 0.f;
       }
       if (live) {
@@ -386,7 +412,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
     if (live && t == 0) {
       const float lse = empty ? -INFINITY : (M + log2f(L)) * kLn2;
       if (whole)
-        p.LSE[(static_cast<long long>(w.b) * p.H + h) * p.T + tok] = lse;
+        p.LSE[(static_cast<long long>(b) * p.H + h) * p.T + tok] = lse;
       else
         p.lse_part[prow] = lse;
     }
@@ -404,7 +430,7 @@ __device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uin
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   uint32_t a_phase[2] = {0, 0}, vc = 0;  // vc: V tiles so far
   bool ok = true;
-  for (Walk w = walk_start(p, bars); ok && walk_next(p, w);) {
+  for (Walk w = bars->start; ok && walk_next(p, w);) {
     // Drafts that some draft sees; the rows of V of the others, like those of
     // keys before the window and behind the drafts, are zeroed below.
     unsigned long long seen = 0ull;
@@ -484,7 +510,7 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUte
   const uint32_t q_bytes = static_cast<uint32_t>(p.tok_tile * p.group * HD * 2);
   uint32_t n = 0, seg = 0;  // tiles and segments so far
   bool ok = true;
-  for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
+  for (Walk w = bars->start; ok && walk_next(p, w); ++seg) {
     if constexpr (!kV) {
       if (seg > 0) {
         ok = warp_wait(&bars->q_empty, (seg - 1) & 1u, wc, kSiteQEmpty);
@@ -563,7 +589,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Bars* bars, uint32_t t
   const uint32_t s_id = idesc_f16_f32(128, 128, 0, kF16) | p.neg_q;
   uint32_t kc = 0, vc = 0, seg = 0, p_phase[2] = {0, 0};
   bool ok = true;
-  for (Walk w = walk_start(p, bars); ok && walk_next(p, w); ++seg) {
+  for (Walk w = bars->start; ok && walk_next(p, w); ++seg) {
     [[maybe_unused]] const bool linear = MODE == kModSlopes && slopes_linear(p, w.hk);
     ok = warp_wait(&bars->q_full, seg & 1u, wc, kSiteQ);
     if (!ok) break;
@@ -574,7 +600,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Bars* bars, uint32_t t
       tc_fence_after_sync();
       mma_abt_id<HD>(tmem + (i & 1) * BN, q_desc, k_desc + s * kStep, s_id);
       if constexpr (MODE == kModSlopes) {
-        if (linear && (w.tile0 + i + 1) * BN <= w.ctx)  // not where drafts are
+        if (linear && !tile_masked(p, w.ctx, (w.tile0 + i) * BN))
           mma_ss_k<1, true>(tmem + (i & 1) * BN, slope_rows_desc(smem_u32(slopes) + kSlopeRowsBytes),
                             slope_rows_desc(smem_u32(slopes)), idesc_f16_f32(128, 128, 0, kF16));
       }
@@ -611,58 +637,68 @@ __device__ __forceinline__ void mma_role(const Params& p, Bars* bars, uint32_t t
   __syncwarp();
 }
 
-// Where this CTA's share starts in the list, and the list's length; CTA 0
-// also writes every sequence's first position for the combine kernel.
+// Where this CTA's share starts in the list; CTA 0 also writes every sequence's
+// first position, and the list's length, for the combine kernel.
 __device__ __forceinline__ void find_start(const Params& p, Bars* bars) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int units = p.Hkv * p.row_tiles;
-  auto tiles_of = [&](int b) {
-    int first, n;
-    key_tiles(p, ctx_of(p, b), first, n);
-    return n * units;
-  };
-  // pass 0 sums, pass 1 scans; one pass over up to 512 sequences at a time
-  int total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int before = 0;
-    long long start = 0;
-    if (pass) start = static_cast<long long>(blockIdx.x) * total / shares(total, gridDim.x);
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      const int b = b0 + static_cast<int>(threadIdx.x);
-      const int mine = b < p.B ? tiles_of(b) : 0;
-      if (pass == 0 && b < p.B && blockIdx.x == 0 && __ldg(p.ctx + b) != ctx_of(p, b))
-        atomicMax(p.status, kBadArg);
-      int scan = mine;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, scan, off);
-        if (lane >= off) scan += y;
-      }
-      if (lane == 31) bars->warp_sum[warp] = scan;
-      __syncthreads();
-      int pre = before, all = 0;
-      for (int x = 0; x < kThreads / 32; ++x) {
-        const int y = bars->warp_sum[x];
-        if (x < warp) pre += y;
-        all += y;
-      }
-      __syncthreads();
-      if (pass) {
-        const int base = pre + scan - mine;
-        if (b < p.B && start >= base && start < base + mine) {
-          bars->start_b = b;
-          bars->start_base = base;
-        }
-        if (blockIdx.x == 0 && b < p.B) p.head[b] = base;
-      }
-      before += all;
+  // This thread's sequence of a block of kThreads of them, and the scan of
+  // the block's tiles: position of the sequence's first, and the block's sum.
+  int ctx = 0, first = 0, n_b = 0, base = 0;
+  auto scan_block = [&](int b0, int before) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    n_b = 0;
+    if (b < p.B) {
+      ctx = ctx_of(p, b);
+      key_tiles(p, ctx, first, n_b);
     }
-    total = before;
-  }
+    const int mine = n_b * units;
+    int scan = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, off);
+      if (lane >= off) scan += y;
+    }
+    if (lane == 31) bars->warp_sum[warp] = scan;
+    __syncthreads();
+    int all = 0;
+    base = before + scan - mine;
+    for (int x = 0; x < kThreads / 32; ++x) {
+      const int y = bars->warp_sum[x];
+      if (x < warp) base += y;
+      all += y;
+    }
+    __syncthreads();
+    return all;
+  };
+  int total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan_block(b0, total);
+  const int G = shares(total, gridDim.x), c = blockIdx.x;
+  const int at = c < G ? static_cast<int>(static_cast<long long>(c) * total / G) : 0;
+  const int end = c < G ? static_cast<int>((c + 1ll) * total / G) : 0;
   if (threadIdx.x == 0) {
-    bars->total = total;
-    if (blockIdx.x == 0) p.head[p.B] = total;
+    bars->start.at = at;
+    bars->start.end = end;
   }
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    if (p.B > kThreads) before += scan_block(b0, before);  // else the scan at hand
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    if (b < p.B) {
+      if (at >= base && at < base + n_b * units) {
+        bars->start.b = b;
+        bars->start.base = base;
+        bars->start.ctx = ctx;
+        bars->start.first = first;
+        bars->start.n_b = n_b;
+      }
+      if (blockIdx.x == 0) {
+        p.head[b] = base;
+        if (__ldg(p.ctx + b) != ctx) atomicMax(p.status, kBadArg);
+      }
+    }
+  }
+  if (threadIdx.x == 0 && blockIdx.x == 0) p.head[p.B] = total;
 }
 
 template <int HD, bool kF16, int MODE>
@@ -703,8 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->merge, 256);
     mbar_init(&bars->mma_drain, 1);
     bars->abort_flag = 0;
-    bars->start_b = 0;
-    bars->start_base = 0;
     fence_barrier_init();
   }
   if (warp == kProducerWarp && lane == 0) {
@@ -726,6 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_proxy_async();
   __syncthreads();
   find_start(p, bars);
+  // the combine kernel may take its place (it waits for this one to end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -761,9 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ combine
-// One warp a row: folds the partials of the CTAs that share the row's unit,
-// in CTA order, as (m, l) = (lse, 1) states.  Rows of units that one CTA did
-// whole are done already.
+// One warp a row: joins the partials of the CTAs that share the row's unit,
+// in CTA order.  Rows of units that one CTA did whole are done already.  Runs
+// as a dependent launch: resident before the main kernel ends where there is
+// room, waiting for it in griddepcontrol.wait.
 template <int HD, bool kF16>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const Params p, int grid) {
   constexpr int CPL = HD / 32;
@@ -777,35 +814,42 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const Params p, int g
   const int tl = row / p.group, g = row - tl * p.group;
   const int tok = rt * p.tok_tile + tl;
   if (row >= p.slot_rows || tl >= p.tok_tile || tok >= p.T) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int base = p.head[b], n_b = (p.head[b + 1] - base) / units;
   const long long total = p.head[p.B], G = shares(p.head[p.B], grid);
   const long long x0 = base + static_cast<long long>(unit) * n_b, x1 = x0 + n_b - 1;
   // the share that holds list position x: the largest c with c total / G <= x
   const int c0 = static_cast<int>(((x0 + 1) * G - 1) / total), c1 = static_cast<int>(((x1 + 1) * G - 1) / total);
   if (c0 == c1) return;
-  float m = -INFINITY, l = 0.f, acc[CPL];
+  // a partial is the state (m, l) = (lse, 1) carrying O / l
+  auto row_of = [&](int c) { return static_cast<long long>(2 * c + (c == c0 ? 1 : 0)) * p.slot_rows + row; };
+  float top = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.lse_part[row_of(c)]);
 #pragma unroll
-  for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const int slot = 2 * c + (c == c0 ? 1 : 0);
-    const long long prow = static_cast<long long>(slot) * p.slot_rows + row;
-    const float lse = p.lse_part[prow];
-    const float* src = p.o_part + prow * HD + lane * CPL;
-    float o[CPL];
-    if constexpr (CPL == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      o[0] = v.x; o[1] = v.y;
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float l = 0.f, acc[CPL];
+#pragma unroll
+  for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
+  for (int cb = c0; cb <= c1; cb += 32) {
+    const int n = min(32, c1 - cb + 1);
+    const float lse = lane < n ? p.lse_part[row_of(cb + lane)] : -INFINITY;
+    const float weight = lse == -INFINITY ? 0.f : expf(lse - top);  // (NaN stays NaN)
+#pragma unroll 8
+    for (int x = 0; x < n; ++x) {
+      const float w = __shfl_sync(0xffffffffu, weight, x);
+      const float* src = p.o_part + row_of(cb + x) * HD + lane * CPL;
+      float o[CPL];
+      if constexpr (CPL == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        o[0] = v.x; o[1] = v.y;
+      }
+#pragma unroll
+      for (int k = 0; k < CPL; ++k) acc[k] = fmaf(w, o[k], acc[k]);
+      l += w;
     }
-    if (lse == -INFINITY) continue;
-    const float M = fmaxf(m, lse);
-    const float alpha = expf(m - M), beta = expf(lse - M);
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) acc[k] = fmaf(acc[k], alpha, beta * o[k]);
-    l = fmaf(l, alpha, beta);
-    m = M;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int h = hk * p.group + g;
@@ -813,7 +857,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const Params p, int g
 #pragma unroll
   for (int k = 0; k < CPL; k += 2)
     *reinterpret_cast<uint32_t*>(dst + k) = pack2<kF16>(acc[k] * inv, acc[k + 1] * inv);
-  if (lane == 0) p.LSE[(static_cast<long long>(b) * p.H + h) * p.T + tok] = l == 0.f ? -INFINITY : m + logf(l);
+  if (lane == 0) p.LSE[(static_cast<long long>(b) * p.H + h) * p.T + tok] = l == 0.f ? -INFINITY : top + logf(l);
 }
 
 // ------------------------------------------------------------------ host
@@ -847,8 +891,16 @@ cudaError_t launch_mode(int grid, cudaStream_t s, const CUtensorMap& q, const CU
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.row_tiles * ((p.slot_rows + 7) / 8);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  tree_combine_kernel<HD, kF16><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p, grid);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute dep;
+  dep.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  dep.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &dep;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, kF16>, p, grid);
 }
 
 template <int HD, bool kF16>
