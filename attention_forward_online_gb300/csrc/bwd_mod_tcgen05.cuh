@@ -11,11 +11,14 @@
 //
 // Launches, in order on one stream:
 //   dq_kernel    one CTA per 128-row query tile; K and V tiles stream.  Also
-//                writes D, and with a learned bias the sums of dY by distance.
+//                writes D.
 //   dkdv_kernel  one CTA per 128-key tile of a key head; the query tiles of
 //                every head of its group that can see those keys stream, so
 //                the sums over heads stay in tensor memory and nothing is
 //                added by atomics: results do not depend on the order of CTAs.
+//                With a learned bias also the sums of dY by distance, here and
+//                not in dq_kernel since there is shared memory to spare (there
+//                it cost a K slot, 0.35 us a tile at d = 128).
 //   rel_reduce   folds the partial sums by distance into the table's buckets.
 // P and dS are rounded to 16 bits as MMA operands, everything summed in fp32.
 //
@@ -62,24 +65,27 @@ struct Cfg {
   // table of learned biases, or the slope operands
   static constexpr int kTableBytes = mode_rel(MODE) ? (rel_entries(kMaxRelRange) * 4 + 15) / 16 * 16
                                                     : (MODE == kModSlopes ? kSlopeRowsBytes + 4 * kSlopeQBytes : 0);
-  // dkdv: K, V, kStages stages of (Q_i, dO_i), then per stage LSE, D, lo, hi
+  // dkdv: K, V, kStages stages of (Q_i, dO_i), per stage LSE, D, lo, hi, then
+  // the table, the sums by distance and the warps' diagonal strips
   static constexpr int kStages = HD == 128 ? 2 : 4;
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kDkdvRows = 2 * kTileBytes + kStages * kStageBytes;
   static constexpr int kDkdvTable = kDkdvRows + kStages * kT * 16;
-  static constexpr int kDkdvRegion = kDkdvTable + kTableBytes;
-  // dq: Q, dO, kKSlots K tiles, kVSlots V tiles (K_j is read until dQ_j, V_j
-  // until dP_j); with a learned bias the table, the sums by distance and the
-  // warps' diagonal strips take the place of the third K tile at d = 128.  The
-  // slopes' key operand has 64 rows here, used for each half of a tile.
-  static constexpr int kKSlots = HD == 128 ? (mode_rel(MODE) ? 2 : 3) : 4;
-  static constexpr int kVSlots = HD == 128 ? 2 : 4;
-  static constexpr int kDqTable = (2 + kKSlots + kVSlots) * kTileBytes;
-  static constexpr int kDqTableBytes = MODE == kModSlopes ? kSlopeRowsBytes / 2 + kSlopeQBytes : kTableBytes;
-  static constexpr int kDqSums = kDqTable + kDqTableBytes;
+  static constexpr int kDkdvSums = kDkdvTable + kTableBytes;
   static constexpr int kSumBytes = mode_rel(MODE) ? (sum_entries(kMaxRelRange) * 4 + 15) / 16 * 16 : 0;
   static constexpr int kStripBytes = mode_rel(MODE) ? 2 * 8 * 96 * 4 : 0;
-  static constexpr int kDqRegion = kDqSums + kSumBytes + kStripBytes;
+  static constexpr int kDkdvRegion = kDkdvSums + kSumBytes + kStripBytes;
+  // dq: Q, dO, kKSlots K tiles, kVSlots V tiles (K_j is read until dQ_j, V_j
+  // until dP_j), then the table: at d = 128 a range above kSmallRel
+  // (kModRelWide) takes the third K tile's place.  The slopes' key operand has
+  // 64 rows here, used for each half of a tile.
+  static constexpr int kKSlots = HD == 128 ? (MODE == kModRelWide ? 2 : 3) : 4;
+  static constexpr int kVSlots = HD == 128 ? 2 : 4;
+  static constexpr int kDqTable = (2 + kKSlots + kVSlots) * kTileBytes;
+  static constexpr int kDqTableBytes =
+      MODE == kModSlopes ? kSlopeRowsBytes / 2 + kSlopeQBytes
+                         : (MODE == kModRel && HD == 128 ? (rel_entries(kSmallRel) * 4 + 15) / 16 * 16 : kTableBytes);
+  static constexpr int kDqRegion = kDqTable + kDqTableBytes;
   static constexpr uint32_t kColAcc0 = 256;       // dV
   static constexpr uint32_t kColAcc1 = 256 + HD;  // dK
 };
@@ -102,8 +108,9 @@ struct __align__(16) Bars {
   int abort_flag;
   int it_lo, it_hi;
   int side[4];                    // dkdv: slope_side of the stage's query tile, 0 if not linear
-  float d_part[2][kT];
-  float far_part[2][8];
+  int seen[4];                    // dkdv: bit 0 every query sees every key, bit 1 some query sees none
+  float d_part[kT];        // dq: D, added by the two groups (0 + a + b: the order does not matter)
+  float far_part[2][8];    // dkdv: sums of dY beyond the range, by warp
 };
 
 template <int HD, int MODE>
@@ -423,6 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* slo = reinterpret_cast<int*>(dsum + C::kStages * kT);    //   lo, hi of the query
   int* shi = slo + C::kStages * kT;
   float* bias_all = reinterpret_cast<float*>(smem + C::kDkdvTable);  // or the slope operands
+  [[maybe_unused]] float* sums = reinterpret_cast<float*>(smem + C::kDkdvSums);  // of dY by distance
+  [[maybe_unused]] float* strips = reinterpret_cast<float*>(smem + C::kDkdvSums + C::kSumBytes);  // [2][8][96]
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kDkdvRegion);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -489,35 +498,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(sV + cb * kT * 128, &tmV, &bars->fixed_full, cb * 64, k0, hk, b);
         }
       }
+      // Per-query values of a tile, loaded a tile ahead of their use: the loads
+      // depend on nothing, and none waits for a stage.
+      struct RowValues {
+        float lse[kT / 32], D[kT / 32];
+        int2 see[kT / 32];
+        PlanTile tile;
+      };
+      auto load_rows = [&](int it) {
+        RowValues v;
+        const int h = hk * p.group + it / cnt, qt = it_lo + it % cnt;
+        const long long rowbase = (static_cast<long long>(b) * p.H + h) * p.Nq;
+#pragma unroll
+        for (int r = 0; r < kT / 32; ++r) {
+          const int q = qt * kT + lane + 32 * r;
+          v.lse[r] = q < p.Nq ? p.LSE[rowbase + q] : -INFINITY;
+          v.D[r] = q < p.Nq ? p.D[rowbase + q] : 0.f;
+          // (rows past the last see what it sees, with P = 2^-inf: lo and hi keep their order)
+          v.see[r] = plan_row(p.plan, b, p.Nq, min(q, p.Nq - 1), p.Nkv);
+        }
+        v.tile = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
+        return v;
+      };
+      RowValues next = load_rows(0);
+      [[maybe_unused]] float slope = 0.f;
+      [[maybe_unused]] bool linear = false;
       for (int it = 0; it < n_it; ++it) {
         const int s = it % C::kStages;
         const int h = hk * p.group + it / cnt;
         const int qt = it_lo + it % cnt, q0 = qt * kT;
-        const long long rowbase = (static_cast<long long>(b) * p.H + h) * p.Nq;
-        [[maybe_unused]] float slope = 0.f, lin = 0.f;
+        const RowValues now = next;
+        if (it + 1 < n_it) next = load_rows(it + 1);
+        [[maybe_unused]] float lin = 0.f;  // what a linear slope leaves: lin (k0 - position)
         [[maybe_unused]] int side = 0;
         if constexpr (MODE == kModSlopes) {
-          slope = p.slopes[h];
-          if (slope_linear(slope, p.scale))
-            side = slope_side(k0, q0 + p.q_offset, plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv).left);
-          lin = slope * kModLog2e * static_cast<float>(side);  // what is left: lin (k0 - position)
+          if (it % cnt == 0) {
+            slope = __ldg(p.slopes + h);
+            linear = slope_linear(slope, p.scale);
+          }
+          if (linear) side = slope_side(k0, q0 + p.q_offset, now.tile.left);
+          lin = slope * kModLog2e * static_cast<float>(side);
         }
-        // per-query values, read before the wait for the stage
         float l2[kT / 32], dd[kT / 32];
-        int2 see[kT / 32];
 #pragma unroll
         for (int r = 0; r < kT / 32; ++r) {
           const int q = q0 + lane + 32 * r;
-          l2[r] = -INFINITY;
-          dd[r] = 0.f;
-          // (rows past the last see what it sees, with P = 2^-inf: lo and hi keep their order)
-          see[r] = plan_row(p.plan, b, p.Nq, min(q, p.Nq - 1), p.Nkv);
-          if (q < p.Nq && see[r].x < see[r].y) {
-            const float L = p.LSE[rowbase + q];
-            l2[r] = (L == -INFINITY) ? -INFINITY : -(L * kModLog2e);
-            if constexpr (MODE == kModSlopes) l2[r] = fmaf(lin, static_cast<float>(k0 - (q + p.q_offset)), l2[r]);
-            dd[r] = -p.D[rowbase + q];
-          }
+          const bool sees = q < p.Nq && now.see[r].x < now.see[r].y && now.lse[r] != -INFINITY;
+          l2[r] = sees ? -(now.lse[r] * kModLog2e) : -INFINITY;
+          if constexpr (MODE == kModSlopes)
+            if (sees) l2[r] = fmaf(lin, static_cast<float>(k0 - (q + p.q_offset)), l2[r]);
+          dd[r] = sees ? -now.D[r] : 0.f;
         }
         uint8_t* st = ring + s * C::kStageBytes;
         bool ok = true;
@@ -546,16 +576,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int x = s * kT + lane + 32 * r;
           lse2[x] = l2[r];
           dsum[x] = dd[r];
-          slo[x] = see[r].x;
-          shi[x] = see[r].y;
+          slo[x] = now.see[r].x;
+          shi[x] = now.see[r].y;
         }
         if constexpr (MODE == kModSlopes) {
-          if (lane < 8)
-            slope_fill_q<kF16>(reinterpret_cast<uint8_t*>(bias_all) + kSlopeRowsBytes + s * kSlopeQBytes, lane,
-                               slope, p.scale);
+          // A head's operand goes to place (head mod 4): the tiles of the head
+          // that had it are at least 4 tiles, so at least a ring, back.
+          if (it % cnt == 0) {
+            if (lane < 8)
+              slope_fill_q<kF16>(reinterpret_cast<uint8_t*>(bias_all) + kSlopeRowsBytes +
+                                     (it / cnt) % 4 * kSlopeQBytes,
+                                 lane, slope, p.scale);
+            fence_proxy_async();
+          }
           if (lane == 0) bars->side[s] = side;
-          fence_proxy_async();
         }
+        if (lane == 0)
+          bars->seen[s] = (now.tile.lo_max <= k0 && now.tile.hi_min >= k0 + kT ? 1 : 0) | (now.tile.hi_min == 0 ? 2 : 0);
         __syncwarp();
         if (lane == 0) {
 #pragma unroll
@@ -604,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
           mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(nq, 16, 1024));
           if constexpr (MODE == kModSlopes)
-            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + s1 * kSlopeQBytes,
-                                   smem_u32(bias_all), bars->side[s1]);
+            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + (it + 1) / cnt % 4 * kSlopeQBytes,
+                              smem_u32(bias_all), bars->side[s1]);
           mma_commit<true>(&bars->s_full[0]);
         }
         ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
@@ -630,8 +667,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     bool ok = true;
     int h_of = -1;
-    [[maybe_unused]] uint32_t sync_phase = 0;
+    [[maybe_unused]] uint32_t sync_phase = 0, near = 0;
+    [[maybe_unused]] float far_lo = 0.f, far_hi = 0.f;  // sums of dY at distances <= -R and >= R
     float slope2 = 0.f;
+    // Writes the sums of head h by clamped distance, the pads folded into the
+    // ends, and clears them.
+    [[maybe_unused]] auto flush_sums = [&](int h) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        far_lo += __shfl_xor_sync(0xffffffffu, far_lo, off);
+        far_hi += __shfl_xor_sync(0xffffffffu, far_hi, off);
+      }
+      if (lane == 0) {
+        bars->far_part[0][warp] = far_lo;
+        bars->far_part[1][warp] = far_hi;
+      }
+      far_lo = far_hi = 0.f;
+      if (!elem_sync(bars, sync_phase, wc)) return false;
+      const int R = p.rel.range;
+      float* out = p.rel_part + ((static_cast<long long>(b) * p.H + h) * p.num_tiles + kt) * (2 * R + 1);
+      for (int x = 1 + static_cast<int>(threadIdx.x); x < 2 * R; x += 256) out[x] = sums[x + kSumPad];
+      if (warp < 2) {  // distance -R (warp 0), R (warp 1)
+        const float* pad = sums + (warp == 0 ? 0 : 2 * R + kSumPad);
+        float v = 0.f;
+        for (int x = lane; x <= kSumPad; x += 32) v += pad[x];
+        if (lane < 8) v += bars->far_part[warp][lane];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if (lane == 0) out[warp == 0 ? 0 : 2 * R] = v;
+      }
+      if (!elem_sync(bars, sync_phase, wc)) return false;
+      for (int x = threadIdx.x; x < sum_entries(R); x += 256) sums[x] = 0.f;
+      return true;
+    };
+    if constexpr (mode_rel(MODE)) {
+      for (int x = threadIdx.x; x < sum_entries(p.rel.range); x += 256) sums[x] = 0.f;
+      if (n_it == 0) {  // nobody sees these keys: every head's sums are 0
+        ok = elem_sync(bars, sync_phase, wc);
+        for (int g = 0; ok && g < p.group; ++g) ok = flush_sums(hk * p.group + g);
+      }
+    }
     for (int it = 0; ok && it < n_it; ++it) {
       const int s = it % C::kStages;
       const int h = hk * p.group + it / cnt;
@@ -640,15 +715,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (h != h_of) {  // uniform over the elementwise warps
         if constexpr (mode_slopes(MODE)) slope2 = p.slopes[h] * kModLog2e;
         if constexpr (mode_rel(MODE)) {
-          // everyone is done with the last head's table
-          if (h_of >= 0 && !(ok = elem_sync(bars, sync_phase, wc))) break;
+          // the last head's sums, after which everyone is done with its table
+          if (h_of >= 0 && !(ok = flush_sums(h_of))) break;
           float least, most;
           rel_fill<kF16>(bias_all, p.rel, p.H, h, threadIdx.x, 256, least, most);
           if (!(ok = elem_sync(bars, sync_phase, wc))) break;
         }
         h_of = h;
       }
-      const PlanTile pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
       ok = mbar_wait(&bars->s_full[0], static_cast<uint32_t>(it) & 1u, wc, kSiteElem);
       if (ok) ok = mbar_wait(&bars->full[s], static_cast<uint32_t>(it / C::kStages) & 1u, wc, kSiteElem);
       ok = __all_sync(0xffffffffu, ok);
@@ -664,18 +738,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The group's columns for this warp's rows: all visible, none, or some.
       // lo and hi do not fall from one query to the next that sees a key, so
       // the first and last column decide, in tiles where every query does.
-      bool none = false, full = pt.lo_max <= k0 && pt.hi_min >= k0 + kT;
-      if (!full && pt.hi_min > 0) {
+      const int seen = bars->seen[s];
+      bool none = false, full = (seen & 1) != 0;
+      if (seen == 0) {
         full = __all_sync(0xffffffffu, lo[c0 + 63] <= kabs && kabs < hi[c0]);
         none = __all_sync(0xffffffffu, kabs < lo[c0] || kabs >= hi[c0 + 63]);
+      }
+      [[maybe_unused]] int side = 0;  // learned bias: distances of the warp's 32 keys to the group's 64 queries
+      if constexpr (mode_rel(MODE)) {
+        const int first = k0 + 32 * (warp & 3) - p0 - c0 - 63;
+        side = far_side(first, first + 94, p.rel.range);
       }
       float pr[64];
       auto part = [&](auto mask) {
         constexpr bool kMask = decltype(mask)::value;
         if constexpr (mode_rel(MODE)) {
-          // distances of the warp's 32 keys to the group's 64 queries
-          const int first = k0 + 32 * (warp & 3) - p0 - c0 - 63, R = p.rel.range;
-          const int side = far_side(first, first + 94, R);
+          const int R = p.rel.range;
           if (side != 0) {
             const float far = bias_all[side < 0 ? 0 : rel_entries(R) - 1];
             p_part<kF16, MODE, true, kMask, true>(lane_base, c0, p, vis, l2of4, [&](int) { return far; }, pr);
@@ -700,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p_none<true>(lane_base, c0, pr);
       } else {
         part(std::true_type{});
-        if (pt.hi_min == 0) {
+        if (seen & 2) {
           // Queries of this tile that see nothing: their rows of Q and dO
           // must not reach the sums (0 * NaN is NaN).  dP^T, the last other
           // reader of dO, is awaited first.
@@ -727,13 +805,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after_sync();
       auto dof4 = [&](int col) { return dd[col >> 2]; };
+      constexpr bool kKeep = mode_rel(MODE);
       if (full)
-        ds_part<kF16, false, false>(lane_base + 128, c0, dof4, pr);
+        ds_part<kF16, false, kKeep>(lane_base + 128, c0, dof4, pr);
       else
-        ds_part<kF16, true, false>(lane_base + 128, c0, dof4, pr);
+        ds_part<kF16, true, kKeep>(lane_base + 128, c0, dof4, pr);
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&bars->ds_full);
+      if constexpr (mode_rel(MODE)) {
+        // A block of 32 keys and 64 queries beyond the range goes to one
+        // distance.  Otherwise sums along its diagonals: a running sum moves
+        // one lane up with every column, so that it stays on one distance;
+        // lane 31 stores the diagonals that end there.  Strip entry u holds
+        // distance (32 quarter - c0) + 31 - u within the tile.
+        if (side != 0 && !none) {
+          float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 64; ++x) a[x & 3] += pr[x];
+          const float sum = (a[0] + a[1]) + (a[2] + a[3]);
+          if (side < 0) far_lo += sum;
+          else far_hi += sum;
+        }
+        if (far_side(k0 - p0 - 127, k0 - p0 + 127, p.rel.range) == 0) {
+          const int buf = near++ & 1;
+          float* strip = strips + buf * 8 * 96 + warp * 96;
+          if (side != 0 || none) {
+#pragma unroll
+            for (int x = 0; x < 3; ++x) strip[32 * x + lane] = 0.f;
+          } else {
+            // four runs of 16 columns side by side (one run of 64 waits for
+            // each shuffle); what a run has left in lane r would have left
+            // lane 31 31 - r columns later
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                acc[u] = __shfl_up_sync(0xffffffffu, acc[u], 1);
+                acc[u] = (lane == 0 ? 0.f : acc[u]) + pr[16 * u + x];
+                if (lane == 31) strip[16 * u + x] = acc[u];
+              }
+            }
+            if (lane < 31) strip[94 - lane] = acc[3];
+#pragma unroll
+            for (int u = 2; u >= 0; --u) {
+              __syncwarp();
+              if (lane < 31) strip[16 * u + 46 - lane] += acc[u];
+            }
+          }
+          if (!(ok = elem_sync(bars, sync_phase, wc))) break;
+          // thread u adds distance u - 127 of the tile to the sums
+          const int u = threadIdx.x;
+          if (u < 2 * kT - 1) {
+            float add = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const int at = 31 + 32 * (w & 3) - 64 * (w >> 2) - (u - 127);
+              if (at >= 0 && at < 95) add += strips[buf * 8 * 96 + w * 96 + at];
+            }
+            sums[k0 - p0 + (u - 127) + p.rel.range + kSumPad] += add;
+          }
+        }
+      }
+    }
+    if constexpr (mode_rel(MODE)) {
+      if (ok && n_it > 0) ok = flush_sums(h_of);
     }
     // epilogue: warpgroup 0 writes dV, warpgroup 1 dK
     bool has_acc = false;
@@ -794,8 +931,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* kring = smem + 2 * C::kTileBytes;
   uint8_t* vring = kring + C::kKSlots * C::kTileBytes;
   float* bias = reinterpret_cast<float*>(smem + C::kDqTable);  // or the slope operands
-  float* dsum = reinterpret_cast<float*>(smem + C::kDqSums);   // sums of dY by distance
-  float* strips = reinterpret_cast<float*>(smem + C::kDqSums + C::kSumBytes);  // [2][8][96]
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kDqRegion);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -833,9 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bars->tmem_base, kCols);
     tmem_relinquish();
   }
-  if constexpr (mode_rel(MODE)) {
-    for (int x = threadIdx.x; x < sum_entries(p.rel.range); x += kThreads) dsum[x] = 0.f;
-  }
+  if (threadIdx.x < kT) bars->d_part[threadIdx.x] = 0.f;
   [[maybe_unused]] bool linear = false;
   if constexpr (MODE == kModSlopes) {
     linear = slope_linear(slope, p.scale);
@@ -960,7 +1093,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4 dv4 = make_float4(0.f, 0.f, 0.f, 0.f);  // -D
     if (n_kt == 0 && g == 0 && in) p.D[rix] = 0.f;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float far_lo = 0.f, far_hi = 0.f;  // sums of dY at distances <= -R and >= R
     [[maybe_unused]] uint32_t sync_phase = 0;
     bool ok = true;
     if constexpr (mode_rel(MODE)) {  // while the first loads and products run
@@ -977,8 +1109,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int d0 = kx - (q + p.q_offset);
       // the row's visible keys of the group, as bits
       const int from = see.x - kx - c0, to = see.y - kx - c0;
-      const bool full = __all_sync(0xffffffffu, from <= 0 && to >= 64);
-      const bool none = __all_sync(0xffffffffu, max(from, 0) >= min(to, 64));
+      bool none = false, full = pt.lo_max <= kx && pt.hi_min >= kx + kT;
+      if (!full) {
+        full = __all_sync(0xffffffffu, from <= 0 && to >= 64);
+        none = __all_sync(0xffffffffu, max(from, 0) >= min(to, 64));
+      }
       const uint32_t bits[2] = {bit_range(from, to), bit_range(from - 32, to - 32)};
       auto vis = [&](int col) { return (bits[(col - c0) >> 5] & (1u << ((col - c0) & 31))) != 0u; };
       float nl = l2;
@@ -1052,12 +1187,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
           }
         }
-        bars->d_part[g][row] = sum;
+        atomicAdd(&bars->d_part[row], sum);
         mbar_arrive(&bars->d_full);
         ok = mbar_wait(&bars->d_full, 0, wc, kSiteElem);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const float D = row_live ? bars->d_part[0][row] + bars->d_part[1][row] : 0.f;
+        const float D = row_live ? bars->d_part[row] : 0.f;
         dv4 = make_float4(-D, -D, -D, -D);
         if (g == 0 && in) p.D[rix] = D;
       }
@@ -1066,59 +1201,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       auto dof4 = [&](int) { return dv4; };
-      constexpr bool kKeep = mode_rel(MODE);
       if (full)
-        ds_part<kF16, false, kKeep>(lane_base + kDqColDP, c0, dof4, pr);
+        ds_part<kF16, false, false>(lane_base + kDqColDP, c0, dof4, pr);
       else
-        ds_part<kF16, true, kKeep>(lane_base + kDqColDP, c0, dof4, pr);
+        ds_part<kF16, true, false>(lane_base + kDqColDP, c0, dof4, pr);
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&bars->ds_full);
-      if constexpr (mode_rel(MODE)) {
-        // A block of 32 queries and 64 keys beyond the range goes to one
-        // distance.  Otherwise sums along its diagonals: a running sum moves
-        // one lane up with every column, so that it stays on one distance;
-        // lane 31 stores the diagonals that end there.  Strip entry u holds
-        // distance (c0 - 32 quarter) + u - 31 within the tile.
-        const bool tile_far = far_side(kx - p0 - 127, kx - p0 + 127, p.rel.range) != 0;
-        if (side != 0 && !none) {
-          float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int x = 0; x < 64; ++x) a[x & 3] += pr[x];
-          const float sum = (a[0] + a[1]) + (a[2] + a[3]);
-          if (side < 0) far_lo += sum;
-          else far_hi += sum;
-        }
-        if (!tile_far) {
-          const int buf = sync_phase & 1;
-          float* strip = strips + buf * 8 * 96 + warp * 96;
-          if (side != 0 || none) {
-#pragma unroll
-            for (int x = 0; x < 3; ++x) strip[32 * x + lane] = 0.f;
-          } else {
-            float acc = 0.f;
-#pragma unroll
-            for (int x = 0; x < 64; ++x) {
-              acc = __shfl_up_sync(0xffffffffu, acc, 1);
-              acc = (lane == 0 ? 0.f : acc) + pr[x];
-              if (lane == 31) strip[x] = acc;
-            }
-            if (lane < 31) strip[94 - lane] = acc;
-          }
-          if (!(ok = elem_sync(bars, sync_phase, wc))) break;
-          // thread u adds distance u - 127 of the tile to the sums
-          const int u = threadIdx.x;
-          if (u < 2 * kT - 1) {
-            float add = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-              const int at = (u - 127) - 64 * (w >> 2) + 32 * (w & 3) + 31;
-              if (at >= 0 && at < 95) add += strips[buf * 8 * 96 + w * 96 + at];
-            }
-            dsum[kx - p0 + (u - 127) + p.rel.range + kSumPad] += add;
-          }
-        }
-      }
     }
     bool has_acc = false;
     if (ok && n_kt > 0) {
@@ -1142,17 +1231,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    if constexpr (mode_rel(MODE)) {
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        far_lo += __shfl_xor_sync(0xffffffffu, far_lo, off);
-        far_hi += __shfl_xor_sync(0xffffffffu, far_hi, off);
-      }
-      if (lane == 0) {
-        bars->far_part[0][warp] = far_lo;
-        bars->far_part[1][warp] = far_hi;
-      }
-    }
   }
 
   __syncwarp();
@@ -1164,37 +1242,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, kCols);
   }
-  if constexpr (mode_rel(MODE)) {
-    // this CTA's sums by clamped distance, the pads folded into the ends
-    const int R = p.rel.range;
-    float* out = p.rel_part + (static_cast<long long>(bh) * p.num_tiles + qt) * (2 * R + 1);
-    for (int x = threadIdx.x; x < 2 * R + 1; x += kThreads)
-      if (x != 0 && x != 2 * R) out[x] = dsum[x + kSumPad];
-    if (warp < 2) {  // distance -R (warp 0), R (warp 1)
-      const float* pad = dsum + (warp == 0 ? 0 : 2 * R + kSumPad);
-      float v = 0.f;
-      for (int x = lane; x <= kSumPad; x += 32) v += pad[x];
-      if (lane < 8) v += bars->far_part[warp][lane];
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (lane == 0) out[warp == 0 ? 0 : 2 * R] = v;
-    }
-  }
 }
 
 // The table's gradient: one block per head.  Each warp sums a share of the
-// query tiles' partials over batch entries and tiles, lanes along the
-// distances; the warps' sums are added in order, then each warp sums the
+// key tiles' partials over batch entries and tiles, lanes along the distances; the warps' sums are added in order, then each warp sums the
 // distances of its buckets.  Bound by latency: 2 R + 1 floats a tile.
 template <bool kF16>
 __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restrict__ part,
                                                           uint16_t* __restrict__ out, RelArgs rel, int B,
-                                                          int H, int q_tiles) {
+                                                          int H, int tiles) {
   constexpr int kX = 4;  // blocks of 32 distances a warp takes at a time
   __shared__ float warp_sum[32][32 * kX];
   __shared__ float sums[2 * kMaxRelRange + 1];
   __shared__ int map[2 * kMaxRelRange + 1];
-  const int h = blockIdx.x, n = 2 * rel.range + 1, rows = B * q_tiles;
+  const int h = blockIdx.x, n = 2 * rel.range + 1, rows = B * tiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int x = threadIdx.x; x < n; x += 1024) map[x] = rel.map[x];
   for (int x0 = 0; x0 < n; x0 += 32 * kX) {
@@ -1203,8 +1264,8 @@ __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restric
     for (int u = 0; u < kX; ++u) a[u] = 0.f;
 #pragma unroll 4
     for (int r = warp; r < rows; r += 32) {
-      const int b = r / q_tiles, t = r - b * q_tiles;
-      const float* src = part + ((static_cast<long long>(b) * H + h) * q_tiles + t) * n + x0 + lane;
+      const int b = r / tiles, t = r - b * tiles;
+      const float* src = part + ((static_cast<long long>(b) * H + h) * tiles + t) * n + x0 + lane;
 #pragma unroll
       for (int u = 0; u < kX; ++u)
         if (x0 + lane + 32 * u < n) a[u] += src[32 * u];
@@ -1232,11 +1293,12 @@ __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restric
 
 template <int HD, bool kF16, int MODE>
 cudaError_t set_attrs() {
-  static_assert(dkdv_smem_bytes<HD, MODE>() <= 232448 && dq_smem_bytes<HD, MODE>() <= 232448,
+  constexpr int kDkdvMode = MODE == kModRelWide ? kModRel : MODE;
+  static_assert(dkdv_smem_bytes<HD, kDkdvMode>() <= 232448 && dq_smem_bytes<HD, MODE>() <= 232448,
                 "shared memory per CTA");
-  cudaError_t e = cudaFuncSetAttribute(dkdv_kernel<HD, kF16, MODE>,
+  cudaError_t e = cudaFuncSetAttribute(dkdv_kernel<HD, kF16, kDkdvMode>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       dkdv_smem_bytes<HD, MODE>());
+                                       dkdv_smem_bytes<HD, kDkdvMode>());
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(dq_kernel<HD, kF16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               dq_smem_bytes<HD, MODE>());
@@ -1249,6 +1311,8 @@ cudaError_t prepare() {
   if ((e = set_attrs<HD, kF16, kModCap>()) != cudaSuccess) return e;
   if ((e = set_attrs<HD, kF16, kModSlopes>()) != cudaSuccess) return e;
   if ((e = set_attrs<HD, kF16, kModCapSlopes>()) != cudaSuccess) return e;
+  if constexpr (HD == 128)
+    if ((e = set_attrs<HD, kF16, kModRelWide>()) != cudaSuccess) return e;
   return set_attrs<HD, kF16, kModRel>();
 }
 
@@ -1259,11 +1323,12 @@ cudaError_t launch_mode(const ModArgs& a, const Params& pq, const Params& pk, un
   dq_kernel<HD, kF16, MODE><<<gq, kThreads, dq_smem_bytes<HD, MODE>(), a.stream>>>(m.q, m.k, m.v, m.g, m.dq, pq);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dkdv_kernel<HD, kF16, MODE><<<gk, kThreads, dkdv_smem_bytes<HD, MODE>(), a.stream>>>(m.q, m.k, m.v, m.g, m.dk, m.dv, pk);
+  constexpr int kDkdvMode = MODE == kModRelWide ? kModRel : MODE;
+  dkdv_kernel<HD, kF16, kDkdvMode><<<gk, kThreads, dkdv_smem_bytes<HD, kDkdvMode>(), a.stream>>>(m.q, m.k, m.v, m.g, m.dk, m.dv, pk);
   e = cudaGetLastError();
   if (e != cudaSuccess || !mode_rel(MODE)) return e;
   rel_reduce_kernel<kF16><<<a.H, 1024, 0, a.stream>>>(a.rel_part, static_cast<uint16_t*>(a.dRel), a.rel,
-                                                      a.B, a.H, pq.q_tiles);
+                                                      a.B, a.H, pk.num_tiles);
   return cudaGetLastError();
 }
 
@@ -1312,7 +1377,10 @@ cudaError_t launch(const ModArgs& a, const BwdModMaps& m) {
     case kModCap: return launch_mode<HD, kF16, kModCap>(a, pq, pk, uq, uk, m);
     case kModSlopes: return launch_mode<HD, kF16, kModSlopes>(a, pq, pk, uq, uk, m);
     case kModCapSlopes: return launch_mode<HD, kF16, kModCapSlopes>(a, pq, pk, uq, uk, m);
-    case kModRel: return launch_mode<HD, kF16, kModRel>(a, pq, pk, uq, uk, m);
+    case kModRel:
+      if constexpr (HD == 128)
+        if (a.rel.range > kSmallRel) return launch_mode<HD, kF16, kModRelWide>(a, pq, pk, uq, uk, m);
+      return launch_mode<HD, kF16, kModRel>(a, pq, pk, uq, uk, m);
     default: return launch_mode<HD, kF16, kModPlain>(a, pq, pk, uq, uk, m);
   }
 }

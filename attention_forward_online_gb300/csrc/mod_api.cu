@@ -186,10 +186,10 @@ int osattn_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* 
   return e == cudaSuccess ? OSATTN_OK : OSATTN_ERR_CUDA;
 }
 
-size_t osattn_bwd_mod_workspace_bytes(int B, int H, int Nq, int rel_range) {
-  if (B < 1 || H < 1 || Nq < 1 || rel_range < 0) return 0;
+size_t osattn_bwd_mod_workspace_bytes(int B, int H, int Nq, int Nkv, int rel_range) {
+  if (B < 1 || H < 1 || Nq < 1 || Nkv < 1 || rel_range < 0) return 0;
   const size_t rows = static_cast<size_t>(B) * H * Nq;
-  const size_t tiles = static_cast<size_t>(B) * H * ((static_cast<size_t>(Nq) + kPlanTile - 1) / kPlanTile);
+  const size_t tiles = static_cast<size_t>(B) * H * ((static_cast<size_t>(Nkv) + 127) / 128);
   return (rows + (rel_range ? tiles * (2 * static_cast<size_t>(rel_range) + 1) : 0)) * sizeof(float);
 }
 
@@ -208,7 +208,7 @@ int osattn_bwd_mod(const void* Q, const void* K, const void* V, const void* O, c
   const bool rel = score && score->rel_table;
   if (rel != (dRel != nullptr) || (dRel && !aligned_to(dRel, 2))) return OSATTN_ERR_INVALID_ARG;
   if (!workspace || !aligned_to(workspace, 16) ||
-      workspace_bytes < osattn_bwd_mod_workspace_bytes(B, H, Nq, rel ? score->rel_range : 0))
+      workspace_bytes < osattn_bwd_mod_workspace_bytes(B, H, Nq, Nkv, rel ? score->rel_range : 0))
     return OSATTN_ERR_INVALID_ARG;
   const int64_t* in[8] = {q_strides, k_strides, v_strides, o_strides,
                           do_strides, dq_strides, dk_strides, dv_strides};

@@ -30,7 +30,7 @@ enum ScoreMode : int {
   kModSlopes = 2,
   kModCapSlopes = 3,
   kModRel = 4,
-  kModRelWide = 5  // forward at d = 128: ranges above kSmallRel
+  kModRelWide = 5  // forward and dQ at d = 128: ranges above kSmallRel
 };
 constexpr int kSmallRel = 128;
 __host__ __device__ constexpr bool mode_cap(int m) { return m == kModCap || m == kModCapSlopes; }

@@ -45,7 +45,7 @@ struct ModArgs {
   const void* O_in;
   long long o_s[3];  // its element strides of the b, h and row axes
   float* D;         // workspace [B, H, Nq]
-  float* rel_part;  // workspace [B, H, query tiles, 2 range + 1]
+  float* rel_part;  // workspace [B, H, key tiles, 2 range + 1]
   void* dRel;       // [num, H] or null
 };
 

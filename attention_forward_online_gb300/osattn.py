@@ -132,7 +132,7 @@ def lib():
             L.osattn_fwd_mod.argtypes = ([vp] * 5 + [i32] * 6 + [i64p] * 4 +
                                          [ctypes.c_float, scp, vp, i32, vp])
             L.osattn_fwd_mod.restype = i32
-            L.osattn_bwd_mod_workspace_bytes.argtypes = [i32] * 4
+            L.osattn_bwd_mod_workspace_bytes.argtypes = [i32] * 5
             L.osattn_bwd_mod_workspace_bytes.restype = sz
             L.osattn_bwd_mod.argtypes = ([vp] * 10 + [i32] * 6 + [i64p] * 8 +
                                          [ctypes.c_float, scp, vp, i32, vp, sz, vp])
@@ -787,8 +787,8 @@ def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0
     return out, lse
 
 
-def bwd_mod_workspace_bytes(B: int, H: int, Nq: int, rel_range: int = 0) -> int:
-    return int(lib().osattn_bwd_mod_workspace_bytes(int(B), int(H), int(Nq), int(rel_range)))
+def bwd_mod_workspace_bytes(B: int, H: int, Nq: int, Nkv: int, rel_range: int = 0) -> int:
+    return int(lib().osattn_bwd_mod_workspace_bytes(int(B), int(H), int(Nq), int(Nkv), int(rel_range)))
 
 
 def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap: float = 0.0,
@@ -798,7 +798,7 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
     upstream gradient `do`, from its outputs o and lse.  Arguments as for
     fwd_mod(); dk and dv are summed over the query heads of a key head.
     Outputs and the workspace (a CUDA uint8 tensor of at least
-    bwd_mod_workspace_bytes(B, H, Nq, R or 0) bytes) may be given."""
+    bwd_mod_workspace_bytes(B, H, Nq, Nkv, R or 0) bytes) may be given."""
     B, H, Hkv, Nq, Nkv, d, index = _mod_shapes(q, k, v)
     if _elsewhere(index):
         with torch.cuda.device(index):
@@ -829,7 +829,7 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
         raise ValueError("drel needs a rel_table")
     L = _lib or lib()
     if workspace is None:
-        need = L.osattn_bwd_mod_workspace_bytes(B, H, Nq, score.rel_range)
+        need = L.osattn_bwd_mod_workspace_bytes(B, H, Nq, Nkv, score.rel_range)
         workspace = q.new_empty(need, dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError("workspace must be contiguous on q's device")

@@ -542,10 +542,10 @@ int osattn_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* 
  *   dRel       device [rel_num, H], element type `dtype` (written), exactly
  *              when score->rel_table is given, else NULL
  *   workspace  device, 16-byte aligned, osattn_bwd_mod_workspace_bytes(B, H,
- *              Nq, rel_range or 0 without a rel_table) bytes
+ *              Nq, Nkv, rel_range or 0 without a rel_table) bytes
  * The other arguments as for osattn_fwd_mod; errors likewise.
  */
-size_t osattn_bwd_mod_workspace_bytes(int B, int H, int Nq, int rel_range);
+size_t osattn_bwd_mod_workspace_bytes(int B, int H, int Nq, int Nkv, int rel_range);
 int osattn_bwd_mod(const void* Q, const void* K, const void* V, const void* O, const void* dO,
                    const float* LSE, void* dQ, void* dK, void* dV, void* dRel, int B, int H,
                    int Hkv, int Nq, int Nkv, int d, const int64_t* q_strides,

@@ -154,9 +154,9 @@ def test_bwd_mod_refusals(L, kw, expect):
 
 
 def test_sizes(L):
-    assert osattn.bwd_mod_workspace_bytes(2, 3, 300) == 2 * 3 * 300 * 4
-    assert osattn.bwd_mod_workspace_bytes(2, 3, 300, 16) == (2 * 3 * 300 + 2 * 3 * 3 * 33) * 4
-    assert osattn.bwd_mod_workspace_bytes(2, 3, 0) == 0
+    assert osattn.bwd_mod_workspace_bytes(2, 3, 300, 500) == 2 * 3 * 300 * 4
+    assert osattn.bwd_mod_workspace_bytes(2, 3, 300, 500, 16) == (2 * 3 * 300 + 2 * 3 * 4 * 33) * 4
+    assert osattn.bwd_mod_workspace_bytes(2, 3, 0, 5) == 0
     assert L.osattn_mask_plan_bytes(2, 300) == 2 * (3 * 16 + 300 * 8)
     assert L.osattn_mask_plan_bytes(0, 300) == 0
 
