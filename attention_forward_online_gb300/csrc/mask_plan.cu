@@ -9,8 +9,8 @@
 //
 // One block per 128 query rows: bound by latency (a launch and, with
 // documents, the search for the ends of the runs that cross the tile).  A
-// run's end outside the tile is found by the whole block, 4096 positions a
-// step with 16 coalesced loads a thread in flight.
+// run's ends outside the tile are found by the whole block, 2048 positions a
+// step in both directions, all loads of a step in flight together.
 #include <climits>
 #include <cstdint>
 
@@ -20,7 +20,7 @@ namespace osattn {
 namespace {
 
 constexpr int kPlanThreads = 256;
-constexpr int kPerThread = 16;
+constexpr int kPerThread = 8;
 
 struct PlanParams {
   int4* tiles;
@@ -31,32 +31,40 @@ struct PlanParams {
   const int32_t* doc_ids;
 };
 
-// Smallest (dir = 1) or largest (dir = -1) position x from `from` on in
-// direction dir whose run of ids ends there (id[x + dir] differs or does not
-// exist).  The whole block calls it; `slot` is shared.
-__device__ int run_end(const int32_t* ids, int n, int from, int dir, int* slot) {
-  for (int base = 0;; base += kPlanThreads * kPerThread) {
-    if (threadIdx.x == 0) *slot = INT_MAX;
-    __syncthreads();
-    int best = INT_MAX;  // distance from `from`
+// The first positions x <= first and x >= last (both given) at which a run of
+// ids ends in that direction: ids[x - 1] or ids[x + 1] differs or does not
+// exist.  The whole block calls it; slots: [3][2], all INT_MAX, shared.  Step k
+// uses slots[k mod 3], so one barrier a step is enough.
+__device__ int2 run_ends(const int32_t* ids, int n, int first, int last, int (*slots)[2]) {
+  int back = INT_MAX, fwd = INT_MAX;  // distances found
+  for (int k = 0;; ++k) {
+    const int base = k * kPlanThreads * kPerThread + static_cast<int>(threadIdx.x);
+    int b = INT_MAX, f = INT_MAX;
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      const int dist = base + k * kPlanThreads + static_cast<int>(threadIdx.x);
-      const long long x = from + static_cast<long long>(dir) * dist;
-      if (x < 0 || x >= n) continue;
-      const long long y = x + dir;
-      if (y < 0 || y >= n || ids[y] != ids[x]) best = min(best, dist);
+    for (int u = 0; u < kPerThread; ++u) {
+      const int dist = base + u * kPlanThreads;
+      if (back == INT_MAX && dist <= first) {
+        const int x = first - dist;
+        if (x == 0 || ids[x - 1] != ids[x]) b = min(b, dist);
+      }
+      if (fwd == INT_MAX && dist < n - last) {
+        const int x = last + dist;
+        if (x == n - 1 || ids[x + 1] != ids[x]) f = min(f, dist);
+      }
     }
-    if (best != INT_MAX) atomicMin(slot, best);
+    int* slot = slots[k % 3];
+    if (b != INT_MAX) atomicMin(&slot[0], b);
+    if (f != INT_MAX) atomicMin(&slot[1], f);
     __syncthreads();
-    const int got = *slot;
-    __syncthreads();
-    if (got != INT_MAX) return from + dir * got;
+    if (back == INT_MAX) back = slot[0];
+    if (fwd == INT_MAX) fwd = slot[1];
+    if (back != INT_MAX && fwd != INT_MAX) return make_int2(first - back, last + fwd);
+    if (threadIdx.x < 2) slots[(k + 2) % 3][threadIdx.x] = INT_MAX;  // last read a step ago
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) mask_plan_kernel(const PlanParams p) {
-  __shared__ int slot, s_lo_min, s_hi_max, s_lo_max, s_hi_min, s_right;
+  __shared__ int slots[3][2], s_lo_min, s_hi_max, s_lo_max, s_hi_min, s_right;
   __shared__ int s_id[kPlanTile];
   __shared__ unsigned s_bits[2][kPlanThreads / 32];
   __shared__ int s_start[kPlanTile], s_end[kPlanTile];
@@ -79,11 +87,12 @@ __global__ void __launch_bounds__(kPlanThreads) mask_plan_kernel(const PlanParam
     const int first = static_cast<int>(at0 < 0 ? 0 : at0);
     const int last = static_cast<int>(at1 >= p.Nkv ? p.Nkv - 1 : at1);
     if (at1 >= 0 && at0 < p.Nkv) {  // uniform over the block
-      const int back = run_end(ids, p.Nkv, first, -1, &slot);
-      const int fwd = run_end(ids, p.Nkv, last, 1, &slot);
       const int n = last - first + 1;
       for (int x = r; x < n; x += kPlanThreads) s_id[x] = ids[first + x];
+      if (r < 6) slots[r / 2][r & 1] = INT_MAX;
       __syncthreads();
+      const int2 run = run_ends(ids, p.Nkv, first, last, slots);
+      const int back = run.x, fwd = run.y;
       // start and end of each position's run inside the tile, from the bits
       // of the positions where a run starts or ends
       const bool starts = r < n && (r == 0 || s_id[r - 1] != s_id[r]);
