@@ -16,6 +16,9 @@ struct ApiDevice {
   uint64_t wait_limit_ns = 0;
 };
 
+// Whether `softcap` is 0 (none) or a cap that the kernels take (NaN is not).
+inline bool cap_ok(float softcap) { return softcap == 0.f || (softcap >= 1e-3f && softcap <= 1e4f); }
+
 // The current device, set up for the library's kernels.
 int api_device(ApiDevice* out);
 

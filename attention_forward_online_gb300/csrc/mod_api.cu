@@ -64,7 +64,7 @@ int validate_mod(const void* Q, const void* K, const void* V, const void* O, con
     return OSATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * H > 0x7fffffffLL) return OSATTN_ERR_INVALID_ARG;
   if (s) {
-    if (!std::isfinite(s->softcap) || s->softcap < 0.f) return OSATTN_ERR_INVALID_ARG;
+    if (!cap_ok(s->softcap)) return OSATTN_ERR_INVALID_ARG;
     if (s->q_offset < -kMaxOffset || s->q_offset > kMaxOffset) return OSATTN_ERR_INVALID_ARG;
     if (s->slopes && !aligned_to(s->slopes, 4)) return OSATTN_ERR_INVALID_ARG;
     if (s->rel_table) {

@@ -88,9 +88,10 @@ __device__ __forceinline__ float cap_r(float s, float c1) { return rcp_approx(1.
 // 3: coefficients fitted here for the least relative error on that range
 // (2^-23.3, reweighted least squares on Chebyshev points).  k[n] carries
 // cap2 (scale / cap)^(2 n + 1), so that the polynomial is in the raw score:
-// cap2 tanh = s (k0 + s^2 (k1 + ...)).  s_max = 0.4 cap / |scale|, or -1 where
-// |scale| / cap is not in [2^-12, 2^12] (products could leave fp32's range):
-// then the other form is used.
+// cap2 tanh = s (k0 + s^2 (k1 + ...)).  s_max = 0.4 cap / |scale|, but at most
+// 2^16 where |scale| / cap is below 2^-19 (k[3] leaves fp32's range there, and
+// is not needed up to 2^16), and -1 where it is above 2^12: then only the
+// other form is used.  c1 is kept finite (inf times a score of 0 is NaN).
 struct CapArgs {
   float c1, cap2, s_max;  // c1 = 2 scale log2(e) / cap
   float inv2;             // 1 / cap2^2
@@ -101,13 +102,14 @@ inline CapArgs make_cap(float scale, float softcap) {
   if (!(softcap > 0.f)) return c;
   const double a = static_cast<double>(scale) / softcap;  // the tanh is odd: either sign
   const double cap2 = static_cast<double>(softcap) * 1.4426950408889634;
-  c.c1 = static_cast<float>(2.0 * a * 1.4426950408889634);
+  const double c1 = 2.0 * a * 1.4426950408889634;
+  c.c1 = static_cast<float>(c1 > 3e38 ? 3e38 : c1 < -3e38 ? -3e38 : c1);
   c.cap2 = static_cast<float>(cap2);
   c.inv2 = static_cast<float>(1.0 / (cap2 * cap2));
   const double t[4] = {0.9999999019, -0.3333136247, 0.1327097680, -0.0475536037};
-  const double size = a < 0 ? -a : a;
-  const bool ok = size >= 1.0 / 4096 && size <= 4096.0;
-  c.s_max = ok ? static_cast<float>(0.4 / size) : -1.f;
+  const double size = a < 0 ? -a : a, low = 1.0 / 524288;
+  const bool ok = size <= 4096.0;
+  c.s_max = !ok ? -1.f : (size < low ? 65536.f : static_cast<float>(0.4 / size));
   double pw = a;
   for (int n = 0; n < 4; ++n, pw *= a * a) c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;
   return c;

@@ -59,7 +59,7 @@ int osattn_tree_attn(const void* Q, const void* K_pages, const void* V_pages,
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || T < 1 || d < 1 || num_pages < 1 || page_size < 1 ||
       max_pages < 1 || window < 0)
     return OSATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return OSATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !cap_ok(softcap)) return OSATTN_ERR_INVALID_ARG;
   if (!aligned_to(Q, 16) || !aligned_to(K_pages, 16) || !aligned_to(V_pages, 16) || !aligned_to(O, 16) ||
       !aligned_to(LSE, 4) || !aligned_to(page_table, 4) || !aligned_to(ctx_len, 4) ||
       (tree_mask && !aligned_to(tree_mask, 8)) || (slopes && !aligned_to(slopes, 4)) ||

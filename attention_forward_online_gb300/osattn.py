@@ -758,7 +758,7 @@ def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0
     is contiguous.
 
     The scaled score y of query position p and key j becomes
-    softcap * tanh(y / softcap) if softcap > 0, then y - slopes[h] |j - p|
+    softcap * tanh(y / softcap) if softcap > 0 (0.001 .. 10000), then y - slopes[h] |j - p|
     (slopes: fp32 [H]) or y + rel_table[rel_map[clamp(j - p, -R, R) + R], h]
     (rel_table: [buckets, H] in q's dtype; rel_map: int32 [2 R + 1], see
     rel_buckets()).  plan: a MaskPlan, or None for no mask.  A row that sees

@@ -2,6 +2,9 @@
 osattn_bwd_mod) against the 64-bit forms of _mod_ref.py, every output element
 within the bound derived there."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -175,6 +178,13 @@ def test_scores_far_beyond_the_cap():
     compare(*tensors(1, 2, 2, 140, 140, 64, BF, seed=9, std=60.0), dict(causal=True), cap=2.0)
 
 
+@pytest.mark.parametrize("cap", [1e-3, 0.5, 300.0, 1e4])
+def test_caps_of_every_size(cap):
+    compare(*tensors(1, 2, 1, 150, 200, 64, BF, seed=10), dict(key_len=i32([190])), cap=cap)
+    # scores on both sides of 0.4 cap, where the form of the tanh changes
+    compare(*tensors(1, 2, 1, 150, 200, 64, FP, seed=13, std=cap if 0.1 < cap < 1e3 else 2.0), {}, cap=cap)
+
+
 @pytest.mark.parametrize("fill", [math.nan, math.inf, -math.inf, 3e38])
 @pytest.mark.parametrize("kind", ["plain", "cap", "slopes", "rel"])
 def test_masked_places_hold_anything(kind, fill):
@@ -242,6 +252,32 @@ def test_same_bits_again_and_in_a_graph():
         torch.cuda.synchronize()
         for x, n in zip(outs, ("o", "lse", "dq", "dk", "dv", "drel")):
             assert torch.equal(x, first[n]), n
+
+
+def test_first_call_of_a_process_may_be_captured():
+    code = """
+import torch
+from attention_forward_online_gb300 import osattn
+g = torch.Generator(device="cuda").manual_seed(1)
+q, k, v = (torch.randn(1, 2, 200, 64, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+osattn.fwd(q, k, v)  # the library's set-up of the device
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    plan = osattn.mask_plan(1, 200, 200, causal=True, device="cuda")
+    o, lse = osattn.fwd_mod(q, k, v, plan=plan, softcap=5.0)
+    grads = osattn.bwd_mod(q, k, v, o, lse, q, plan=plan, softcap=5.0)
+graph.replay()
+torch.cuda.synchronize()
+plan = osattn.mask_plan(1, 200, 200, causal=True, device="cuda")
+o2, lse2 = osattn.fwd_mod(q, k, v, plan=plan, softcap=5.0)
+assert torch.equal(o, o2) and torch.equal(lse, lse2)
+for a, b in zip(grads, osattn.bwd_mod(q, k, v, o, lse, q, plan=plan, softcap=5.0)):
+    assert torch.equal(a, b)
+assert osattn.get_device_status() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=120)
 
 
 def test_two_streams_at_once():

@@ -84,6 +84,9 @@ SHAPES = [
     (2, 8, 1, 64, 16, [64, 1500]),
     (1, 16, 1, 64, 384, [700]),
     (40, 4, 2, 3, 16, [(37 * x) % 600 for x in range(40)]),
+    (1, 96, 1, 3, 16, [200]),    # one token a row tile
+    (2, 128, 1, 2, 8, [130, 9]),  # a group that fills the tile
+    (700, 1, 1, 1, 8, [x % 20 for x in range(700)]),  # more sequences than threads
 ]
 
 

@@ -129,7 +129,8 @@ BAD, NOT = osattn.ERR_INVALID_ARG, osattn.ERR_UNSUPPORTED
     (dict(Nq=0), BAD), (dict(Nkv=0), BAD), (dict(B=0), BAD), (dict(plan=P + 8), BAD),
     (dict(Nq=(1 << 30) + 1), BAD), (dict(scale=math.inf), BAD), (dict(d=80), NOT), (dict(dtype=osattn.FP32), NOT),
     (dict(score=osattn._Score(softcap=-1.0)), BAD), (dict(score=osattn._Score(softcap=math.nan)), BAD),
-    (dict(score=osattn._Score(softcap=math.inf)), BAD), (dict(score=osattn._Score(slopes=P + 2)), BAD),
+    (dict(score=osattn._Score(softcap=math.inf)), BAD), (dict(score=osattn._Score(softcap=9e-4)), BAD),
+    (dict(score=osattn._Score(softcap=10001.0)), BAD), (dict(score=osattn._Score(slopes=P + 2)), BAD),
     (dict(score=osattn._Score(q_offset=(1 << 30) + 1)), BAD),
     (dict(score=rel_score(slopes=P)), BAD), (dict(score=rel_score(rel_map=None)), BAD),
     (dict(score=rel_score(rel_num=0)), BAD), (dict(score=rel_score(rel_range=0)), BAD),

@@ -39,7 +39,7 @@ def call(**kw):
     (dict(p=[P] * 3 + [P + 2, P]), BAD), (dict(o=P + 8), BAD),
     (dict(B=0), BAD), (dict(T=0), BAD), (dict(H=7), BAD), (dict(Hkv=0), BAD), (dict(pages=0), BAD),
     (dict(page=0), BAD), (dict(per=0), BAD), (dict(window=-1), BAD), (dict(scale=math.nan), BAD),
-    (dict(cap=-2.0), BAD), (dict(cap=math.inf), BAD),
+    (dict(cap=-2.0), BAD), (dict(cap=math.inf), BAD), (dict(cap=1e-4), BAD),
     (dict(T=65), NOT), (dict(H=258, Hkv=2), NOT), (dict(d=96), NOT), (dict(dtype=osattn.FP32), NOT),
     (dict(page=4), NOT), (dict(page=24), NOT), (dict(page=192), NOT),
     (dict(page=8, per=1, T=9), BAD),                     # the drafts do not fit the table
