@@ -439,6 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   unit_of(p, bhk, kt);
   const int b = bhk / p.Hkv, hk = bhk % p.Hkv;
   const int k0 = kt * kT;
+  // this thread's first query tile of the search below, on its way during the set-up
+  int4 entry = static_cast<int>(threadIdx.x) < p.q_tiles ? plan_load(p.plan, b, p.q_tiles, threadIdx.x, p.Nkv)
+                                                         : make_int4(0, 0, 0, 0);
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->fixed_full, 1);
@@ -472,11 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // Query tiles [it_lo, it_hi) hold every row that sees one of these keys.
   for (int q = threadIdx.x; q < p.q_tiles; q += kThreads) {
-    const PlanTile pt = plan_tile(p.plan, b, p.q_tiles, q, p.Nkv);
-    if (pt.lo < k0 + kT && pt.hi > k0) {
+    if (entry.x < k0 + kT && entry.y > k0) {
       atomicMin(&bars->it_lo, q);
       atomicMax(&bars->it_hi, q + 1);
     }
+    if (q + kThreads < p.q_tiles) entry = plan_load(p.plan, b, p.q_tiles, q + kThreads, p.Nkv);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -941,9 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   [[maybe_unused]] float slope = 0.f;
   if constexpr (mode_slopes(MODE)) slope = __ldg(p.slopes + h);
   const int q0 = qt * kT;
-  const PlanTile pt = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
-  const int kt0 = pt.lo / kT;
-  const int n_kt = pt.lo < pt.hi ? (pt.hi + kT - 1) / kT - kt0 : 0;
+  const int4 entry = plan_load(p.plan, b, p.q_tiles, qt, p.Nkv);  // on its way during the set-up
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->fixed_full, 1);
@@ -982,6 +983,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
+  const PlanTile pt = plan_entry(entry);
+  const int kt0 = pt.lo / kT;
+  const int n_kt = pt.lo < pt.hi ? (pt.hi + kT - 1) / kT - kt0 : 0;
 
   if (warp == kProdWarp) {
     if (lane == 0 && n_kt > 0) {

@@ -526,21 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (mode_slopes(MODE)) slope = __ldg(p.slopes + h);
   const int q0 = qb * (kQTiles * BM);
   const int t0 = qb * kQTiles;
-  const PlanTile pt0 = plan_tile(p.plan, b, p.n_tiles, t0, p.Nkv);
-  const PlanTile pt1 =
-      t0 + 1 < p.n_tiles ? plan_tile(p.plan, b, p.n_tiles, t0 + 1, p.Nkv) : PlanTile{0, 0, 0, 0, false};
-  const bool any0 = pt0.lo < pt0.hi, any1 = pt1.lo < pt1.hi;
-  int lo = 0, hi = 0;  // keys that either tile sees
-  if (any0) lo = pt0.lo, hi = pt0.hi;
-  if (any1) {
-    lo = any0 ? min(lo, pt1.lo) : pt1.lo;
-    hi = max(hi, pt1.hi);
-  }
-  const int kt0 = lo / BN;
-  const int n = (hi + BN - 1) / BN - kt0;  // 0 when no row sees a key (lo = hi = 0)
-  Range r0{0, 0}, r1{0, 0};
-  if (any0) r0 = Range{pt0.lo / BN - kt0, (pt0.hi + BN - 1) / BN - pt0.lo / BN};
-  if (any1) r1 = Range{pt1.lo / BN - kt0, (pt1.hi + BN - 1) / BN - pt1.lo / BN};
+  // (on their way during the set-up)
+  const int4 entry0 = plan_load(p.plan, b, p.n_tiles, t0, p.Nkv);
+  const int4 entry1 = t0 + 1 < p.n_tiles ? plan_load(p.plan, b, p.n_tiles, t0 + 1, p.Nkv) : make_int4(0, 0, 0, 0);
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < kQTiles; ++t) {
@@ -580,6 +568,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
+  const PlanTile pt0 = plan_entry(entry0), pt1 = plan_entry(entry1);
+  const bool any0 = pt0.lo < pt0.hi, any1 = pt1.lo < pt1.hi;
+  int lo = 0, hi = 0;  // keys that either tile sees
+  if (any0) lo = pt0.lo, hi = pt0.hi;
+  if (any1) {
+    lo = any0 ? min(lo, pt1.lo) : pt1.lo;
+    hi = max(hi, pt1.hi);
+  }
+  const int kt0 = lo / BN;
+  const int n = (hi + BN - 1) / BN - kt0;  // 0 when no row sees a key (lo = hi = 0)
+  Range r0{0, 0}, r1{0, 0};
+  if (any0) r0 = Range{pt0.lo / BN - kt0, (pt0.hi + BN - 1) / BN - pt0.lo / BN};
+  if (any1) r1 = Range{pt1.lo / BN - kt0, (pt1.hi + BN - 1) / BN - pt1.lo / BN};
 
   // 256 x 184 + 128 x 88 + 128 x 56 = 512 x 128 registers
   if (warp < kCorrWarp0) {

@@ -52,10 +52,15 @@ struct PlanTile {
   bool left;
 };
 
-__device__ __forceinline__ PlanTile plan_tile(const PlanView& pv, int b, int n_tiles, int tile, int Nkv) {
-  if (!pv.tiles) return PlanTile{0, Nkv, 0, Nkv, false};
-  const int4 t = pv.tiles[static_cast<long long>(b) * n_tiles + tile];
+__device__ __forceinline__ int4 plan_load(const PlanView& pv, int b, int n_tiles, int tile, int Nkv) {
+  if (!pv.tiles) return make_int4(0, Nkv, 0, Nkv);
+  return pv.tiles[static_cast<long long>(b) * n_tiles + tile];
+}
+__device__ __forceinline__ PlanTile plan_entry(int4 t) {
   return PlanTile{t.x, t.y, t.z & (kPlanLeft - 1), t.w, (t.z & kPlanLeft) != 0};
+}
+__device__ __forceinline__ PlanTile plan_tile(const PlanView& pv, int b, int n_tiles, int tile, int Nkv) {
+  return plan_entry(plan_load(pv, b, n_tiles, tile, Nkv));
 }
 
 __device__ __forceinline__ int2 plan_row(const PlanView& pv, int b, int Nq, int i, int Nkv) {
