@@ -797,23 +797,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ combine
-// One warp a row: joins the partials of the CTAs that share the row's unit,
-// in CTA order.  Rows of units that one CTA did whole are done already.  Runs
-// as a dependent launch: resident before the main kernel ends where there is
-// room, waiting for it in griddepcontrol.wait.
-template <int HD, bool kF16>
+// One warp a row joins the partials of the CTAs that share the row's unit, in
+// CTA order; with many partials a unit, kWays warps (8, not 1) take every
+// kWays-th of them and are joined in order too.  Rows of units that one CTA did
+// whole are done already.  Runs as a dependent launch: resident before the
+// main kernel ends where there is room, waiting for it in griddepcontrol.wait.
+template <int HD, bool kF16, int kWays>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const Params p, int grid) {
   constexpr int CPL = HD / 32;
-  const int per_unit = (p.slot_rows + 7) / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_unit = (p.slot_rows * kWays + 7) / 8;
   const int unit_all = blockIdx.x / per_unit;
-  const int row = (blockIdx.x - unit_all * per_unit) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int row = kWays == 1 ? (blockIdx.x - unit_all * per_unit) * 8 + warp : blockIdx.x - unit_all * per_unit;
+  const int way = kWays == 1 ? 0 : warp;
   const int units = p.Hkv * p.row_tiles;
   const int b = unit_all / units, unit = unit_all - b * units;
   const int hk = unit / p.row_tiles, rt = unit - hk * p.row_tiles;
   const int tl = row / p.group, g = row - tl * p.group;
   const int tok = rt * p.tok_tile + tl;
-  if (row >= p.slot_rows || tl >= p.tok_tile || tok >= p.T) return;
+  if (row >= p.slot_rows || tl >= p.tok_tile || tok >= p.T) return;  // (the whole block if kWays > 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int base = p.head[b], n_b = (p.head[b + 1] - base) / units;
   const long long total = p.head[p.B], G = shares(p.head[p.B], grid);
@@ -824,20 +826,20 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const Params p, int g
   // a partial is the state (m, l) = (lse, 1) carrying O / l
   auto row_of = [&](int c) { return static_cast<long long>(2 * c + (c == c0 ? 1 : 0)) * p.slot_rows + row; };
   float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.lse_part[row_of(c)]);
+  for (int c = c0 + way + kWays * lane; c <= c1; c += 32 * kWays) top = fmaxf(top, p.lse_part[row_of(c)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   float l = 0.f, acc[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
-  for (int cb = c0; cb <= c1; cb += 32) {
-    const int n = min(32, c1 - cb + 1);
-    const float lse = lane < n ? p.lse_part[row_of(cb + lane)] : -INFINITY;
+  for (int cb = c0 + way; cb <= c1; cb += 32 * kWays) {
+    const int n = min(32, (c1 - cb) / kWays + 1);
+    const float lse = lane < n ? p.lse_part[row_of(cb + kWays * lane)] : -INFINITY;
     const float weight = lse == -INFINITY ? 0.f : expf(lse - top);  // (NaN stays NaN)
 #pragma unroll 8
     for (int x = 0; x < n; ++x) {
       const float w = __shfl_sync(0xffffffffu, weight, x);
-      const float* src = p.o_part + row_of(cb + x) * HD + lane * CPL;
+      const float* src = p.o_part + row_of(cb + kWays * x) * HD + lane * CPL;
       float o[CPL];
       if constexpr (CPL == 4) {
         const float4 v = *reinterpret_cast<const float4*>(src);
@@ -849,6 +851,27 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const Params p, int g
 #pragma unroll
       for (int k = 0; k < CPL; ++k) acc[k] = fmaf(w, o[k], acc[k]);
       l += w;
+    }
+  }
+  if constexpr (kWays > 1) {
+    __shared__ float joined[kWays][HD + 2];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) joined[warp][lane * CPL + k] = acc[k];
+    if (lane == 0) {
+      joined[warp][HD] = top;
+      joined[warp][HD + 1] = l;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    for (int x = 1; x < kWays; ++x) top = fmaxf(top, joined[x][HD]);
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
+    for (int x = 0; x < kWays; ++x) {
+      const float lx = joined[x][HD + 1], w = lx == 0.f ? 0.f : expf(joined[x][HD] - top);
+      l = fmaf(lx, w, l);
+#pragma unroll
+      for (int k = 0; k < CPL; ++k) acc[k] = fmaf(joined[x][lane * CPL + k], w, acc[k]);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -889,7 +912,11 @@ cudaError_t launch_mode(int grid, cudaStream_t s, const CUtensorMap& q, const CU
   tree_kernel<HD, kF16, MODE><<<grid, kThreads, smem_bytes<HD, MODE>(), s>>>(q, k, v, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.row_tiles * ((p.slot_rows + 7) / 8);
+  const long long units = static_cast<long long>(p.B) * p.Hkv * p.row_tiles;
+  // 16 or more partials a unit, if the units are about alike: 8 warps a row (19 partials, H32 kv8 ctx
+  // 32000: 34.5 us against 36.6 with one warp; at 9.5, B2 H16 kv2 T64 d64: 67.4 against 65.6)
+  const int ways = grid >= 16 * units ? 8 : 1;
+  const long long blocks = units * ((static_cast<long long>(p.slot_rows) * ways + 7) / 8);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -900,7 +927,8 @@ cudaError_t launch_mode(int grid, cudaStream_t s, const CUtensorMap& q, const CU
   dep.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &dep;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, kF16>, p, grid);
+  return ways == 1 ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, kF16, 1>, p, grid)
+                   : cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, kF16, 8>, p, grid);
 }
 
 template <int HD, bool kF16>

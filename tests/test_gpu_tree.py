@@ -86,6 +86,8 @@ SHAPES = [
     (40, 4, 2, 3, 16, [(37 * x) % 600 for x in range(40)]),
     (1, 96, 1, 3, 16, [200]),    # one token a row tile
     (2, 128, 1, 2, 8, [130, 9]),  # a group that fills the tile
+    (1, 8, 1, 2, 64, [9000]),    # many partials a row
+    (1, 20, 1, 9, 16, [20011]),
     (700, 1, 1, 1, 8, [x % 20 for x in range(700)]),  # more sequences than threads
 ]
 
