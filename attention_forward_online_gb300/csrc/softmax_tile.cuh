@@ -138,10 +138,10 @@ struct TileScore {
   // 2^(kMaxSlack + this), which has to stay a finite 16-bit value.
   static constexpr float kSpread = kF16 ? 7.f : 64.f;
 
-  // Distances that grow by one from key to key.
+  // Distances that grow by one from key to key: of key e of chunk ch.
   __device__ __forceinline__ auto by_place() const {
     const float d = d0;
-    return [d](int e) { return d + static_cast<float>(e); };
+    return [d](int ch) { return [d, ch](int e) { return d + static_cast<float>(32 * ch + e); }; };
   }
 
   // cap(s) c of one score
@@ -153,7 +153,7 @@ struct TileScore {
   // One tile of the row: S at s_addr becomes P = 2^(x - m) in 16 bits over its
   // first 64 columns.  Moves m, publishes the factor of the accumulator by
   // publish(alpha_bits) as soon as it is known, and updates l.
-  // gap(e): the distance of key e of the tile, for both_sides.
+  // gap(ch)(e): the distance of key e of chunk ch, for both_sides.
   // kMasked: some rows of the warp may not see all of the tile.
   template <bool kMasked, typename BitsOf, typename Gap, typename Publish>
   __device__ __forceinline__ void tile(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
@@ -313,9 +313,10 @@ struct TileScore {
     }
     if constexpr (mode_slopes(MODE)) {
       const float mul = mode_cap(MODE) ? 1.f : c;
+      const auto dist = gap(ch);
 #pragma unroll
       for (int e = 0; e < 32; ++e)
-        v[e] = __float_as_uint(fmaf(-slope2, fabsf(gap(ch * 32 + e)), __uint_as_float(v[e]) * mul));
+        v[e] = __float_as_uint(fmaf(-slope2, fabsf(dist(e)), __uint_as_float(v[e]) * mul));
     }
   }
 

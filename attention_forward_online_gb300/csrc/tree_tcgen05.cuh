@@ -336,10 +336,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
             if (lane + 32 < p.T) dep1 = static_cast<float>(depth_of(mask_of(p, at.b, lane + 32)));
           }
         }
-        auto gap = [&](int e) {
-          const int u = k0 + e - ctx;  // (uniform over the warp)
-          if (u < 0) return ts.d0 + static_cast<float>(e);
-          return __shfl_sync(0xffffffffu, u < 32 ? dep0 : dep1, u & 31) - static_cast<float>(depth);
+        // before the drafts by place; lane x fetches the depth of the draft in column x of the chunk
+        auto gap = [&](int ch) {
+          const int before = ctx - (k0 + 32 * ch), u = lane - before;
+          const float a = __shfl_sync(0xffffffffu, dep0, u & 31), b = __shfl_sync(0xffffffffu, dep1, u & 31);
+          const float draft = u < 32 ? a : b, own = static_cast<float>(depth), first = ts.d0 + static_cast<float>(32 * ch);
+          return [=](int e) {
+            const float at = __shfl_sync(0xffffffffu, draft, e) - own;
+            return e < before ? first + static_cast<float>(e) : at;
+          };
         };
         ts.tile_rolled(s_addr, mk, bits_of, gap, m, l, publish);
       } else {
