@@ -132,6 +132,9 @@ struct Params {
   int q_tiles;      // 128-row query tiles per (b, h)
   int num_tiles;    // this kernel's tiles per head
   int BH;           // this kernel's heads: B * H (dq) or B * Hkv (dkdv)
+  int split;        // dkdv: CTAs (of one cluster) that share a key tile's query tiles
+  uint16_t* dkv[2];        // dkdv with split > 1: dV, dK
+  long long dkv_s[2][3];
   int group_heads;  // heads per last-tile-first (dq) or first-tile-first (dkdv) group of CTAs
   float scale;
   float scale_log2;
@@ -170,6 +173,20 @@ __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t tx_byte
                : "memory");
 }
 
+// Barrier over a cluster's CTAs, with their shared memory in order.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four floats at `at` (an address of this CTA) in the shared memory of CTA `rank`.
+__device__ __forceinline__ void cluster_load4(uint32_t at, int rank, float* v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+      : "r"(at), "r"(rank)
+      : "memory");
+}
+
 // Barrier over the 256 elementwise threads, bounded like every other wait
 // (a warp that gave up elsewhere must not leave the rest waiting).  phase
 // counts the barrier's uses; false: give up.
@@ -182,11 +199,11 @@ __device__ __forceinline__ bool elem_sync(Bars* bars, uint32_t& phase, const Wai
 
 // The head and the rank by length (0 = longest under a causal mask) of this
 // CTA's tile: heads in groups whose streamed tiles fit in L2 together.
-__device__ __forceinline__ void unit_of(const Params& p, int& bh, int& rank) {
+__device__ __forceinline__ void unit_of(const Params& p, int unit, int& bh, int& rank) {
   const int nt = p.num_tiles, G = p.group_heads;
-  const int g0 = (static_cast<int>(blockIdx.x) / (G * nt)) * G;
+  const int g0 = (unit / (G * nt)) * G;
   const int gsize = min(G, p.BH - g0);
-  const int r = static_cast<int>(blockIdx.x) - g0 * nt;
+  const int r = unit - g0 * nt;
   bh = g0 + r % gsize;
   rank = r / gsize;
 }
@@ -436,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int bhk, kt;
-  unit_of(p, bhk, kt);
+  const int part = blockIdx.x % p.split;
+  unit_of(p, blockIdx.x / p.split, bhk, kt);
   const int b = bhk / p.Hkv, hk = bhk % p.Hkv;
   const int k0 = kt * kT;
   // this thread's first query tile of the search below, on its way during the set-up
@@ -486,7 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const int it_lo = bars->it_lo;
   const int cnt = max(0, bars->it_hi - it_lo);  // query tiles per head
-  const int n_it = cnt * p.group;
+  // This CTA's share [first, first + n_it) of the key tile's (head, query tile)
+  // pairs; with a learned bias it is whole heads, as the sums by distance are
+  // a head's.
+  const int pairs = cnt * p.group;
+  const int first_it = static_cast<int>(static_cast<long long>(pairs) * part / p.split);
+  const int n_it = static_cast<int>(static_cast<long long>(pairs) * (part + 1) / p.split) - first_it;
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
 
@@ -510,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto load_rows = [&](int it) {
         RowValues v;
-        const int h = hk * p.group + it / cnt, qt = it_lo + it % cnt;
+        const int h = hk * p.group + (first_it + it) / cnt, qt = it_lo + (first_it + it) % cnt;
         const long long rowbase = (static_cast<long long>(b) * p.H + h) * p.Nq;
 #pragma unroll
         for (int r = 0; r < kT / 32; ++r) {
@@ -528,14 +551,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       [[maybe_unused]] bool linear = false;
       for (int it = 0; it < n_it; ++it) {
         const int s = it % C::kStages;
-        const int h = hk * p.group + it / cnt;
-        const int qt = it_lo + it % cnt, q0 = qt * kT;
+        const int head = (first_it + it) / cnt, h = hk * p.group + head;
+        const int qt = it_lo + (first_it + it) % cnt, q0 = qt * kT;
         const RowValues now = next;
         if (it + 1 < n_it) next = load_rows(it + 1);
         [[maybe_unused]] float lin = 0.f;  // what a linear slope leaves: lin (k0 - position)
         [[maybe_unused]] int side = 0;
         if constexpr (MODE == kModSlopes) {
-          if (it % cnt == 0) {
+          if (it == 0 || qt == it_lo) {
             slope = __ldg(p.slopes + h);
             linear = slope_linear(slope, p.scale);
           }
@@ -585,10 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (MODE == kModSlopes) {
           // A head's operand goes to place (head mod 4): the tiles of the head
           // that had it are at least 4 tiles, so at least a ring, back.
-          if (it % cnt == 0) {
+          if (it == 0 || qt == it_lo) {
             if (lane < 8)
               slope_fill_q<kF16>(reinterpret_cast<uint8_t*>(bias_all) + kSlopeRowsBytes +
-                                     (it / cnt) % 4 * kSlopeQBytes,
+                                     head % 4 * kSlopeQBytes,
                                  lane, slope, p.scale);
             fence_proxy_async();
           }
@@ -623,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sq = smem_u32(ring), sdo = sq + C::kTileBytes;
         mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(sq, 16, 1024));
         if constexpr (MODE == kModSlopes)
-          add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes, smem_u32(bias_all), bars->side[0]);
+          add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + first_it / cnt % 4 * kSlopeQBytes,
+                            smem_u32(bias_all), bars->side[0]);
         mma_commit<true>(&bars->s_full[0]);
         mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(sdo, 16, 1024));
         mma_commit<true>(&bars->dp_full);
@@ -644,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
           mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(nq, 16, 1024));
           if constexpr (MODE == kModSlopes)
-            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + (it + 1) / cnt % 4 * kSlopeQBytes,
+            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + (first_it + it + 1) / cnt % 4 * kSlopeQBytes,
                               smem_u32(bias_all), bars->side[s1]);
           mma_commit<true>(&bars->s_full[0]);
         }
@@ -707,13 +731,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = threadIdx.x; x < sum_entries(p.rel.range); x += 256) sums[x] = 0.f;
       if (n_it == 0) {  // nobody sees these keys: every head's sums are 0
         ok = elem_sync(bars, sync_phase, wc);
-        for (int g = 0; ok && g < p.group; ++g) ok = flush_sums(hk * p.group + g);
+        const int heads = p.group / p.split;
+        for (int g = part * heads; ok && g < (part + 1) * heads; ++g) ok = flush_sums(hk * p.group + g);
       }
     }
     for (int it = 0; ok && it < n_it; ++it) {
       const int s = it % C::kStages;
-      const int h = hk * p.group + it / cnt;
-      const int qt = it_lo + it % cnt;
+      const int h = hk * p.group + (first_it + it) / cnt;
+      const int qt = it_lo + (first_it + it) % cnt;
       const int p0 = qt * kT + p.q_offset;  // position of the tile's first query
       if (h != h_of) {  // uniform over the elementwise warps
         if constexpr (mode_slopes(MODE)) slope2 = p.slopes[h] * kModLog2e;
@@ -883,7 +908,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) tc_fence_after_sync();
       has_acc = ok;
     }
-    if (ok) {
+    if (ok && p.split > 1) {
+      // fp32 over the tiles, whose last readers are done, for the join below
+      const int w = warp >> 2;
+      float4* out = reinterpret_cast<float4*>(smem + w * kT * HD * 4) + row * (HD / 4);
+      const uint32_t acc = lane_base + (w == 0 ? C::kColAcc0 : C::kColAcc1);
+#pragma unroll 1
+      for (int ch = 0; ch < HD / 32; ++ch) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + ch * 32, r);
+        tmem_ld_wait();
+        reg_fence32(r);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          out[(ch * 8 + x) ^ (row & 7)] =
+              has_acc ? make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
+                                    __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3]))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    } else if (ok) {
       // over V and K, whose last readers are done
       const int w = warp >> 2;
       uint8_t* out = w == 0 ? sV : sK;
@@ -905,6 +948,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncwarp();
+  if (p.split > 1) {
+    // The sums of the cluster's CTAs, added in rank order; each CTA finishes
+    // its share of the rows.  (A CTA whose waits gave up comes here too.)
+    cluster_sync();
+    const int rows = kT / p.split;
+    for (int x = threadIdx.x; x < 2 * rows * (HD / 8); x += kThreads) {
+      const int w = x / (rows * (HD / 8)), c = x % (HD / 8);
+      const int row = part * rows + x / (HD / 8) % rows;
+      const uint32_t at = smem_u32(smem) + (w * kT + row) * HD * 4;
+      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < p.split; ++r) {
+        float v[8];
+        cluster_load4(at + ((2 * c) ^ (row & 7)) * 16, r, v);
+        cluster_load4(at + ((2 * c + 1) ^ (row & 7)) * 16, r, v + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += v[e];
+      }
+      const float mul = w == 0 ? 1.f : p.scale;
+      if (k0 + row < p.Nkv)
+        *reinterpret_cast<uint4*>(p.dkv[w] + b * p.dkv_s[w][0] + hk * p.dkv_s[w][1] + (k0 + row) * p.dkv_s[w][2] + 8 * c) =
+            make_uint4(pack2<kF16>(a[0] * mul, a[1] * mul), pack2<kF16>(a[2] * mul, a[3] * mul),
+                       pack2<kF16>(a[4] * mul, a[5] * mul), pack2<kF16>(a[6] * mul, a[7] * mul));
+    }
+    cluster_sync();  // the others have read this CTA's sums
+  }
   tmem_st_wait();
   tc_fence_before_sync();
   __syncthreads();
@@ -938,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int bh, rank;
-  unit_of(p, bh, rank);
+  unit_of(p, blockIdx.x, bh, rank);
   const int qt = p.num_tiles - 1 - rank;
   const int b = bh / p.H, h = bh % p.H, hk = h / p.group;
   [[maybe_unused]] float slope = 0.f;
@@ -1295,6 +1363,20 @@ __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restric
   }
 }
 
+// CTAs that share a key tile's (head, query tile) pairs, of which it has at
+// most `pairs`: a power of two that divides `of`, leaves a CTA two pairs, and
+// makes the kernel shortest if a CTA takes 1 / split of a tile's time and a
+// quarter of it besides, and the SMs take the CTAs in rounds.
+inline int dkdv_split(long long units, int num_sms, long long pairs, int of) {
+  int best = 1;
+  double cost = 0.0;
+  for (int s = 1; s == 1 || (s <= 8 && of % s == 0 && 2 * s <= pairs); s *= 2) {
+    const double c = static_cast<double>((units * s + num_sms - 1) / num_sms) * (1.0 / s + 0.25);
+    if (s == 1 || c < cost) best = s, cost = c;
+  }
+  return best;
+}
+
 template <int HD, bool kF16, int MODE>
 cudaError_t set_attrs() {
   constexpr int kDkdvMode = MODE == kModRelWide ? kModRel : MODE;
@@ -1328,8 +1410,18 @@ cudaError_t launch_mode(const ModArgs& a, const Params& pq, const Params& pk, un
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   constexpr int kDkdvMode = MODE == kModRelWide ? kModRel : MODE;
-  dkdv_kernel<HD, kF16, kDkdvMode><<<gk, kThreads, dkdv_smem_bytes<HD, kDkdvMode>(), a.stream>>>(m.q, m.k, m.v, m.g, m.dk, m.dv, pk);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(gk);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = dkdv_smem_bytes<HD, kDkdvMode>();
+  cfg.stream = a.stream;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = static_cast<unsigned>(pk.split);
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = pk.split > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, dkdv_kernel<HD, kF16, kDkdvMode>, m.q, m.k, m.v, m.g, m.dk, m.dv, pk);
   if (e != cudaSuccess || !mode_rel(MODE)) return e;
   rel_reduce_kernel<kF16><<<a.H, 1024, 0, a.stream>>>(a.rel_part, static_cast<uint16_t*>(a.dRel), a.rel,
                                                       a.B, a.H, pk.num_tiles);
@@ -1338,7 +1430,7 @@ cudaError_t launch_mode(const ModArgs& a, const Params& pq, const Params& pk, un
 
 template <int HD, bool kF16>
 cudaError_t launch(const ModArgs& a, const BwdModMaps& m) {
-  Params p;
+  Params p = {};
   for (int i = 0; i < 3; ++i) p.o_s[i] = a.o_s[i];
   p.LSE = a.LSE;
   p.D = a.D;
@@ -1373,7 +1465,15 @@ cudaError_t launch(const ModArgs& a, const BwdModMaps& m) {
   pq.BH = a.B * a.H;
   pq.num_tiles = p.q_tiles;
   pq.group_heads = group(a.Nkv, pq.BH);
-  const long long gk = static_cast<long long>(pk.num_tiles) * pk.BH;
+  pk.split = dkdv_split(static_cast<long long>(pk.num_tiles) * pk.BH, a.num_sms,
+                        static_cast<long long>(p.q_tiles) * p.group, a.rel.table ? p.group : 8);
+  pk.dkv[0] = static_cast<uint16_t*>(a.dV);
+  pk.dkv[1] = static_cast<uint16_t*>(a.dK);
+  for (int i = 0; i < 3; ++i) {
+    pk.dkv_s[0][i] = a.dv_s[i];
+    pk.dkv_s[1][i] = a.dk_s[i];
+  }
+  const long long gk = static_cast<long long>(pk.num_tiles) * pk.BH * pk.split;
   const long long gq = static_cast<long long>(pq.num_tiles) * pq.BH;
   if (gk > 0x7fffffffLL || gq > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned uq = static_cast<unsigned>(gq), uk = static_cast<unsigned>(gk);

@@ -226,7 +226,13 @@ int osattn_bwd_mod(const void* Q, const void* K, const void* V, const void* O, c
   a.O_in = O;
   a.LSE = const_cast<float*>(LSE);
   a.dRel = dRel;
-  for (int i = 0; i < 3; ++i) a.o_s[i] = st[3][i];
+  a.dK = dK;
+  a.dV = dV;
+  for (int i = 0; i < 3; ++i) {
+    a.o_s[i] = st[3][i];
+    a.dk_s[i] = st[6][i];
+    a.dv_s[i] = st[7][i];
+  }
   a.D = static_cast<float*>(workspace);
   a.rel_part = a.D + static_cast<size_t>(B) * H * Nq;
   BwdModMaps maps;

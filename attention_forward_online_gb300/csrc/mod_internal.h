@@ -47,6 +47,8 @@ struct ModArgs {
   float* D;         // workspace [B, H, Nq]
   float* rel_part;  // workspace [B, H, key tiles, 2 range + 1]
   void* dRel;       // [num, H] or null
+  void *dK, *dV;    // [B, Hkv, Nkv, d], and their element strides
+  long long dk_s[3], dv_s[3];
 };
 
 // Tensor maps of the backward pass; g: dO.
@@ -55,6 +57,5 @@ struct BwdModMaps {
 };
 
 int mod_score_mode(const ModArgs& a);
-
 
 }  // namespace osattn

@@ -185,6 +185,25 @@ def test_caps_of_every_size(cap):
     compare(*tensors(1, 2, 1, 150, 200, 64, FP, seed=13, std=cap if 0.1 < cap < 1e3 else 2.0), {}, cap=cap)
 
 
+# few key tiles: their queries are shared out to 8, 4, 2 CTAs; the last one's
+# windows leave some of them nothing
+SHARED = [
+    (1, 8, 1, 600, 900, dict(causal=True, q_offset=300, key_len=[777])),
+    (2, 4, 2, 500, 700, dict(key_len=[700, 130])),
+    (3, 4, 2, 400, 1000, dict(causal=True, q_offset=600)),
+    (1, 2, 1, 1500, 1500, dict(causal=True, window=4)),
+]
+
+
+@pytest.mark.parametrize("kind", ["plain", "cap", "slopes", "rel"])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (FP, 64)], ids=["bf16-128", "fp16-64"])
+@pytest.mark.parametrize("case", SHARED, ids=lambda c: "x".join(map(str, c[:5])))
+def test_key_tiles_shared_by_ctas(case, dtype, d, kind):
+    B, H, Hkv, Nq, Nkv, masks = case
+    masks = {k: i32(v) if isinstance(v, list) else v for k, v in masks.items()}
+    compare(*tensors(B, H, Hkv, Nq, Nkv, d, dtype, seed=21, bnhd=True), masks, **score_args(kind, H, dtype))
+
+
 @pytest.mark.parametrize("fill", [math.nan, math.inf, -math.inf, 3e38])
 @pytest.mark.parametrize("kind", ["plain", "cap", "slopes", "rel"])
 def test_masked_places_hold_anything(kind, fill):
