@@ -132,8 +132,8 @@ struct Params {
   int q_tiles;      // 128-row query tiles per (b, h)
   int num_tiles;    // this kernel's tiles per head
   int BH;           // this kernel's heads: B * H (dq) or B * Hkv (dkdv)
-  int split;        // dkdv: CTAs (of one cluster) that share a key tile's query tiles
-  uint16_t* dkv[2];        // dkdv with split > 1: dV, dK
+  int split_log2;   // dkdv: 2^this CTAs (a cluster) share a key tile's query tiles
+  uint16_t* dkv[2];        // then: dV, dK
   long long dkv_s[2][3];
   int group_heads;  // heads per last-tile-first (dq) or first-tile-first (dkdv) group of CTAs
   float scale;
@@ -453,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int bhk, kt;
-  const int part = blockIdx.x % p.split;
-  unit_of(p, blockIdx.x / p.split, bhk, kt);
+  const int part = blockIdx.x & ((1 << p.split_log2) - 1);
+  unit_of(p, blockIdx.x >> p.split_log2, bhk, kt);
   const int b = bhk / p.Hkv, hk = bhk % p.Hkv;
   const int k0 = kt * kT;
   // this thread's first query tile of the search below, on its way during the set-up
@@ -508,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // pairs; with a learned bias it is whole heads, as the sums by distance are
   // a head's.
   const int pairs = cnt * p.group;
-  const int first_it = static_cast<int>(static_cast<long long>(pairs) * part / p.split);
-  const int n_it = static_cast<int>(static_cast<long long>(pairs) * (part + 1) / p.split) - first_it;
+  const int first_it = static_cast<int>((static_cast<long long>(pairs) * part) >> p.split_log2);
+  const int n_it = static_cast<int>((static_cast<long long>(pairs) * (part + 1)) >> p.split_log2) - first_it;
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
 
@@ -731,14 +731,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = threadIdx.x; x < sum_entries(p.rel.range); x += 256) sums[x] = 0.f;
       if (n_it == 0) {  // nobody sees these keys: every head's sums are 0
         ok = elem_sync(bars, sync_phase, wc);
-        const int heads = p.group / p.split;
+        const int heads = p.group >> p.split_log2;
         for (int g = part * heads; ok && g < (part + 1) * heads; ++g) ok = flush_sums(hk * p.group + g);
       }
     }
-    for (int it = 0; ok && it < n_it; ++it) {
+    int h = 0, qt = 0;
+    if (n_it > 0) {
+      h = hk * p.group + first_it / cnt;
+      qt = it_lo + first_it % cnt;
+    }
+    for (int it = 0; ok && it < n_it; ++it, ++qt) {
       const int s = it % C::kStages;
-      const int h = hk * p.group + (first_it + it) / cnt;
-      const int qt = it_lo + (first_it + it) % cnt;
+      if (qt == bars->it_hi) {
+        qt = it_lo;
+        ++h;
+      }
       const int p0 = qt * kT + p.q_offset;  // position of the tile's first query
       if (h != h_of) {  // uniform over the elementwise warps
         if constexpr (mode_slopes(MODE)) slope2 = p.slopes[h] * kModLog2e;
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) tc_fence_after_sync();
       has_acc = ok;
     }
-    if (ok && p.split > 1) {
+    if (ok && p.split_log2 > 0) {
       // fp32 over the tiles, whose last readers are done, for the join below
       const int w = warp >> 2;
       float4* out = reinterpret_cast<float4*>(smem + w * kT * HD * 4) + row * (HD / 4);
@@ -948,17 +955,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncwarp();
-  if (p.split > 1) {
+  if (p.split_log2 > 0) {
     // The sums of the cluster's CTAs, added in rank order; each CTA finishes
     // its share of the rows.  (A CTA whose waits gave up comes here too.)
     cluster_sync();
-    const int rows = kT / p.split;
+    const int rows = kT >> p.split_log2;
     for (int x = threadIdx.x; x < 2 * rows * (HD / 8); x += kThreads) {
       const int w = x / (rows * (HD / 8)), c = x % (HD / 8);
       const int row = part * rows + x / (HD / 8) % rows;
       const uint32_t at = smem_u32(smem) + (w * kT + row) * HD * 4;
       float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int r = 0; r < p.split; ++r) {
+      for (int r = 0; r < (1 << p.split_log2); ++r) {
         float v[8];
         cluster_load4(at + ((2 * c) ^ (row & 7)) * 16, r, v);
         cluster_load4(at + ((2 * c + 1) ^ (row & 7)) * 16, r, v + 4);
@@ -1364,15 +1371,15 @@ __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restric
 }
 
 // CTAs that share a key tile's (head, query tile) pairs, of which it has at
-// most `pairs`: a power of two that divides `of`, leaves a CTA two pairs, and
-// makes the kernel shortest if a CTA takes 1 / split of a tile's time and a
-// quarter of it besides, and the SMs take the CTAs in rounds.
+// most `pairs`, as a power of two: one that divides `of`, leaves a CTA two
+// pairs, and makes the kernel shortest if a CTA takes 1 / s of a tile's time
+// and a quarter of it besides, and the SMs take the CTAs in rounds.
 inline int dkdv_split(long long units, int num_sms, long long pairs, int of) {
-  int best = 1;
+  int best = 0;
   double cost = 0.0;
-  for (int s = 1; s == 1 || (s <= 8 && of % s == 0 && 2 * s <= pairs); s *= 2) {
-    const double c = static_cast<double>((units * s + num_sms - 1) / num_sms) * (1.0 / s + 0.25);
-    if (s == 1 || c < cost) best = s, cost = c;
+  for (int n = 0; n == 0 || (n <= 3 && of % (1 << n) == 0 && (2 << n) <= pairs); ++n) {
+    const double c = static_cast<double>(((units << n) + num_sms - 1) / num_sms) * (1.0 / (1 << n) + 0.25);
+    if (n == 0 || c < cost) best = n, cost = c;
   }
   return best;
 }
@@ -1417,10 +1424,10 @@ cudaError_t launch_mode(const ModArgs& a, const Params& pq, const Params& pk, un
   cfg.stream = a.stream;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = static_cast<unsigned>(pk.split);
+  cluster.val.clusterDim.x = 1u << pk.split_log2;
   cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   cfg.attrs = &cluster;
-  cfg.numAttrs = pk.split > 1 ? 1 : 0;
+  cfg.numAttrs = pk.split_log2 > 0 ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, dkdv_kernel<HD, kF16, kDkdvMode>, m.q, m.k, m.v, m.g, m.dk, m.dv, pk);
   if (e != cudaSuccess || !mode_rel(MODE)) return e;
   rel_reduce_kernel<kF16><<<a.H, 1024, 0, a.stream>>>(a.rel_part, static_cast<uint16_t*>(a.dRel), a.rel,
@@ -1465,7 +1472,7 @@ cudaError_t launch(const ModArgs& a, const BwdModMaps& m) {
   pq.BH = a.B * a.H;
   pq.num_tiles = p.q_tiles;
   pq.group_heads = group(a.Nkv, pq.BH);
-  pk.split = dkdv_split(static_cast<long long>(pk.num_tiles) * pk.BH, a.num_sms,
+  pk.split_log2 = dkdv_split(static_cast<long long>(pk.num_tiles) * pk.BH, a.num_sms,
                         static_cast<long long>(p.q_tiles) * p.group, a.rel.table ? p.group : 8);
   pk.dkv[0] = static_cast<uint16_t*>(a.dV);
   pk.dkv[1] = static_cast<uint16_t*>(a.dK);
@@ -1473,7 +1480,7 @@ cudaError_t launch(const ModArgs& a, const BwdModMaps& m) {
     pk.dkv_s[0][i] = a.dv_s[i];
     pk.dkv_s[1][i] = a.dk_s[i];
   }
-  const long long gk = static_cast<long long>(pk.num_tiles) * pk.BH * pk.split;
+  const long long gk = static_cast<long long>(pk.num_tiles) * pk.BH << pk.split_log2;
   const long long gq = static_cast<long long>(pq.num_tiles) * pq.BH;
   if (gk > 0x7fffffffLL || gq > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned uq = static_cast<unsigned>(gq), uk = static_cast<unsigned>(gk);
