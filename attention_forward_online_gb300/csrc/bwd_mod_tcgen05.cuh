@@ -264,14 +264,16 @@ __device__ __forceinline__ void p_part(uint32_t s_addr, int c0, const Params& p,
   const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
   auto half = [&](Chunk& sv, float top, int h) {
     uint32_t pk[16];
-    bool small = true;
+    bool small = true, tiny = false;
     if constexpr (kCap) {
       if constexpr (kMask) {  // masked scores, which may hold anything, take no part in the choice
 #pragma unroll
         for (int e = 0; e < 32; ++e) sv[e] = vis(c0 + 32 * h + e) ? sv[e] : 0u;
         top = chunk_max(sv);
       }
-      small = __all_sync(0xffffffffu, top <= p.cap.s_max && chunk_min(sv) >= -p.cap.s_max);
+      const float size = fmaxf(top, -chunk_min(sv));
+      small = __all_sync(0xffffffffu, size <= p.cap.s_max);
+      tiny = __all_sync(0xffffffffu, size <= 0.5f * p.cap.s_max);
     }
     auto finish = [&](int x, uint64_t a2, uint64_t f2) {  // entries x, x + 1 of the half: exponent, factor
       const int col = c0 + 32 * h + x;
@@ -288,7 +290,7 @@ __device__ __forceinline__ void p_part(uint32_t s_addr, int c0, const Params& p,
       pr[32 * h + x] = e0;
       pr[32 * h + x + 1] = e1;
     };
-    if (!kCap || small) {
+    auto direct = [&](auto degree) {
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         const float4 L = nl2of4(c0 + 32 * h + 4 * g);
@@ -299,9 +301,13 @@ __device__ __forceinline__ void p_part(uint32_t s_addr, int c0, const Params& p,
           if constexpr (kCap) {
             const CapArgs& a = p.cap;
             const uint64_t w = f2_mul(s2, s2);
-            const uint64_t q = f2_fma(f2_fma(f2_fma(f2_pack(a.k[3], a.k[3]), w, f2_pack(a.k[2], a.k[2])), w,
-                                             f2_pack(a.k[1], a.k[1])),
-                                      w, f2_pack(a.k[0], a.k[0]));
+            uint64_t q;
+            if constexpr (decltype(degree)::value == 2)
+              q = f2_fma(f2_fma(f2_pack(a.q[2], a.q[2]), w, f2_pack(a.q[1], a.q[1])), w, f2_pack(a.q[0], a.q[0]));
+            else
+              q = f2_fma(f2_fma(f2_fma(f2_pack(a.k[3], a.k[3]), w, f2_pack(a.k[2], a.k[2])), w,
+                                f2_pack(a.k[1], a.k[1])),
+                         w, f2_pack(a.k[0], a.k[0]));
             const uint64_t y = f2_mul(q, s2);  // cap2 tanh
             finish(x, f2_add(y, n2), f2_fma(f2_mul(y, y), f2_pack(-a.inv2, -a.inv2), f2_pack(1.f, 1.f)));
           } else {
@@ -309,6 +315,11 @@ __device__ __forceinline__ void p_part(uint32_t s_addr, int c0, const Params& p,
           }
         }
       }
+    };
+    if (kCap && tiny) {
+      direct(std::integral_constant<int, 2>{});
+    } else if (!kCap || small) {
+      direct(std::integral_constant<int, 3>{});
     } else {
 #pragma unroll
       for (int g = 0; g < 8; ++g) {

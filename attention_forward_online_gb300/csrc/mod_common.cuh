@@ -93,7 +93,7 @@ __device__ __forceinline__ float cap_r(float s, float c1) { return rcp_approx(1.
 // 3: coefficients fitted here for the least relative error on that range
 // (2^-23.3, reweighted least squares on Chebyshev points).  k[n] carries
 // cap2 (scale / cap)^(2 n + 1), so that the polynomial is in the raw score:
-// cap2 tanh = s (k0 + s^2 (k1 + ...)).  s_max = 0.4 cap / |scale|, but at most
+// cap2 tanh = s (k0 + s^2 (k1 + ...)).  Degree 2 (2^-23.2) does up to 0.2.  s_max = 0.4 cap / |scale|, but at most
 // 2^16 where |scale| / cap is below 2^-19 (k[3] leaves fp32's range there, and
 // is not needed up to 2^16), and -1 where it is above 2^12: then only the
 // other form is used.  c1 is kept finite (inf times a score of 0 is NaN).
@@ -101,6 +101,7 @@ struct CapArgs {
   float c1, cap2, s_max;  // c1 = 2 scale log2(e) / cap
   float inv2;             // 1 / cap2^2
   float k[4];
+  float q[3];             // the same of degree 2, for |y / cap| <= 0.2, that is up to s_max / 2
 };
 inline CapArgs make_cap(float scale, float softcap) {
   CapArgs c{};
@@ -115,8 +116,12 @@ inline CapArgs make_cap(float scale, float softcap) {
   const double size = a < 0 ? -a : a, low = 1.0 / 524288;
   const bool ok = size <= 4096.0;
   c.s_max = !ok ? -1.f : (size < low ? 65536.f : static_cast<float>(0.4 / size));
+  const double t2[3] = {0.9999998948, -0.3332859090, 0.1301540755};
   double pw = a;
-  for (int n = 0; n < 4; ++n, pw *= a * a) c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;
+  for (int n = 0; n < 4; ++n, pw *= a * a) {
+    c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;
+    if (n < 3) c.q[n] = ok ? static_cast<float>(cap2 * t2[n] * pw) : 0.f;
+  }
   return c;
 }
 // min(x, 30); NaN stays NaN

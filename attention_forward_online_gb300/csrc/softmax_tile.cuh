@@ -155,7 +155,9 @@ struct TileScore {
   // publish(alpha_bits) as soon as it is known, and updates l.
   // gap(ch)(e): the distance of key e of chunk ch, for both_sides.
   // kMasked: some rows of the warp may not see all of the tile.
-  template <bool kMasked, typename BitsOf, typename Gap, typename Publish>
+  // kShort: with the shorter polynomial for small capped scores (capped prompt
+  // of 8192: 467 us against 487; its code costs kernels of few tiles 2 us).
+  template <bool kMasked, bool kShort, typename BitsOf, typename Gap, typename Publish>
   __device__ __forceinline__ void tile(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
                                        float& m, float& l, Publish&& publish) const {
     Row v;
@@ -183,10 +185,13 @@ struct TileScore {
     }
     const float best_raw = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     bool direct = true;  // uniform over the warp
-    if constexpr (MODE == kModCap)
-      direct = __all_sync(0xffffffffu, best_raw <= cap->s_max &&
-                                           fminf(fminf(chunk_min(v[0]), chunk_min(v[1])),
-                                                 fminf(chunk_min(v[2]), chunk_min(v[3]))) >= -cap->s_max);
+    [[maybe_unused]] bool tiny = false;  // the shorter polynomial will do
+    if constexpr (MODE == kModCap) {
+      const float least = fminf(fminf(chunk_min(v[0]), chunk_min(v[1])), fminf(chunk_min(v[2]), chunk_min(v[3])));
+      const float size = fmaxf(best_raw, -least);
+      direct = __all_sync(0xffffffffu, size <= cap->s_max);
+      if constexpr (kShort) tiny = __all_sync(0xffffffffu, size <= 0.5f * cap->s_max);
+    }
     if constexpr (MODE == kModSlopes) direct = !both_sides;
     if constexpr (MODE == kModCapSlopes) direct = false;
     if constexpr (mode_rel(MODE)) direct = strip == nullptr;
@@ -197,7 +202,8 @@ struct TileScore {
       // a row with no key so far has m_new = -inf and every x = -inf: against
       // 0 each p is exactly 0
       const float n = off - (m_new == -INFINITY ? 0.f : m_new);
-      sum = exps<kMasked, true>(s_addr, v, k, bits_of, n);
+      if (kShort && MODE == kModCap && tiny) sum = exps<kMasked, true, 2>(s_addr, v, k, bits_of, n);
+      else sum = exps<kMasked, true, 3>(s_addr, v, k, bits_of, n);
     } else if constexpr (MODE != kModPlain) {
       float best = -INFINITY;
       const bool bound = mode_rel(MODE) && strip_close;
@@ -211,7 +217,7 @@ struct TileScore {
       }
       m_new = next_max(m, best);
       publish(alpha_bits(m, m_new));
-      sum = exps<kMasked, false>(s_addr, v, k, bits_of, m_new == -INFINITY ? 0.f : -m_new);
+      sum = exps<kMasked, false, 0>(s_addr, v, k, bits_of, m_new == -INFINITY ? 0.f : -m_new);
     }
     l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
     m = m_new;
@@ -321,8 +327,14 @@ struct TileScore {
   }
 
   // x + n of two raw scores (direct tiles); n2: n twice, with off in it.
+  template <int kDegree>
   __device__ __forceinline__ uint64_t direct_pair(uint64_t s, uint64_t n2) const {
-    if constexpr (MODE == kModCap) {
+    if constexpr (MODE == kModCap && kDegree == 2) {
+      const uint64_t u = f2_mul(s, s);
+      const uint64_t k0 = f2_pack(cap->q[0], cap->q[0]), k1 = f2_pack(cap->q[1], cap->q[1]),
+                     k2 = f2_pack(cap->q[2], cap->q[2]);
+      return f2_fma(f2_fma(f2_fma(k2, u, k1), u, k0), s, n2);
+    } else if constexpr (MODE == kModCap) {
       const uint64_t u = f2_mul(s, s);
       const uint64_t k0 = f2_pack(cap->k[0], cap->k[0]), k1 = f2_pack(cap->k[1], cap->k[1]),
                      k2 = f2_pack(cap->k[2], cap->k[2]), k3 = f2_pack(cap->k[3], cap->k[3]);
@@ -335,7 +347,7 @@ struct TileScore {
   // P in 16 bits over the first 64 columns of the row's scores, and the sum:
   // 2^(x + n) from raw scores (kDirect, n with off), or 2^(v + n).  kMasked:
   // chunks that no row of the warp sees are zeros.
-  template <bool kMasked, bool kDirect, typename BitsOf>
+  template <bool kMasked, bool kDirect, int kDegree, typename BitsOf>
   __device__ __forceinline__ float exps(uint32_t s_addr, const Row& v, const TileMask& k, BitsOf&& bits_of,
                                         float n) const {
     uint64_t rs_a = 0, rs_b = 0;  // packed partial sums (bit pattern 0 = 0.0f)
@@ -355,7 +367,7 @@ struct TileScore {
         for (int e = 0; e < 16; ++e) {
           const uint64_t s = pair_of(v[ch], 2 * e);
           float x0, x1;
-          f2_unpack(kDirect ? direct_pair(s, n2) : f2_add(s, n2), x0, x1);
+          f2_unpack(kDirect ? direct_pair<kDegree>(s, n2) : f2_add(s, n2), x0, x1);
           if constexpr (kCut) {
             x0 = (bits & (1u << (2 * e))) ? x0 : -INFINITY;
             x1 = (bits & (2u << (2 * e))) ? x1 : -INFINITY;

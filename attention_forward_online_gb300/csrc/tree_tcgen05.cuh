@@ -348,7 +348,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
         };
         ts.tile_rolled(s_addr, mk, bits_of, gap, m, l, publish);
       } else {
-        ts.template tile<false>(s_addr, mk, [](int) { return 0xffffffffu; }, ts.by_place(), m, l, publish);
+        ts.template tile<false, false>(s_addr, mk, [](int) { return 0xffffffffu; }, ts.by_place(), m, l, publish);
       }
       tmem_st_wait();
       tc_fence_before_sync();
