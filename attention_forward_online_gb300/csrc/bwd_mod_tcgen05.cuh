@@ -48,7 +48,7 @@ namespace osattn {
 namespace bwdmod {
 
 constexpr int kT = 128;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kProdWarp = 8, kMmaWarp = 9;
 constexpr uint32_t kCols = 512;
 
@@ -146,6 +146,15 @@ struct Params {
   unsigned int* status;
   uint64_t wait_limit_ns;
 };
+
+template <uint32_t N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <bool kF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -524,181 +533,186 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, p.status, p.status + 1, p.wait_limit_ns};
 
-  if (warp == kProdWarp) {
-    int issued = 0;
-    if (n_it > 0) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->fixed_full, 2 * C::kTileBytes);
-#pragma unroll
-        for (int cb = 0; cb < HD / 64; ++cb) {
-          tma_load_4d(sK + cb * kT * 128, &tmK, &bars->fixed_full, cb * 64, k0, hk, b);
-          tma_load_4d(sV + cb * kT * 128, &tmV, &bars->fixed_full, cb * 64, k0, hk, b);
-        }
-      }
-      // Per-query values of a tile, loaded a tile ahead of their use: the loads
-      // depend on nothing, and none waits for a stage.
-      struct RowValues {
-        float lse[kT / 32], D[kT / 32];
-        int2 see[kT / 32];
-        PlanTile tile;
-      };
-      auto load_rows = [&](int it) {
-        RowValues v;
-        const int h = hk * p.group + (first_it + it) / cnt, qt = it_lo + (first_it + it) % cnt;
-        const long long rowbase = (static_cast<long long>(b) * p.H + h) * p.Nq;
-#pragma unroll
-        for (int r = 0; r < kT / 32; ++r) {
-          const int q = qt * kT + lane + 32 * r;
-          v.lse[r] = q < p.Nq ? p.LSE[rowbase + q] : -INFINITY;
-          v.D[r] = q < p.Nq ? p.D[rowbase + q] : 0.f;
-          // (rows past the last see what it sees, with P = 2^-inf: lo and hi keep their order)
-          v.see[r] = plan_row(p.plan, b, p.Nq, min(q, p.Nq - 1), p.Nkv);
-        }
-        v.tile = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
-        return v;
-      };
-      RowValues next = load_rows(0);
-      [[maybe_unused]] float slope = 0.f;
-      [[maybe_unused]] bool linear = false;
-      for (int it = 0; it < n_it; ++it) {
-        const int s = it % C::kStages;
-        const int head = (first_it + it) / cnt, h = hk * p.group + head;
-        const int qt = it_lo + (first_it + it) % cnt, q0 = qt * kT;
-        const RowValues now = next;
-        if (it + 1 < n_it) next = load_rows(it + 1);
-        [[maybe_unused]] float lin = 0.f;  // what a linear slope leaves: lin (k0 - position)
-        [[maybe_unused]] int side = 0;
-        if constexpr (MODE == kModSlopes) {
-          if (it == 0 || qt == it_lo) {
-            slope = __ldg(p.slopes + h);
-            linear = slope_linear(slope, p.scale);
-          }
-          if (linear) side = slope_side(k0, q0 + p.q_offset, now.tile.left);
-          lin = slope * kModLog2e * static_cast<float>(side);
-        }
-        float l2[kT / 32], dd[kT / 32];
-#pragma unroll
-        for (int r = 0; r < kT / 32; ++r) {
-          const int q = q0 + lane + 32 * r;
-          const bool sees = q < p.Nq && now.see[r].x < now.see[r].y && now.lse[r] != -INFINITY;
-          l2[r] = sees ? -(now.lse[r] * kModLog2e) : -INFINITY;
-          if constexpr (MODE == kModSlopes)
-            if (sees) l2[r] = fmaf(lin, static_cast<float>(k0 - (q + p.q_offset)), l2[r]);
-          dd[r] = sees ? -now.D[r] : 0.f;
-        }
-        uint8_t* st = ring + s * C::kStageBytes;
-        bool ok = true;
-        if (it >= C::kStages)
-          ok = mbar_wait(&bars->empty2[s], static_cast<uint32_t>(it / C::kStages - 1) & 1u, wc, kSiteLoad);
-        if (!__all_sync(0xffffffffu, ok)) break;
+  // 256 x 216 + 128 x 72 = 384 x 168 registers
+  if (warp >= kProdWarp) {
+    regs_dec<72>();
+    if (warp == kProdWarp) {
+      int issued = 0;
+      if (n_it > 0) {
         if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->full[s], 2 * C::kTileBytes);
+          mbar_arrive_expect_tx(&bars->fixed_full, 2 * C::kTileBytes);
 #pragma unroll
-          for (int cb = 0; cb < HD / 64; ++cb)
-            tma_load_4d(st + C::kTileBytes + cb * kT * 128, &tmdO, &bars->full[s], cb * 64, q0, h, b);
+          for (int cb = 0; cb < HD / 64; ++cb) {
+            tma_load_4d(sK + cb * kT * 128, &tmK, &bars->fixed_full, cb * 64, k0, hk, b);
+            tma_load_4d(sV + cb * kT * 128, &tmV, &bars->fixed_full, cb * 64, k0, hk, b);
+          }
         }
-        issued = it + 1;
-        if (it >= C::kStages)
-          ok = mbar_wait(&bars->empty[s], static_cast<uint32_t>(it / C::kStages - 1) & 1u, wc, kSiteLoad);
-        if (!__all_sync(0xffffffffu, ok)) {
-          // Q_i will not be loaded: count its bytes and arrival as done
+        // Per-query values of a tile, loaded a tile ahead of their use: the loads
+        // depend on nothing, and none waits for a stage.
+        struct RowValues {
+          float lse[kT / 32], D[kT / 32];
+          int2 see[kT / 32];
+          PlanTile tile;
+        };
+        auto load_rows = [&](int it) {
+          RowValues v;
+          const int h = hk * p.group + (first_it + it) / cnt, qt = it_lo + (first_it + it) % cnt;
+          const long long rowbase = (static_cast<long long>(b) * p.H + h) * p.Nq;
+#pragma unroll
+          for (int r = 0; r < kT / 32; ++r) {
+            const int q = qt * kT + lane + 32 * r;
+            v.lse[r] = q < p.Nq ? p.LSE[rowbase + q] : -INFINITY;
+            v.D[r] = q < p.Nq ? p.D[rowbase + q] : 0.f;
+            // (rows past the last see what it sees, with P = 2^-inf: lo and hi keep their order)
+            v.see[r] = plan_row(p.plan, b, p.Nq, min(q, p.Nq - 1), p.Nkv);
+          }
+          v.tile = plan_tile(p.plan, b, p.q_tiles, qt, p.Nkv);
+          return v;
+        };
+        RowValues next = load_rows(0);
+        [[maybe_unused]] float slope = 0.f;
+        [[maybe_unused]] bool linear = false;
+        for (int it = 0; it < n_it; ++it) {
+          const int s = it % C::kStages;
+          const int head = (first_it + it) / cnt, h = hk * p.group + head;
+          const int qt = it_lo + (first_it + it) % cnt, q0 = qt * kT;
+          const RowValues now = next;
+          if (it + 1 < n_it) next = load_rows(it + 1);
+          [[maybe_unused]] float lin = 0.f;  // what a linear slope leaves: lin (k0 - position)
+          [[maybe_unused]] int side = 0;
+          if constexpr (MODE == kModSlopes) {
+            if (it == 0 || qt == it_lo) {
+              slope = __ldg(p.slopes + h);
+              linear = slope_linear(slope, p.scale);
+            }
+            if (linear) side = slope_side(k0, q0 + p.q_offset, now.tile.left);
+            lin = slope * kModLog2e * static_cast<float>(side);
+          }
+          float l2[kT / 32], dd[kT / 32];
+#pragma unroll
+          for (int r = 0; r < kT / 32; ++r) {
+            const int q = q0 + lane + 32 * r;
+            const bool sees = q < p.Nq && now.see[r].x < now.see[r].y && now.lse[r] != -INFINITY;
+            l2[r] = sees ? -(now.lse[r] * kModLog2e) : -INFINITY;
+            if constexpr (MODE == kModSlopes)
+              if (sees) l2[r] = fmaf(lin, static_cast<float>(k0 - (q + p.q_offset)), l2[r]);
+            dd[r] = sees ? -now.D[r] : 0.f;
+          }
+          uint8_t* st = ring + s * C::kStageBytes;
+          bool ok = true;
+          if (it >= C::kStages)
+            ok = mbar_wait(&bars->empty2[s], static_cast<uint32_t>(it / C::kStages - 1) & 1u, wc, kSiteLoad);
+          if (!__all_sync(0xffffffffu, ok)) break;
           if (lane == 0) {
-            mbar_complete_tx(&bars->full[s], C::kTileBytes);
-            mbar_arrive(&bars->full[s]);
-          }
-          break;
-        }
+            mbar_arrive_expect_tx(&bars->full[s], 2 * C::kTileBytes);
 #pragma unroll
-        for (int r = 0; r < kT / 32; ++r) {
-          const int x = s * kT + lane + 32 * r;
-          lse2[x] = l2[r];
-          dsum[x] = dd[r];
-          slo[x] = now.see[r].x;
-          shi[x] = now.see[r].y;
-        }
-        if constexpr (MODE == kModSlopes) {
-          // A head's operand goes to place (head mod 4): the tiles of the head
-          // that had it are at least 4 tiles, so at least a ring, back.
-          if (it == 0 || qt == it_lo) {
-            if (lane < 8)
-              slope_fill_q<kF16>(reinterpret_cast<uint8_t*>(bias_all) + kSlopeRowsBytes +
-                                     head % 4 * kSlopeQBytes,
-                                 lane, slope, p.scale);
-            fence_proxy_async();
+            for (int cb = 0; cb < HD / 64; ++cb)
+              tma_load_4d(st + C::kTileBytes + cb * kT * 128, &tmdO, &bars->full[s], cb * 64, q0, h, b);
           }
-          if (lane == 0) bars->side[s] = side;
+          issued = it + 1;
+          if (it >= C::kStages)
+            ok = mbar_wait(&bars->empty[s], static_cast<uint32_t>(it / C::kStages - 1) & 1u, wc, kSiteLoad);
+          if (!__all_sync(0xffffffffu, ok)) {
+            // Q_i will not be loaded: count its bytes and arrival as done
+            if (lane == 0) {
+              mbar_complete_tx(&bars->full[s], C::kTileBytes);
+              mbar_arrive(&bars->full[s]);
+            }
+            break;
+          }
+#pragma unroll
+          for (int r = 0; r < kT / 32; ++r) {
+            const int x = s * kT + lane + 32 * r;
+            lse2[x] = l2[r];
+            dsum[x] = dd[r];
+            slo[x] = now.see[r].x;
+            shi[x] = now.see[r].y;
+          }
+          if constexpr (MODE == kModSlopes) {
+            // A head's operand goes to place (head mod 4): the tiles of the head
+            // that had it are at least 4 tiles, so at least a ring, back.
+            if (it == 0 || qt == it_lo) {
+              if (lane < 8)
+                slope_fill_q<kF16>(reinterpret_cast<uint8_t*>(bias_all) + kSlopeRowsBytes +
+                                       head % 4 * kSlopeQBytes,
+                                   lane, slope, p.scale);
+              fence_proxy_async();
+            }
+            if (lane == 0) bars->side[s] = side;
+          }
+          if (lane == 0)
+            bars->seen[s] = (now.tile.lo_max <= k0 && now.tile.hi_min >= k0 + kT ? 1 : 0) | (now.tile.hi_min == 0 ? 2 : 0);
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int cb = 0; cb < HD / 64; ++cb)
+              tma_load_4d(st + cb * kT * 128, &tmQ, &bars->full[s], cb * 64, q0, h, b);
+            mbar_arrive(&bars->full[s]);  // releases the per-query values above
+          }
         }
-        if (lane == 0)
-          bars->seen[s] = (now.tile.lo_max <= k0 && now.tile.hi_min >= k0 + kT ? 1 : 0) | (now.tile.hi_min == 0 ? 2 : 0);
-        __syncwarp();
         if (lane == 0) {
-#pragma unroll
-          for (int cb = 0; cb < HD / 64; ++cb)
-            tma_load_4d(st + cb * kT * 128, &tmQ, &bars->full[s], cb * 64, q0, h, b);
-          mbar_arrive(&bars->full[s]);  // releases the per-query values above
+          drain(&bars->fixed_full, 0, wc.limit_ns);
+          for (int it = (issued > C::kStages ? issued - C::kStages : 0); it < issued; ++it)
+            drain(&bars->full[it % C::kStages], static_cast<uint32_t>(it / C::kStages) & 1u, wc.limit_ns);
         }
       }
-      if (lane == 0) {
-        drain(&bars->fixed_full, 0, wc.limit_ns);
-        for (int it = (issued > C::kStages ? issued - C::kStages : 0); it < issued; ++it)
-          drain(&bars->full[it % C::kStages], static_cast<uint32_t>(it / C::kStages) & 1u, wc.limit_ns);
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    // Order: S^T_0, dP^T_0; then per query tile dV += P^T dO, the next S^T,
-    // dK += dS^T Q, the next dP^T.  The tensor core runs them in issue order.
-    if (n_it > 0) {
-      const uint64_t kA = sdesc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t vA = sdesc_sw128(smem_u32(sV), 16, 1024);
-      bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);
-      if (ok) ok = warp_wait(&bars->full[0], 0, wc, kSiteMma);
-      if (ok) {
-        tc_fence_after_sync();
-        const uint32_t sq = smem_u32(ring), sdo = sq + C::kTileBytes;
-        mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(sq, 16, 1024));
-        if constexpr (MODE == kModSlopes)
-          add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + first_it / cnt % 4 * kSlopeQBytes,
-                            smem_u32(bias_all), bars->side[0]);
-        mma_commit<true>(&bars->s_full[0]);
-        mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(sdo, 16, 1024));
-        mma_commit<true>(&bars->dp_full);
-      }
-      for (int it = 0; ok && it < n_it; ++it) {
-        const int s = it % C::kStages, s1 = (it + 1) % C::kStages;
-        const uint32_t sq = smem_u32(ring + s * C::kStageBytes), sdo = sq + C::kTileBytes;
-        const uint32_t nq = smem_u32(ring + s1 * C::kStageBytes), ndo = nq + C::kTileBytes;
-        const bool more = it + 1 < n_it;
-        ok = warp_wait(&bars->p_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
-        if (!ok) break;
-        tc_fence_after_sync();
-        mma_groups<HD, kF16>(tmem + C::kColAcc0, tmem, sdesc_sw128(sdo, kT * 128, 1024), it > 0);
-        mma_commit<true>(&bars->empty2[s]);
-        if (more) {
-          ok = warp_wait(&bars->full[s1], static_cast<uint32_t>((it + 1) / C::kStages) & 1u, wc, kSiteMma);
-          if (!ok) break;
+    } else if (warp == kMmaWarp) {
+      // Order: S^T_0, dP^T_0; then per query tile dV += P^T dO, the next S^T,
+      // dK += dS^T Q, the next dP^T.  The tensor core runs them in issue order.
+      if (n_it > 0) {
+        const uint64_t kA = sdesc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t vA = sdesc_sw128(smem_u32(sV), 16, 1024);
+        bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);
+        if (ok) ok = warp_wait(&bars->full[0], 0, wc, kSiteMma);
+        if (ok) {
           tc_fence_after_sync();
-          mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(nq, 16, 1024));
+          const uint32_t sq = smem_u32(ring), sdo = sq + C::kTileBytes;
+          mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(sq, 16, 1024));
           if constexpr (MODE == kModSlopes)
-            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + (first_it + it + 1) / cnt % 4 * kSlopeQBytes,
-                              smem_u32(bias_all), bars->side[s1]);
+            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + first_it / cnt % 4 * kSlopeQBytes,
+                              smem_u32(bias_all), bars->side[0]);
           mma_commit<true>(&bars->s_full[0]);
-        }
-        ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
-        if (!ok) break;
-        tc_fence_after_sync();
-        mma_groups<HD, kF16>(tmem + C::kColAcc1, tmem + 128, sdesc_sw128(sq, kT * 128, 1024), it > 0);
-        mma_commit<true>(&bars->empty[s]);
-        if (more) {
-          mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(ndo, 16, 1024));
+          mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(sdo, 16, 1024));
           mma_commit<true>(&bars->dp_full);
         }
+        for (int it = 0; ok && it < n_it; ++it) {
+          const int s = it % C::kStages, s1 = (it + 1) % C::kStages;
+          const uint32_t sq = smem_u32(ring + s * C::kStageBytes), sdo = sq + C::kTileBytes;
+          const uint32_t nq = smem_u32(ring + s1 * C::kStageBytes), ndo = nq + C::kTileBytes;
+          const bool more = it + 1 < n_it;
+          ok = warp_wait(&bars->p_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
+          if (!ok) break;
+          tc_fence_after_sync();
+          mma_groups<HD, kF16>(tmem + C::kColAcc0, tmem, sdesc_sw128(sdo, kT * 128, 1024), it > 0);
+          mma_commit<true>(&bars->empty2[s]);
+          if (more) {
+            ok = warp_wait(&bars->full[s1], static_cast<uint32_t>((it + 1) / C::kStages) & 1u, wc, kSiteMma);
+            if (!ok) break;
+            tc_fence_after_sync();
+            mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(nq, 16, 1024));
+            if constexpr (MODE == kModSlopes)
+              add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + (first_it + it + 1) / cnt % 4 * kSlopeQBytes,
+                                smem_u32(bias_all), bars->side[s1]);
+            mma_commit<true>(&bars->s_full[0]);
+          }
+          ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
+          if (!ok) break;
+          tc_fence_after_sync();
+          mma_groups<HD, kF16>(tmem + C::kColAcc1, tmem + 128, sdesc_sw128(sq, kT * 128, 1024), it > 0);
+          mma_commit<true>(&bars->empty[s]);
+          if (more) {
+            mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(ndo, 16, 1024));
+            mma_commit<true>(&bars->dp_full);
+          }
+        }
+        if (ok) mma_commit<true>(&bars->acc_full);
+        mma_commit<true>(&bars->mma_drain);
+        drain(&bars->mma_drain, 0, wc.limit_ns);
+        __syncwarp();
       }
-      if (ok) mma_commit<true>(&bars->acc_full);
-      mma_commit<true>(&bars->mma_drain);
-      drain(&bars->mma_drain, 0, wc.limit_ns);
-      __syncwarp();
     }
   } else {
+    regs_inc<216>();
     const int c0 = 64 * (warp >> 2);         // this warpgroup's columns (queries)
     const int row = (warp & 3) * 32 + lane;  // key row of the tile = tensor-memory lane
     const int kabs = k0 + row;
@@ -1073,88 +1087,93 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kt0 = pt.lo / kT;
   const int n_kt = pt.lo < pt.hi ? (pt.hi + kT - 1) / kT - kt0 : 0;
 
-  if (warp == kProdWarp) {
-    if (lane == 0 && n_kt > 0) {
-      mbar_arrive_expect_tx(&bars->fixed_full, 2 * C::kTileBytes);
-#pragma unroll
-      for (int cb = 0; cb < HD / 64; ++cb) {
-        tma_load_4d(sQ + cb * kT * 128, &tmQ, &bars->fixed_full, cb * 64, q0, h, b);
-        tma_load_4d(sdO + cb * kT * 128, &tmdO, &bars->fixed_full, cb * 64, q0, h, b);
-      }
-      int issued = 0;
-      for (int j = 0; j < n_kt; ++j) {
-        const int a = j % C::kKSlots, v = j % C::kVSlots;
-        if (j >= C::kKSlots &&
-            !mbar_wait(&bars->empty[a], static_cast<uint32_t>(j / C::kKSlots - 1) & 1u, wc, kSiteLoad))
-          break;
-        if (j >= C::kVSlots &&
-            !mbar_wait(&bars->empty2[v], static_cast<uint32_t>(j / C::kVSlots - 1) & 1u, wc, kSiteLoad))
-          break;
-        mbar_arrive_expect_tx(&bars->full[a], 2 * C::kTileBytes);
+  // 256 x 216 + 128 x 72 = 384 x 168 registers
+  if (warp >= kProdWarp) {
+    regs_dec<72>();
+    if (warp == kProdWarp) {
+      if (lane == 0 && n_kt > 0) {
+        mbar_arrive_expect_tx(&bars->fixed_full, 2 * C::kTileBytes);
 #pragma unroll
         for (int cb = 0; cb < HD / 64; ++cb) {
-          tma_load_4d(kring + a * C::kTileBytes + cb * kT * 128, &tmK, &bars->full[a], cb * 64,
-                      (kt0 + j) * kT, hk, b);
-          tma_load_4d(vring + v * C::kTileBytes + cb * kT * 128, &tmV, &bars->full[a], cb * 64,
-                      (kt0 + j) * kT, hk, b);
+          tma_load_4d(sQ + cb * kT * 128, &tmQ, &bars->fixed_full, cb * 64, q0, h, b);
+          tma_load_4d(sdO + cb * kT * 128, &tmdO, &bars->fixed_full, cb * 64, q0, h, b);
         }
-        issued = j + 1;
+        int issued = 0;
+        for (int j = 0; j < n_kt; ++j) {
+          const int a = j % C::kKSlots, v = j % C::kVSlots;
+          if (j >= C::kKSlots &&
+              !mbar_wait(&bars->empty[a], static_cast<uint32_t>(j / C::kKSlots - 1) & 1u, wc, kSiteLoad))
+            break;
+          if (j >= C::kVSlots &&
+              !mbar_wait(&bars->empty2[v], static_cast<uint32_t>(j / C::kVSlots - 1) & 1u, wc, kSiteLoad))
+            break;
+          mbar_arrive_expect_tx(&bars->full[a], 2 * C::kTileBytes);
+#pragma unroll
+          for (int cb = 0; cb < HD / 64; ++cb) {
+            tma_load_4d(kring + a * C::kTileBytes + cb * kT * 128, &tmK, &bars->full[a], cb * 64,
+                        (kt0 + j) * kT, hk, b);
+            tma_load_4d(vring + v * C::kTileBytes + cb * kT * 128, &tmV, &bars->full[a], cb * 64,
+                        (kt0 + j) * kT, hk, b);
+          }
+          issued = j + 1;
+        }
+        drain(&bars->fixed_full, 0, wc.limit_ns);
+        for (int j = (issued > C::kKSlots ? issued - C::kKSlots : 0); j < issued; ++j)
+          drain(&bars->full[j % C::kKSlots], static_cast<uint32_t>(j / C::kKSlots) & 1u, wc.limit_ns);
       }
-      drain(&bars->fixed_full, 0, wc.limit_ns);
-      for (int j = (issued > C::kKSlots ? issued - C::kKSlots : 0); j < issued; ++j)
-        drain(&bars->full[j % C::kKSlots], static_cast<uint32_t>(j / C::kKSlots) & 1u, wc.limit_ns);
-    }
-  } else if (warp == kMmaWarp) {
-    // Order: S_0, dP_0; then per key tile j: S_{j+1}, dQ += dS_j K_j, dP_{j+1}.
-    if (n_kt > 0) {
-      const uint64_t qA = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t dA = sdesc_sw128(smem_u32(sdO), 16, 1024);
-      [[maybe_unused]] auto slope_step = [&](uint32_t s_col, int j) {
-        add_slope<kF16>(s_col, smem_u32(bias) + kSlopeRowsBytes / 2, smem_u32(bias),
-                        linear ? slope_side((kt0 + j) * kT, q0 + p.q_offset, pt.left) : 0);
-      };
-      bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);
-      if (ok) ok = warp_wait(&bars->full[0], 0, wc, kSiteMma);
-      if (ok) {
-        tc_fence_after_sync();
-        mma_abt<128, HD, kF16, true>(tmem, qA, sdesc_sw128(smem_u32(kring), 16, 1024));
-        if constexpr (MODE == kModSlopes) slope_step(tmem, 0);
-        mma_commit<true>(&bars->s_full[0]);
-        mma_abt<128, HD, kF16, true>(tmem + kDqColDP, dA, sdesc_sw128(smem_u32(vring), 16, 1024));
-        mma_commit<true>(&bars->dp_full);
-        mma_commit<true>(&bars->empty2[0]);
-      }
-      for (int j = 0; ok && j < n_kt; ++j) {
-        const int a = j % C::kKSlots, a1 = (j + 1) % C::kKSlots, v1 = (j + 1) % C::kVSlots;
-        const uint32_t sk = smem_u32(kring + a * C::kTileBytes);
-        const uint32_t nk = smem_u32(kring + a1 * C::kTileBytes);
-        const uint32_t nv = smem_u32(vring + v1 * C::kTileBytes);
-        const bool more = j + 1 < n_kt;
-        if (more) {
-          ok = warp_wait(&bars->full[a1], static_cast<uint32_t>((j + 1) / C::kKSlots) & 1u, wc, kSiteMma);
+    } else if (warp == kMmaWarp) {
+      // Order: S_0, dP_0; then per key tile j: S_{j+1}, dQ += dS_j K_j, dP_{j+1}.
+      if (n_kt > 0) {
+        const uint64_t qA = sdesc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dA = sdesc_sw128(smem_u32(sdO), 16, 1024);
+        [[maybe_unused]] auto slope_step = [&](uint32_t s_col, int j) {
+          add_slope<kF16>(s_col, smem_u32(bias) + kSlopeRowsBytes / 2, smem_u32(bias),
+                          linear ? slope_side((kt0 + j) * kT, q0 + p.q_offset, pt.left) : 0);
+        };
+        bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);
+        if (ok) ok = warp_wait(&bars->full[0], 0, wc, kSiteMma);
+        if (ok) {
+          tc_fence_after_sync();
+          mma_abt<128, HD, kF16, true>(tmem, qA, sdesc_sw128(smem_u32(kring), 16, 1024));
+          if constexpr (MODE == kModSlopes) slope_step(tmem, 0);
+          mma_commit<true>(&bars->s_full[0]);
+          mma_abt<128, HD, kF16, true>(tmem + kDqColDP, dA, sdesc_sw128(smem_u32(vring), 16, 1024));
+          mma_commit<true>(&bars->dp_full);
+          mma_commit<true>(&bars->empty2[0]);
+        }
+        for (int j = 0; ok && j < n_kt; ++j) {
+          const int a = j % C::kKSlots, a1 = (j + 1) % C::kKSlots, v1 = (j + 1) % C::kVSlots;
+          const uint32_t sk = smem_u32(kring + a * C::kTileBytes);
+          const uint32_t nk = smem_u32(kring + a1 * C::kTileBytes);
+          const uint32_t nv = smem_u32(vring + v1 * C::kTileBytes);
+          const bool more = j + 1 < n_kt;
+          if (more) {
+            ok = warp_wait(&bars->full[a1], static_cast<uint32_t>((j + 1) / C::kKSlots) & 1u, wc, kSiteMma);
+            if (!ok) break;
+            tc_fence_after_sync();
+            mma_abt<128, HD, kF16, true>(tmem + 128 * ((j + 1) & 1), qA, sdesc_sw128(nk, 16, 1024));
+            if constexpr (MODE == kModSlopes) slope_step(tmem + 128 * ((j + 1) & 1), j + 1);
+            mma_commit<true>(&bars->s_full[(j + 1) & 1]);
+          }
+          ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(j) & 1u, wc, kSiteMma);
           if (!ok) break;
           tc_fence_after_sync();
-          mma_abt<128, HD, kF16, true>(tmem + 128 * ((j + 1) & 1), qA, sdesc_sw128(nk, 16, 1024));
-          if constexpr (MODE == kModSlopes) slope_step(tmem + 128 * ((j + 1) & 1), j + 1);
-          mma_commit<true>(&bars->s_full[(j + 1) & 1]);
+          mma_groups<HD, kF16>(tmem + kDqColAcc, tmem + kDqColDP, sdesc_sw128(sk, kT * 128, 1024), j > 0);
+          mma_commit<true>(&bars->empty[a]);
+          if (more) {
+            mma_abt<128, HD, kF16, true>(tmem + kDqColDP, dA, sdesc_sw128(nv, 16, 1024));
+            mma_commit<true>(&bars->dp_full);
+            mma_commit<true>(&bars->empty2[v1]);
+          }
         }
-        ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(j) & 1u, wc, kSiteMma);
-        if (!ok) break;
-        tc_fence_after_sync();
-        mma_groups<HD, kF16>(tmem + kDqColAcc, tmem + kDqColDP, sdesc_sw128(sk, kT * 128, 1024), j > 0);
-        mma_commit<true>(&bars->empty[a]);
-        if (more) {
-          mma_abt<128, HD, kF16, true>(tmem + kDqColDP, dA, sdesc_sw128(nv, 16, 1024));
-          mma_commit<true>(&bars->dp_full);
-          mma_commit<true>(&bars->empty2[v1]);
-        }
+        if (ok) mma_commit<true>(&bars->acc_full);
+        mma_commit<true>(&bars->mma_drain);
+        drain(&bars->mma_drain, 0, wc.limit_ns);
+        __syncwarp();
       }
-      if (ok) mma_commit<true>(&bars->acc_full);
-      mma_commit<true>(&bars->mma_drain);
-      drain(&bars->mma_drain, 0, wc.limit_ns);
-      __syncwarp();
     }
   } else {
+    regs_inc<216>();
     const int c0 = 64 * (warp >> 2);         // this warpgroup's columns (keys)
     const int row = (warp & 3) * 32 + lane;  // query row of the tile = tensor-memory lane
     const int q = q0 + row;
@@ -1395,12 +1414,23 @@ inline int dkdv_split(long long units, int num_sms, long long pairs, int of) {
   return best;
 }
 
+// The setmaxnreg split hands out exactly 384 x 168 registers; a build with
+// another launch count would wait forever in setmaxnreg.inc and is refused.
+constexpr int kLaunchRegs = 168;
+
 template <int HD, bool kF16, int MODE>
 cudaError_t set_attrs() {
   constexpr int kDkdvMode = MODE == kModRelWide ? kModRel : MODE;
   static_assert(dkdv_smem_bytes<HD, kDkdvMode>() <= 232448 && dq_smem_bytes<HD, MODE>() <= 232448,
                 "shared memory per CTA");
-  cudaError_t e = cudaFuncSetAttribute(dkdv_kernel<HD, kF16, kDkdvMode>,
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, dkdv_kernel<HD, kF16, kDkdvMode>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncGetAttributes(&fa, dq_kernel<HD, kF16, MODE>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(dkdv_kernel<HD, kF16, kDkdvMode>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        dkdv_smem_bytes<HD, kDkdvMode>());
   if (e != cudaSuccess) return e;
