@@ -283,24 +283,23 @@ __device__ __forceinline__ void p_part(uint32_t s_addr, int c0, const Params& p,
   constexpr bool kCap = mode_cap(MODE);
   Chunk sa, sb;
   float ta = 0.f, tb = 0.f;
-  if constexpr (kCap) tmem_ld_red_32x32b_x32<true>(s_addr + c0, sa, ta);
+  if constexpr (kCap) tmem_ld_absmax_32(s_addr + c0, sa, ta);
   else tmem_ld_32x32b_x32(s_addr + c0, sa);
   tmem_ld_wait();
   reg_fence32(sa);
   asm volatile("" : "+f"(ta));
-  if constexpr (kCap) tmem_ld_red_32x32b_x32<true>(s_addr + c0 + 32, sb, tb);
+  if constexpr (kCap) tmem_ld_absmax_32(s_addr + c0 + 32, sb, tb);
   else tmem_ld_32x32b_x32(s_addr + c0 + 32, sb);
   const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-  auto half = [&](Chunk& sv, float top, int h) {
+  auto half = [&](Chunk& sv, float size, int h) {
     uint32_t pk[16];
     bool small = true, tiny = false;
     if constexpr (kCap) {
       if constexpr (kMask) {  // masked scores, which may hold anything, take no part in the choice
 #pragma unroll
         for (int e = 0; e < 32; ++e) sv[e] = vis(c0 + 32 * h + e) ? sv[e] : 0u;
-        top = chunk_max(sv);
+        size = fmaxf(chunk_max(sv), -chunk_min(sv));
       }
-      const float size = fmaxf(top, -chunk_min(sv));
       small = __all_sync(0xffffffffu, size <= p.cap.s_max);
       tiny = __all_sync(0xffffffffu, size <= 0.5f * p.cap.s_max);
     }

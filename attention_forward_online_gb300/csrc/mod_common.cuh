@@ -102,6 +102,7 @@ struct CapArgs {
   float inv2;             // 1 / cap2^2
   float k[4];
   float q[3];             // the same of degree 2, for |y / cap| <= 0.2, that is up to s_max / 2
+  float s_free;           // up to here, s_max / 2 at most, logits are within 15 (base 2): 2^x needs no max
 };
 inline CapArgs make_cap(float scale, float softcap) {
   CapArgs c{};
@@ -117,6 +118,8 @@ inline CapArgs make_cap(float scale, float softcap) {
   const bool ok = size <= 4096.0;
   c.s_max = !ok ? -1.f : (size < low ? 65536.f : static_cast<float>(0.4 / size));
   const double t2[3] = {0.9999998948, -0.3332859090, 0.1301540755};
+  const double unit = (scale < 0 ? -scale : scale) * 1.4426950408889634;  // logit of a score of 1
+  c.s_free = static_cast<float>(15.0 / unit < 0.5 * c.s_max ? 15.0 / unit : 0.5 * c.s_max);
   double pw = a;
   for (int n = 0; n < 4; ++n, pw *= a * a) {
     c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;

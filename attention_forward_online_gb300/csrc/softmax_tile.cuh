@@ -47,12 +47,34 @@ __device__ __forceinline__ void set_pair(Chunk& v, int e, uint64_t x) {
   v[e + 1] = __float_as_uint(b);
 }
 
+// 32 scores of a row, and the greatest of their magnitudes (NaN aside).
+__device__ __forceinline__ void tmem_ld_absmax_32(uint32_t taddr, Chunk& v, float& size) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.f32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+      "%32, [%33];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]),
+        "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+        "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+        "=r"(v[30]), "=r"(v[31]), "=f"(size)
+      : "r"(taddr));
+}
+
 using Row = Chunk[kChunks];
 
-// The row's scores and the max of each chunk, formed by the loads.
+// The row's scores and the max (kAbs: the greatest magnitude) of each chunk,
+// formed by the loads.
+template <bool kAbs>
 __device__ __forceinline__ void load_row(uint32_t s_addr, Row& v, float (&top)[kChunks]) {
 #pragma unroll
-  for (int ch = 0; ch < kChunks; ++ch) tmem_ld_red_32x32b_x32<true>(s_addr + ch * 32, v[ch], top[ch]);
+  for (int ch = 0; ch < kChunks; ++ch) {
+    if constexpr (kAbs) tmem_ld_absmax_32(s_addr + ch * 32, v[ch], top[ch]);
+    else tmem_ld_red_32x32b_x32<true>(s_addr + ch * 32, v[ch], top[ch]);
+  }
   tmem_ld_wait();
 #pragma unroll
   for (int ch = 0; ch < kChunks; ++ch) {
@@ -156,14 +178,30 @@ struct TileScore {
   // publish(alpha_bits) as soon as it is known, and updates l.
   // gap(ch)(e): the distance of key e of chunk ch, for both_sides.
   // kMasked: some rows of the warp may not see all of the tile.
-  // kShort: with the shorter polynomial for small capped scores (capped prompt
-  // of 8192: 467 us against 487; its code costs kernels of few tiles 2 us).
+  // kShort: with a shorter way for small capped scores (its code costs kernels
+  // of few tiles 2 us).
   template <bool kMasked, bool kShort, typename BitsOf, typename Gap, typename Publish>
   __device__ __forceinline__ void tile(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
                                        float& m, float& l, Publish&& publish) const {
     Row v;
     float top[kChunks];
-    load_row(s_addr, v, top);
+    constexpr bool kFree = kShort && !kMasked && MODE == kModCap;
+    load_row<kFree>(s_addr, v, top);
+    if constexpr (kFree) {
+      // Scores so small that 2^x is safe against any max up to 2^15 off: no
+      // max, and the accumulator's factor (1, but for a max below 0 so far)
+      // before anything else.
+      if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= cap->s_free)) {
+        const float m_new = fmaxf(m, 0.f);
+        publish(alpha_bits(m, m_new));
+        const float sum = exps<false, true, 2>(s_addr, v, k, bits_of, -m_new);
+        l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
+        m = m_new;
+        return;
+      }
+#pragma unroll
+      for (int ch = 0; ch < kChunks; ++ch) top[ch] = chunk_max(v[ch]);
+    }
     if constexpr (kMasked) {
       // Masked scores, which may hold anything: out of the max, and 0 where
       // scores share a reciprocal.
@@ -186,12 +224,10 @@ struct TileScore {
     }
     const float best_raw = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     bool direct = true;  // uniform over the warp
-    [[maybe_unused]] bool tiny = false;  // the shorter polynomial will do
     if constexpr (MODE == kModCap) {
       const float least = fminf(fminf(chunk_min(v[0]), chunk_min(v[1])), fminf(chunk_min(v[2]), chunk_min(v[3])));
       const float size = fmaxf(best_raw, -least);
       direct = __all_sync(0xffffffffu, size <= cap->s_max);
-      if constexpr (kShort) tiny = __all_sync(0xffffffffu, size <= 0.5f * cap->s_max);
     }
     if constexpr (MODE == kModSlopes) direct = !both_sides;
     if constexpr (MODE == kModCapSlopes) direct = false;
@@ -203,8 +239,7 @@ struct TileScore {
       // a row with no key so far has m_new = -inf and every x = -inf: against
       // 0 each p is exactly 0
       const float n = off - (m_new == -INFINITY ? 0.f : m_new);
-      if (kShort && MODE == kModCap && tiny) sum = exps<kMasked, true, 2>(s_addr, v, k, bits_of, n);
-      else sum = exps<kMasked, true, 3>(s_addr, v, k, bits_of, n);
+      sum = exps<kMasked, true, 3>(s_addr, v, k, bits_of, n);
     } else if constexpr (MODE != kModPlain) {
       float best = -INFINITY;
       const bool bound = mode_rel(MODE) && strip_close;
