@@ -34,7 +34,7 @@
 // warp 8 TMA producer; warp 9 issues the MMAs; 10 and 11 fill the warpgroup
 // whose registers the others take (216 for the elementwise warps: 2 % faster
 // than the 168 of an even share, which spill).  Tensor memory, dkdv:
-// [0, 128) S^T, [128, 256) dP^T, then dV and dK; dq: two S buffers, dP, dQ.
+// [0, 128) S^T, [128, 256) dP^T, then dV and dK, at d = 64 a second S^T; dq: two S buffers, dP, dQ.
 //
 // Masked places hold anything: their P and dY are selected to 0, never
 // multiplied, and rows of K (dq) or of Q and dO (dkdv) that take part in no
@@ -108,6 +108,12 @@ struct Cfg {
   static constexpr int kDqRegion = kDqTable + kDqTableBytes;
   static constexpr uint32_t kColAcc0 = 256;       // dV
   static constexpr uint32_t kColAcc1 = 256 + HD;  // dK
+  // dkdv: tensor memory has room for a second S^T tile at d = 64; place, column
+  // and phase of tile it
+  static constexpr bool kTwoS = HD == 64;
+  __device__ static constexpr int s_of(int it) { return kTwoS ? it & 1 : 0; }
+  __device__ static constexpr uint32_t s_col(int it) { return s_of(it) ? 384u : 0u; }
+  __device__ static constexpr uint32_t s_phase(int it) { return static_cast<uint32_t>(kTwoS ? it >> 1 : it) & 1u; }
 };
 
 struct __align__(16) Bars {
@@ -117,7 +123,7 @@ struct __align__(16) Bars {
   uint64_t empty2[4];
   uint64_t s_full[2];
   uint64_t dp_full;
-  uint64_t p_full;
+  uint64_t p_full[2];             // of S^T tile 0, 1: a warp may be a tile ahead of another
   uint64_t ds_full;
   uint64_t acc_full;
   uint64_t mma_drain;
@@ -508,8 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->empty2[s], 1);
     }
     mbar_init(&bars->s_full[0], 1);
+    mbar_init(&bars->s_full[1], 1);
     mbar_init(&bars->dp_full, 1);
-    mbar_init(&bars->p_full, 256);
+    mbar_init(&bars->p_full[0], 256);
+    mbar_init(&bars->p_full[1], 256);
     mbar_init(&bars->ds_full, 256);
     mbar_init(&bars->acc_full, 1);
     mbar_init(&bars->mma_drain, 1);
@@ -677,52 +685,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp) {
       // Order: S^T_0, dP^T_0; then per query tile dV += P^T dO, the next S^T,
-      // dK += dS^T Q, the next dP^T.  The tensor core runs them in issue order.
+      // dK += dS^T Q, the next dP^T; with two S^T tiles the next S^T comes first
+      // of all (it waited for P^T to be read: 440 of 2400 cycles a tile at d = 64).
+      // The tensor core runs them in issue order.
       if (n_it > 0) {
         const uint64_t kA = sdesc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t vA = sdesc_sw128(smem_u32(sV), 16, 1024);
-        bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma);
-        if (ok) ok = warp_wait(&bars->full[0], 0, wc, kSiteMma);
-        if (ok) {
+        auto scores = [&](int it) {
+          const int s = it % C::kStages;
+          if (!warp_wait(&bars->full[s], static_cast<uint32_t>(it / C::kStages) & 1u, wc, kSiteMma)) return false;
           tc_fence_after_sync();
-          const uint32_t sq = smem_u32(ring), sdo = sq + C::kTileBytes;
-          mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(sq, 16, 1024));
+          const uint32_t col = tmem + C::s_col(it);
+          mma_abt<128, HD, kF16, true>(col, kA, sdesc_sw128(smem_u32(ring + s * C::kStageBytes), 16, 1024));
           if constexpr (MODE == kModSlopes)
-            add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + first_it / cnt % 4 * kSlopeQBytes,
-                              smem_u32(bias_all), bars->side[0]);
-          mma_commit<true>(&bars->s_full[0]);
+            add_slope_t<kF16>(col, smem_u32(bias_all) + kSlopeRowsBytes + (first_it + it) / cnt % 4 * kSlopeQBytes,
+                              smem_u32(bias_all), bars->side[s]);
+          mma_commit<true>(&bars->s_full[C::s_of(it)]);
+          return true;
+        };
+        auto dp = [&](int it) {
+          const uint32_t sdo = smem_u32(ring + it % C::kStages * C::kStageBytes + C::kTileBytes);
           mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(sdo, 16, 1024));
           mma_commit<true>(&bars->dp_full);
-        }
+        };
+        bool ok = warp_wait(&bars->fixed_full, 0, wc, kSiteMma) && scores(0);
+        if (ok) dp(0);
         for (int it = 0; ok && it < n_it; ++it) {
-          const int s = it % C::kStages, s1 = (it + 1) % C::kStages;
+          const int s = it % C::kStages;
           const uint32_t sq = smem_u32(ring + s * C::kStageBytes), sdo = sq + C::kTileBytes;
-          const uint32_t nq = smem_u32(ring + s1 * C::kStageBytes), ndo = nq + C::kTileBytes;
           const bool more = it + 1 < n_it;
-          ok = warp_wait(&bars->p_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
+          if (C::kTwoS && more) ok = scores(it + 1);
+          if (ok) ok = warp_wait(&bars->p_full[C::s_of(it)], C::s_phase(it), wc, kSiteMma);
           if (!ok) break;
           tc_fence_after_sync();
-          mma_groups<HD, kF16>(tmem + C::kColAcc0, tmem, sdesc_sw128(sdo, kT * 128, 1024), it > 0);
+          mma_groups<HD, kF16>(tmem + C::kColAcc0, tmem + C::s_col(it), sdesc_sw128(sdo, kT * 128, 1024), it > 0);
           mma_commit<true>(&bars->empty2[s]);
-          if (more) {
-            ok = warp_wait(&bars->full[s1], static_cast<uint32_t>((it + 1) / C::kStages) & 1u, wc, kSiteMma);
-            if (!ok) break;
-            tc_fence_after_sync();
-            mma_abt<128, HD, kF16, true>(tmem, kA, sdesc_sw128(nq, 16, 1024));
-            if constexpr (MODE == kModSlopes)
-              add_slope_t<kF16>(tmem, smem_u32(bias_all) + kSlopeRowsBytes + (first_it + it + 1) / cnt % 4 * kSlopeQBytes,
-                                smem_u32(bias_all), bars->side[s1]);
-            mma_commit<true>(&bars->s_full[0]);
-          }
-          ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
+          if (!C::kTwoS && more) ok = scores(it + 1);
+          if (ok) ok = warp_wait(&bars->ds_full, static_cast<uint32_t>(it) & 1u, wc, kSiteMma);
           if (!ok) break;
           tc_fence_after_sync();
           mma_groups<HD, kF16>(tmem + C::kColAcc1, tmem + 128, sdesc_sw128(sq, kT * 128, 1024), it > 0);
           mma_commit<true>(&bars->empty[s]);
-          if (more) {
-            mma_abt<128, HD, kF16, true>(tmem + 128, vA, sdesc_sw128(ndo, 16, 1024));
-            mma_commit<true>(&bars->dp_full);
-          }
+          if (more) dp(it + 1);
         }
         if (ok) mma_commit<true>(&bars->acc_full);
         mma_commit<true>(&bars->mma_drain);
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         h_of = h;
       }
-      ok = mbar_wait(&bars->s_full[0], static_cast<uint32_t>(it) & 1u, wc, kSiteElem);
+      ok = mbar_wait(&bars->s_full[C::s_of(it)], C::s_phase(it), wc, kSiteElem);
       if (ok) ok = mbar_wait(&bars->full[s], static_cast<uint32_t>(it / C::kStages) & 1u, wc, kSiteElem);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -828,6 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first = k0 + 32 * (warp & 3) - p0 - c0 - 63;
         side = far_side(first, first + 94, p.rel.range);
       }
+      const uint32_t s_addr = lane_base + C::s_col(it);
       float pr[64];
       auto part = [&](auto mask) {
         constexpr bool kMask = decltype(mask)::value;
@@ -835,26 +840,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int R = p.rel.range;
           if (side != 0) {
             const float far = bias_all[side < 0 ? 0 : rel_entries(R) - 1];
-            p_part<kF16, MODE, true, kMask, true>(lane_base, c0, p, vis, l2of4, [&](int) { return far; }, pr);
+            p_part<kF16, MODE, true, kMask, true>(s_addr, c0, p, vis, l2of4, [&](int) { return far; }, pr);
           } else {
             const float* bt = bias_all + (d0 + R + kRelPad);
-            p_part<kF16, MODE, true, kMask, true>(lane_base, c0, p, vis, l2of4,
+            p_part<kF16, MODE, true, kMask, true>(s_addr, c0, p, vis, l2of4,
                                                   [&](int col) { return bt[-col]; }, pr);
           }
         } else if (mode_slopes(MODE) && (MODE == kModCapSlopes || bars->side[s] == 0)) {
           const float f0 = static_cast<float>(d0);
           p_part<kF16, MODE, true, kMask, true>(
-              lane_base, c0, p, vis, l2of4,
+              s_addr, c0, p, vis, l2of4,
               [&](int col) { return -slope2 * fabsf(f0 - static_cast<float>(col)); }, pr);
         } else {
-          p_part<kF16, MODE, true, kMask, false>(lane_base, c0, p, vis, l2of4, [](int) { return 0.f; }, pr);
+          p_part<kF16, MODE, true, kMask, false>(s_addr, c0, p, vis, l2of4, [](int) { return 0.f; }, pr);
         }
       };
       bool waited = false;
       if (full) {
         part(std::false_type{});
       } else if (none) {
-        p_none<true>(lane_base, c0, pr);
+        p_none<true>(s_addr, c0, pr);
       } else {
         part(std::true_type{});
         if (seen & 2) {
@@ -876,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_st_wait();
       tc_fence_before_sync();
-      mbar_arrive(&bars->p_full);
+      mbar_arrive(&bars->p_full[C::s_of(it)]);
       if (!waited) {
         ok = mbar_wait(&bars->dp_full, static_cast<uint32_t>(it) & 1u, wc, kSiteElem);
         ok = __all_sync(0xffffffffu, ok);
