@@ -11,7 +11,10 @@
 //
 // Launches, in order on one stream:
 //   dq_kernel    one CTA per 128-row query tile; K and V tiles stream.  Also
-//                writes D.
+//                writes D, without a cap corrected by the row's sum of dY (for
+//                dK and dTable; 2 % of a step, and bf16 gradients of a learned
+//                bias are off by 0.0015 to 0.0017 of their size, the rounding
+//                of the result, in place of 0.003 to 0.004).
 //   dkdv_kernel  one CTA per 128-key tile of a key head; the query tiles of
 //                every head of its group that can see those keys stream, so
 //                the sums over heads stay in tensor memory and nothing is
@@ -26,8 +29,9 @@
 //   rel_reduce   folds the partial sums by distance into the table's buckets.
 // P and dS are rounded to 16 bits as MMA operands (the tensor core's operand
 // width, half a step of the outputs' type each), everything is summed in fp32.
-// D is formed from the 16-bit O that the caller has: dY then misses a row's
-// true sum by dO times O's rounding, as much again as the rounding of dS.
+// D is formed from the 16-bit O that the caller has: a row's dY then miss their
+// sum of 0 by dO times O's rounding, as much again in dQ as the rounding of dS
+// (bf16: 0.0027 to 0.003 of its size together; dK 0.0024).
 //
 // CTA layout (384 threads): warps 0-7 elementwise in two warpgroups, group g
 // taking columns 64g .. 64g + 63 of every score tile, one tile row a thread;
@@ -44,12 +48,12 @@
 // forward pass: 1.2 us a 128 x 128 tile in dq_kernel and 1.8 in dkdv_kernel
 // at d = 128 without masks, where the 3 and 4 products take 0.75 and 1.0.
 // Measured (dq, dkdv), bf16:
-//   B2 H16 kv4 4096 d128 window 1024 cap 50    134, 181 us
-//   B1 H16 8192 d128 documents of about 700    107, 135 us
-//   B1 H16 4096 d128 learned bias, no mask     157, 229 us (1310 and 1200 TFLOP/s
-//     as executed; 890 together for the 5 products that the mathematics asks for)
-//   B8 H12 512 d64 learned bias                 27,  48 us;  table sums 5 us
-//   B4 H8 kv2 381 d64 fp16 prefix                8,  15 us
+//   B2 H16 kv4 4096 d128 window 1024 cap 50    130, 177 us
+//   B1 H16 8192 d128 documents of about 700    112, 134 us
+//   B1 H16 4096 d128 learned bias, no mask     167, 228 us (1230 and 1210 TFLOP/s
+//     as executed; 870 together for the 5 products that the mathematics asks for)
+//   B8 H12 512 d64 learned bias                 29,  49 us;  table sums 5 us
+//   B4 H8 kv2 381 d64 fp16 prefix                8,  14 us
 #pragma once
 
 #include <cmath>
@@ -395,8 +399,9 @@ __device__ __forceinline__ void p_none(uint32_t s_addr, int c0, float (&pr)[64])
 // dS part over the same 64 columns of the dP tile: dS = pr (dP - D), in 16
 // bits over columns c0 .. c0 + 31; ndof4(column): -D of 4 columns.  kMask: a
 // masked place (pr = 0) gives 0 whatever dP and D are.  kKeep: pr returns dS.
-template <bool kF16, bool kMask, bool kKeep, typename Dof4>
-__device__ __forceinline__ void ds_part(uint32_t dp_addr, int c0, Dof4&& ndof4, float (&pr)[64]) {
+// kSum: sum2 gets the row's fp32 dS added, as two partial sums.
+template <bool kF16, bool kMask, bool kKeep, bool kSum, typename Dof4>
+__device__ __forceinline__ void ds_part(uint32_t dp_addr, int c0, Dof4&& ndof4, float (&pr)[64], uint64_t& sum2) {
   uint32_t dva[32], dvb[32];
   tmem_ld_32x32b_x32(dp_addr + c0, dva);
   tmem_ld_wait();
@@ -423,6 +428,7 @@ __device__ __forceinline__ void ds_part(uint32_t dp_addr, int c0, Dof4&& ndof4, 
 #pragma unroll
         for (int u = 0; u < 4; ++u) pr[x + u] = gr[u];
       }
+      if constexpr (kSum) sum2 = f2_add(sum2, f2_add(f2_pack(gr[0], gr[1]), f2_pack(gr[2], gr[3])));
       gk[2 * g] = pack2<kF16>(gr[0], gr[1]);
       gk[2 * g + 1] = pack2<kF16>(gr[2], gr[3]);
     }
@@ -890,10 +896,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after_sync();
       auto dof4 = [&](int col) { return dd[col >> 2]; };
       constexpr bool kKeep = mode_rel(MODE);
+      uint64_t no_sum = 0;
       if (full)
-        ds_part<kF16, false, kKeep>(lane_base + 128, c0, dof4, pr);
+        ds_part<kF16, false, kKeep, false>(lane_base + 128, c0, dof4, pr, no_sum);
       else
-        ds_part<kF16, true, kKeep>(lane_base + 128, c0, dof4, pr);
+        ds_part<kF16, true, kKeep, false>(lane_base + 128, c0, dof4, pr, no_sum);
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&bars->ds_full);
@@ -1224,6 +1231,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int v = 0; v < kNv; ++v) ov[v] = orow[v];
     }
     float4 dv4 = make_float4(0.f, 0.f, 0.f, 0.f);  // -D
+    // A row's dY sum to 0 but for the error that D has from O's rounding to 16
+    // bits: the sum is what D lacks.  dQ is done by then, dK and the table's
+    // gradient take the right D.  (Capped scores: pr has the cap's factor in it.)
+    constexpr bool kFixD = !mode_cap(MODE);
+    [[maybe_unused]] uint64_t rest2 = 0;
     if (n_kt == 0 && g == 0 && in) p.D[rix] = 0.f;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     [[maybe_unused]] uint32_t sync_phase = 0;
@@ -1335,9 +1347,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after_sync();
       auto dof4 = [&](int) { return dv4; };
       if (full)
-        ds_part<kF16, false, false>(lane_base + kDqColDP, c0, dof4, pr);
+        ds_part<kF16, false, false, kFixD>(lane_base + kDqColDP, c0, dof4, pr, rest2);
       else
-        ds_part<kF16, true, false>(lane_base + kDqColDP, c0, dof4, pr);
+        ds_part<kF16, true, false, kFixD>(lane_base + kDqColDP, c0, dof4, pr, rest2);
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&bars->ds_full);
@@ -1348,6 +1360,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (ok) tc_fence_after_sync();
       has_acc = ok;
+    }
+    if constexpr (kFixD) {
+      if (ok && n_kt > 0) {
+        float r0, r1;
+        f2_unpack(rest2, r0, r1);
+        if (g == 1) bars->d_part[row] = r0 + r1;  // everyone has D: dS was complete
+        ok = elem_sync(bars, sync_phase, wc);
+        if (ok && g == 0 && row_live) p.D[rix] = (r0 + r1 + bars->d_part[row]) - dv4.x;
+      }
     }
     if (ok) {
       // over Q, whose last reader is done

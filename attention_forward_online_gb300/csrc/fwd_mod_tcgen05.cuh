@@ -28,7 +28,7 @@
 // What bounds it: the softmax between a score tile's two products, by issue
 // and latency (two tiles a CTA hide each other's products, not all of each
 // other's softmax).  Per 128 x 128 tile the products take 512 cycles each at
-// d = 128, the exponentials 512 of the multifunction unit; a cap adds 3 to 4
+// d = 128, the exponentials 512 of the multifunction unit; a cap adds 4 to 5
 // packed operations a pair of scores where the polynomial serves, else an
 // exponential and a quarter of a reciprocal a score; one-sided slopes add a
 // 16-element MMA step and nothing per score; a learned bias one packed FMA's
@@ -36,10 +36,10 @@
 //
 // Measured (bf16, causal unless noted; "of measured" is the copy and dense
 // bf16 matrix rate of this GPU type, 6.78 TB/s and 1940 TFLOP/s):
-//   B1 H32 kv8 8192 d128 cap 50       466 us, 1180 TFLOP/s, 61 % of measured
-//   B4 H16 2048 d128 plain / cap / slopes / both      72 / 106 / 83 / 141 us
-//   B4 H16 2048 d64  plain (no mask) / cap / slopes / both   93 / 95 / 71 / 124 us
-//   B4 H16 1501 d64 fp16 learned bias  51 us;  B1 H16 4096 d128, no mask, 115 us
+//   B1 H32 kv8 8192 d128 cap 50       444 us, 1238 TFLOP/s, 64 % of measured
+//   B4 H16 2048 d128 plain / cap / slopes / both      70 / 101 / 82 / 141 us
+//   B4 H16 2048 d64  plain (no mask) / cap / slopes / both   93 / 91 / 71 / 123 us
+//   B4 H16 1501 d64 fp16 learned bias  52 us;  B1 H16 4096 d128, no mask, 115 us
 // A unit of 256 rows costs 3 us before its first score and 2 us after its last
 // besides (about 5 steps of such a pair of tiles in all at d = 64).
 #pragma once
