@@ -49,10 +49,10 @@
 // at d = 128 without masks, where the 3 and 4 products take 0.75 and 1.0.
 // Measured (dq, dkdv), bf16:
 //   B2 H16 kv4 4096 d128 window 1024 cap 50    130, 177 us
-//   B1 H16 8192 d128 documents of about 700    112, 134 us
+//   B1 H16 8192 d128 documents of about 700    113, 134 us
 //   B1 H16 4096 d128 learned bias, no mask     167, 228 us (1230 and 1210 TFLOP/s
 //     as executed; 870 together for the 5 products that the mathematics asks for)
-//   B8 H12 512 d64 learned bias                 29,  49 us;  table sums 5 us
+//   B8 H12 512 d64 learned bias                 28,  49 us;  table sums 5 us
 //   B4 H8 kv2 381 d64 fp16 prefix                8,  14 us
 #pragma once
 

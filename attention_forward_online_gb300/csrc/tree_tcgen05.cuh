@@ -27,7 +27,8 @@
 // 13 MMA issue.  Tensor memory: S0, S1 (P in 16 bits over them), O0, O1.
 //
 // Measured (bf16; "of measured": of this GPU type's copy rate, 6.78 TB/s):
-//   B64 H32 kv8 T1 ctx 4096 .. 8192 d128   258 us, 6.25 TB/s, 92 % of measured
+//   B64 H32 kv8 T1 ctx 4096 .. 8192 d128   258 to 265 us, 6.1 to 6.25 TB/s, 90 to
+//     92 % of measured
 //   B8 H32 kv8 T27 ctx 3000 .. 6000 d128 cap 30, pages of 32    57 us, 39 %:
 //     the first scores come after 9 us (every CTA's 6 slots fill together), the
 //     tiles at 5.3 TB/s after that, the last tile's softmax, the partial and the
