@@ -228,6 +228,19 @@ def test_masked_places_hold_anything(kind, fill):
             assert (dirty[g][b, :, n:] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (FP, 64)], ids=["bf16-128", "fp16-64"])
+def test_bias_gradients_sum_to_zero(dtype, d):
+    # A row's dY sum to 0, so a head's table gradients do, but for the rounding
+    # of each to 16 bits (half a step) and what P, with its exponent and LSE in
+    # fp32, is off (2^-20) times the greatest |dY| there can be, 2 |dO| |V|.
+    q, k, v, do = tensors(2, 4, 2, 300, 333, d, dtype, seed=41)
+    got = run(q, k, v, do, {}, **score_args("rel", 4, dtype))
+    drel = got["drel"].double()
+    most = 2 * do.double().norm(dim=-1).max() * v.double().norm(dim=-1).max()
+    bound = drel.abs().sum(0) * torch.finfo(dtype).eps / 2 + 2 * 300 * most * 2.0**-20
+    assert (drel.sum(0).abs() <= bound).all(), (drel.sum(0), bound)
+
+
 @pytest.mark.parametrize("kind", ["plain", "cap", "slopes", "rel"])
 def test_large_values(kind):
     q, k, v, do = tensors(1, 2, 1, 200, 300, 64, BF, seed=31)
