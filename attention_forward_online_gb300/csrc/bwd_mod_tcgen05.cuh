@@ -1449,7 +1449,10 @@ __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restric
 // CTAs that share a key tile's (head, query tile) pairs, of which it has at
 // most `pairs`, as a power of two: one that divides `of`, leaves a CTA two
 // pairs, and makes the kernel shortest if a CTA takes 1 / s of a tile's time
-// and a quarter of it besides, and the SMs take the CTAs in rounds.
+// and a quarter of it besides, and the SMs take the CTAs in rounds.  Whole
+// steps, without / with: 18 key tiles, B1 H8 kv2 1078 d64, 120 / 73 us (8 CTAs
+// each); 24 tiles of a group of 4, B2 H8 kv2 1530 learned bias, 183 / 130 us (4);
+// but 96 tiles, B1 H4 2967 d128, 112 / 122 us with 4, so they stay whole.
 inline int dkdv_split(long long units, int num_sms, long long pairs, int of) {
   int best = 0;
   double cost = 0.0;

@@ -261,7 +261,9 @@ struct TileScore {
 
   // The same for a masked tile by a rolled loop that reads each chunk from
   // tensor memory twice: a third of the instructions, for tiles that a CTA
-  // meets once or twice, whose code then comes from far.
+  // meets once or twice, whose code then comes from far (a tree of 27 drafts
+  // over 6000 keys: 50 us against 57; a prompt's many masked tiles would be 10
+  // to 25 % slower).
   template <typename BitsOf, typename Gap, typename Publish>
   __device__ __forceinline__ void tile_rolled(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
                                               float& m, float& l, Publish&& publish) const {
