@@ -791,6 +791,11 @@ def bwd_mod_workspace_bytes(B: int, H: int, Nq: int, Nkv: int, rel_range: int = 
     return int(lib().osattn_bwd_mod_workspace_bytes(int(B), int(H), int(Nq), int(Nkv), int(rel_range)))
 
 
+def _bwd_mod_workspace(B, H, Nq, Nkv, rel_range):
+    """bwd_mod_workspace_bytes() without a call into the library."""
+    return 4 * B * H * (Nq + ((Nkv + 127) // 128 * (2 * rel_range + 1) if rel_range else 0))
+
+
 def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap: float = 0.0,
             slopes=None, rel_table=None, rel_map=None, dq=None, dk=None, dv=None, drel=None,
             workspace=None, stream=None):
@@ -829,8 +834,7 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
         raise ValueError("drel needs a rel_table")
     L = _lib or lib()
     if workspace is None:
-        need = L.osattn_bwd_mod_workspace_bytes(B, H, Nq, Nkv, score.rel_range)
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = q.new_empty(_bwd_mod_workspace(B, H, Nq, Nkv, score.rel_range), dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError("workspace must be contiguous on q's device")
     st = L.osattn_bwd_mod(
@@ -850,6 +854,12 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
 # ---------------------------------------------------------------- paged cache
 def tree_workspace_bytes(B: int, H: int, Hkv: int, T: int, d: int) -> int:
     return int(lib().osattn_tree_workspace_bytes(int(B), int(H), int(Hkv), int(T), int(d)))
+
+
+def _tree_workspace(B, group, T, d):
+    """tree_workspace_bytes() without a call into the library (4 us of a step
+    of 31, its code being cold after a launch)."""
+    return (B + 4) // 4 * 16 + 1280 * min(T, max(128 // group, 1)) * group * (d + 1)
 
 
 def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: float | None = None,
@@ -902,8 +912,7 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
     lse = _lse(lse, (B, H, T), index, q)
     L = _lib or lib()
     if workspace is None:
-        workspace = q.new_empty(max(L.osattn_tree_workspace_bytes(B, H, Hkv, T, d), 16),
-                                dtype=torch.uint8)
+        workspace = q.new_empty(_tree_workspace(B, H // Hkv, T, d), dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError("workspace must be contiguous on q's device")
     st = L.osattn_tree_attn(

@@ -52,6 +52,14 @@ def test_refusals(L, kw, expect):
     assert call(**kw) == expect
 
 
+def test_workspaces_of_the_binding(L):
+    for B, H, Hkv, T, d in [(1, 1, 1, 1, 64), (3, 8, 2, 5, 128), (4, 40, 8, 64, 64), (63, 128, 1, 2, 128),
+                            (700, 96, 1, 3, 64)]:
+        assert osattn._tree_workspace(B, H // Hkv, T, d) == osattn.tree_workspace_bytes(B, H, Hkv, T, d)
+    for args in [(1, 1, 1, 1, 0), (2, 12, 381, 129, 0), (3, 4, 500, 128, 1024), (1, 16, 4096, 4097, 128)]:
+        assert osattn._bwd_mod_workspace(*args) == osattn.bwd_mod_workspace_bytes(*args)
+
+
 def test_workspace(L):
     rows = 2 * 160 * 5 * 4  # two partials a CTA, 5 tokens of 4 heads
     assert osattn.tree_workspace_bytes(2, 8, 2, 5, 64) == 16 + rows * 65 * 4
