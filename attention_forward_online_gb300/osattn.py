@@ -7,6 +7,11 @@ allocates outputs with torch (device and pinned host memory are torch's job
 here), and passes raw pointers and the current stream through the C ABI
 declared in include/osattn.h.  If libosattn.so is missing the calls raise:
 there is no fallback implementation.
+
+A call's `stream` defaults to torch's current one.  Given another, the call
+works as if it were current: its kernels, and the copies, outputs and
+workspaces it makes, are in that stream's order, where its inputs have to be
+ready; the results are marked as used by the caller's current stream too.
 """
 from __future__ import annotations
 
@@ -174,6 +179,46 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(index):
+    """Handle of torch's current stream on device `index`."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _elsewhere_stream(stream, index):
+    """Whether `stream` is given and is not torch's current one on device
+    `index`."""
+    if stream is None or stream.cuda_stream == _raw_stream(index):
+        return False
+    if stream.device_index != index:
+        raise ValueError("stream is on another device than the tensors")
+    return True
+
+
+def _under(stream, index, call, *given):
+    """call() with `stream` as torch's current one.  What a call makes (copies
+    of views, outputs, workspaces) then comes from that stream's memory and is
+    written in its order, behind whatever used the memory before; on the
+    caller's stream a copy could come after the kernel that reads it.  The
+    results are marked as used by the caller's stream too, and the tensors that
+    the caller gave as used by `stream`."""
+    import torch
+
+    caller = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        results = call()
+    for t in results if isinstance(results, tuple) else (results,):
+        if isinstance(t, MaskPlan):
+            t = t.buffer
+        if t is not None and t.is_cuda:
+            t.record_stream(caller)
+    for t in given:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
+    return results
+
+
 def fwd_raw(q_ptr, k_ptr, v_ptr, o_ptr, lse_ptr, B, H, Nq, Nkv, d, scale, causal,
             key_len_ptr, dtype, stream_handle) -> int:
     """Direct call of osattn_fwd with integer pointers; returns the status."""
@@ -241,6 +286,9 @@ def fwd(q, k, v, scale: float | None = None, causal: bool = False, key_len=None,
 
     B, H, Nq, Nkv, d = _shapes(q, k, v)
     dtype = _dtype_code(q)
+    index = q.get_device()
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: fwd(q, k, v, scale, causal, key_len, out, lse), out, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -309,9 +357,14 @@ def fwd_offload(q_host, k_host, v_host, out_host=None, lse_host=None, q=None, k=
     if k_host.dtype != q_host.dtype or v_host.dtype != q_host.dtype:
         raise TypeError("q_host, k_host, v_host must share one dtype")
     dtype = _dtype_code(q_host)
+    index = torch.cuda.current_device()
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: fwd_offload(q_host, k_host, v_host, out_host, lse_host, q, k, v, out,
+                                                         lse, scale, causal, key_len, heads_per_chunk),
+                      q, k, v, out, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dev = torch.device("cuda", torch.cuda.current_device())
+    dev = torch.device("cuda", index)
     q = torch.empty(q_host.shape, dtype=q_host.dtype, device=dev) if q is None else q
     k = torch.empty(k_host.shape, dtype=k_host.dtype, device=dev) if k is None else k
     v = torch.empty(v_host.shape, dtype=v_host.dtype, device=dev) if v is None else v
@@ -349,6 +402,10 @@ def fwd_splitkv(q, k, v, num_splits: int, scale: float | None = None, causal: bo
     import torch
 
     B, H, Nq, Nkv, d = _check_qkv(q, k, v)
+    index = q.get_device()
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: fwd_splitkv(q, k, v, num_splits, scale, causal, key_len, out, lse,
+                                                         workspace), out, lse, workspace)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     out = torch.empty_like(q) if out is None else out
@@ -387,6 +444,10 @@ def bwd(q, k, v, o, lse, do, scale: float | None = None, causal: bool = False, k
 
     B, H, Nq, Nkv, d = _shapes(q, k, v)
     dtype = _dtype_code(q)
+    index = q.get_device()
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: bwd(q, k, v, o, lse, do, scale, causal, key_len, dq, dk, dv, workspace),
+                      dq, dk, dv, workspace)
     for t in (o, do):
         if t.shape != q.shape or t.dtype != q.dtype or not t.is_cuda:
             raise ValueError("o and do must be CUDA tensors shaped and typed like q")
@@ -452,9 +513,15 @@ def bwd_offload(q_host, k_host, v_host, o_host, lse_host, do_host, scale: float 
     if tuple(lse_host.shape) != (B, H, Nq) or lse_host.dtype != torch.float32:
         raise ValueError("lse_host must be fp32 [B, H, Nq]")
     dtype = _dtype_code(q_host)
+    index = torch.cuda.current_device()
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: bwd_offload(q_host, k_host, v_host, o_host, lse_host, do_host, scale,
+                                                         causal, key_len, dq_host, dk_host, dv_host, device_buffers,
+                                                         workspace, heads_per_chunk),
+                      *(device_buffers or ()), workspace)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dev = torch.device("cuda", torch.cuda.current_device())
+    dev = torch.device("cuda", index)
     if device_buffers is None:
         mk = lambda ref: torch.empty(ref.shape, dtype=ref.dtype, device=dev)  # noqa: E731
         device_buffers = (mk(q_host), mk(k_host), mk(v_host), mk(o_host), mk(do_host),
@@ -498,6 +565,9 @@ def softmax_rows(x, out=None, lse=None, want_lse: bool = True, stream=None):
     codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
     if x.dtype not in codes:
         raise TypeError("x must be bf16, fp16 or fp32")
+    index = x.get_device()
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: softmax_rows(x, out, lse, want_lse), out, lse)
     rows, N = x.shape
     out = torch.empty_like(x) if out is None else out
     if want_lse and lse is None:
@@ -526,7 +596,11 @@ def softmax_rows_offload(x_host, out_host=None, lse_host=None, x=None, out=None,
     if x_host.dtype not in codes:
         raise TypeError("x_host must be bf16, fp16 or fp32")
     rows, N = x_host.shape
-    dev = torch.device("cuda", torch.cuda.current_device())
+    index = torch.cuda.current_device()
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: softmax_rows_offload(x_host, out_host, lse_host, x, out, lse, want_lse,
+                                                                  rows_per_chunk), x, out, lse)
+    dev = torch.device("cuda", index)
     x = torch.empty(x_host.shape, dtype=x_host.dtype, device=dev) if x is None else x
     out = torch.empty_like(x) if out is None else out
     out_host = torch.empty(x_host.shape, dtype=x_host.dtype).pin_memory() if out_host is None else out_host
@@ -573,27 +647,9 @@ def _int32(t, shape, index, name):
     return t.contiguous()
 
 
-def _raw_stream(index):
-    """Handle of torch's current stream on device `index`."""
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _handle(stream, index):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-
-
 def _elsewhere(index):
     """Whether another device than `index` is current."""
     return torch.cuda.current_device() != index
-
-
-def _keep(stream, index, tensors):
-    """Temporaries of a call that was given `stream`: not to be handed out
-    again before the work there is done."""
-    if stream is not None and stream.cuda_stream != _raw_stream(index):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
 
 
 @functools.lru_cache(maxsize=256)
@@ -639,16 +695,18 @@ def mask_plan(B: int, Nq: int, Nkv: int, causal: bool = False, window: int = 0, 
         with torch.cuda.device(index):
             return mask_plan(B, Nq, Nkv, causal, window, q_offset, *masks, device=f"cuda:{index}", out=out,
                              stream=stream)
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: mask_plan(B, Nq, Nkv, causal, window, q_offset, *masks,
+                                                       device=f"cuda:{index}", out=out),
+                      None if out is None else out.buffer)
     B, Nq, Nkv, window, q_offset = int(B), int(Nq), int(Nkv), int(window), int(q_offset)
     key_len = _int32(key_len, (B,), index, "key_len")
     prefix_len = _int32(prefix_len, (B,), index, "prefix_len")
     doc_ids = _int32(doc_ids, (B, Nkv), index, "doc_ids")
-    made = [key_len, prefix_len, doc_ids]
     if out is None:
         # tiles of 128 rows take 16 bytes each, rows 8
         need = max(B, 0) * ((max(Nq, 0) + 127) // 128 * 16 + max(Nq, 0) * 8)
         buffer = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-        made.append(buffer)
     else:
         buffer = out.buffer
         if out.B != B or out.Nq != Nq or buffer.get_device() != index:
@@ -657,8 +715,7 @@ def mask_plan(B: int, Nq: int, Nkv: int, causal: bool = False, window: int = 0, 
                                 1 if causal else 0, window,
                                 None if key_len is None else key_len.data_ptr(),
                                 None if prefix_len is None else prefix_len.data_ptr(),
-                                None if doc_ids is None else doc_ids.data_ptr(), _handle(stream, index))
-    _keep(stream, index, made)
+                                None if doc_ids is None else doc_ids.data_ptr(), _raw_stream(index))
     if st != OK:
         raise OsattnError(st, "osattn_mask_plan")
     if out is not None:
@@ -767,6 +824,9 @@ def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0
     if _elsewhere(index):
         with torch.cuda.device(index):
             return fwd_mod(q, k, v, scale, plan, softcap, slopes, rel_table, rel_map, out, lse, stream)
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: fwd_mod(q, k, v, scale, plan, softcap, slopes, rel_table, rel_map, out,
+                                                     lse), out, lse)
     dtype = _CODES.get(q.dtype)
     if dtype is None:
         raise TypeError("tensors must be bf16 or fp16")
@@ -780,10 +840,9 @@ def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, Nkv, d,
         _view_strides(q, "q"), _view_strides(k, "k"), _view_strides(v, "v"), _view_strides(out, "out"),
         1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(score),
-        None if plan is None else plan.buffer.data_ptr(), dtype, _handle(stream, index))
+        None if plan is None else plan.buffer.data_ptr(), dtype, _raw_stream(index))
     if st != OK:
         raise OsattnError(st, "osattn_fwd_mod")
-    _keep(stream, index, (out, lse, *held))
     return out, lse
 
 
@@ -809,6 +868,10 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
         with torch.cuda.device(index):
             return bwd_mod(q, k, v, o, lse, do, scale, plan, softcap, slopes, rel_table, rel_map, dq, dk, dv,
                            drel, workspace, stream)
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: bwd_mod(q, k, v, o, lse, do, scale, plan, softcap, slopes, rel_table,
+                                                     rel_map, dq, dk, dv, drel, workspace),
+                      dq, dk, dv, drel, workspace)
     dtype = _CODES.get(q.dtype)
     if dtype is None:
         raise TypeError("tensors must be bf16 or fp16")
@@ -844,10 +907,9 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
         _view_strides(o, "o"), _view_strides(do, "do"), _view_strides(dq, "dq"), _view_strides(dk, "dk"),
         _view_strides(dv, "dv"), 1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(score),
         None if plan is None else plan.buffer.data_ptr(), dtype, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _handle(stream, index))
+        workspace.numel() * workspace.element_size(), _raw_stream(index))
     if st != OK:
         raise OsattnError(st, "osattn_bwd_mod")
-    _keep(stream, index, (dq, dk, dv, drel, workspace, *held))
     return (dq, dk, dv) if drel is None else (dq, dk, dv, drel)
 
 
@@ -892,6 +954,10 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
         with torch.cuda.device(index):
             return tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask, scale, softcap, slopes,
                              window, out, lse, workspace, stream)
+    if _elsewhere_stream(stream, index):
+        return _under(stream, index, lambda: tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask, scale,
+                                                       softcap, slopes, window, out, lse, workspace),
+                      out, lse, workspace)
     dtype = _CODES.get(q.dtype)
     if dtype is None:
         raise TypeError("tensors must be bf16 or fp16")
@@ -922,10 +988,9 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
         _view_strides(v_pages, "v_pages"), _view_strides(out, "out"),
         1.0 / math.sqrt(d) if scale is None else scale, softcap,
         None if slopes is None else slopes.data_ptr(), int(window), dtype, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _handle(stream, index))
+        workspace.numel() * workspace.element_size(), _raw_stream(index))
     if st != OK:
         raise OsattnError(st, "osattn_tree_attn")
-    _keep(stream, index, (out, lse, workspace, page_table, ctx_len, tree_mask, slopes))
     return out, lse
 
 
