@@ -631,10 +631,21 @@ class MaskPlan:
     """Which keys each query row sees: what mask_plan() returns and fwd_mod()
     and bwd_mod() take.  `buffer` is private to the library."""
 
-    __slots__ = ("buffer", "B", "Nq", "Nkv", "q_offset")
+    __slots__ = ("buffer", "B", "Nq", "Nkv", "q_offset", "stream")
 
-    def __init__(self, buffer, B, Nq, Nkv, q_offset):
+    def __init__(self, buffer, B, Nq, Nkv, q_offset, stream=None):
         self.buffer, self.B, self.Nq, self.Nkv, self.q_offset = buffer, B, Nq, Nkv, q_offset
+        self.stream = stream  # the one whose memory the buffer is
+
+    def use(self, stream, index):
+        """The buffer's address, for work on `stream`, the current one of
+        device `index`: until that is done, the memory of a plan that is
+        dropped is not handed out again."""
+        if stream != self.stream:
+            import torch
+
+            self.buffer.record_stream(torch.cuda.current_stream(index))
+        return self.buffer.data_ptr()
 
 
 def _int32(t, shape, index, name):
@@ -703,25 +714,24 @@ def mask_plan(B: int, Nq: int, Nkv: int, causal: bool = False, window: int = 0, 
     key_len = _int32(key_len, (B,), index, "key_len")
     prefix_len = _int32(prefix_len, (B,), index, "prefix_len")
     doc_ids = _int32(doc_ids, (B, Nkv), index, "doc_ids")
+    handle = _raw_stream(index)
     if out is None:
         # tiles of 128 rows take 16 bytes each, rows 8
         need = max(B, 0) * ((max(Nq, 0) + 127) // 128 * 16 + max(Nq, 0) * 8)
-        buffer = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        plan = MaskPlan(torch.empty(max(need, 16), dtype=torch.uint8, device=device), B, Nq, Nkv, q_offset, handle)
     else:
-        buffer = out.buffer
-        if out.B != B or out.Nq != Nq or buffer.get_device() != index:
+        plan = out
+        if out.B != B or out.Nq != Nq or out.buffer.get_device() != index:
             raise ValueError("out must be a MaskPlan of the same B, Nq and device")
-    st = (_lib or lib()).osattn_mask_plan(buffer.data_ptr(), buffer.numel(), B, Nq, Nkv, q_offset,
+    st = (_lib or lib()).osattn_mask_plan(plan.use(handle, index), plan.buffer.numel(), B, Nq, Nkv, q_offset,
                                 1 if causal else 0, window,
                                 None if key_len is None else key_len.data_ptr(),
                                 None if prefix_len is None else prefix_len.data_ptr(),
-                                None if doc_ids is None else doc_ids.data_ptr(), _raw_stream(index))
+                                None if doc_ids is None else doc_ids.data_ptr(), handle)
     if st != OK:
         raise OsattnError(st, "osattn_mask_plan")
-    if out is not None:
-        out.Nkv, out.q_offset = Nkv, q_offset
-        return out
-    return MaskPlan(buffer, B, Nq, Nkv, q_offset)
+    plan.Nkv, plan.q_offset = Nkv, q_offset
+    return plan
 
 
 def rel_buckets(num_buckets: int, max_distance: int, bidirectional: bool = True):
@@ -836,11 +846,12 @@ def fwd_mod(q, k, v, scale: float | None = None, plan=None, softcap: float = 0.0
     elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index:
         raise ValueError("out must match q")
     lse = _lse(lse, (B, H, Nq), index, q)
+    handle = _raw_stream(index)
     st = (_lib or lib()).osattn_fwd_mod(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, Nkv, d,
         _view_strides(q, "q"), _view_strides(k, "k"), _view_strides(v, "v"), _view_strides(out, "out"),
         1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(score),
-        None if plan is None else plan.buffer.data_ptr(), dtype, _raw_stream(index))
+        None if plan is None else plan.use(handle, index), dtype, handle)
     if st != OK:
         raise OsattnError(st, "osattn_fwd_mod")
     return out, lse
@@ -900,14 +911,15 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
         workspace = q.new_empty(_bwd_mod_workspace(B, H, Nq, Nkv, score.rel_range), dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError("workspace must be contiguous on q's device")
+    handle = _raw_stream(index)
     st = L.osattn_bwd_mod(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if drel is None else drel.data_ptr(), B, H, Hkv,
         Nq, Nkv, d, _view_strides(q, "q"), _view_strides(k, "k"), _view_strides(v, "v"),
         _view_strides(o, "o"), _view_strides(do, "do"), _view_strides(dq, "dq"), _view_strides(dk, "dk"),
         _view_strides(dv, "dv"), 1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(score),
-        None if plan is None else plan.buffer.data_ptr(), dtype, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(index))
+        None if plan is None else plan.use(handle, index), dtype, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), handle)
     if st != OK:
         raise OsattnError(st, "osattn_bwd_mod")
     return (dq, dk, dv) if drel is None else (dq, dk, dv, drel)
