@@ -1543,7 +1543,7 @@ cudaError_t launch(const ModArgs& a, const BwdModMaps& m) {
   p.Nkv = a.Nkv;
   p.scale = a.scale;
   p.scale_log2 = a.scale * kModLog2e;
-  p.cap = make_cap(a.scale, a.softcap);
+  p.cap = make_cap(a.scale, a.softcap, kF16);
   p.slopes = a.slopes;
   p.rel = a.rel;
   p.rel_part = a.rel_part;

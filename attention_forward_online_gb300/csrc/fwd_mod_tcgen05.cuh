@@ -687,7 +687,7 @@ cudaError_t launch(const ModArgs& a, const CUtensorMap& q, const CUtensorMap& k,
   p.scale = positive_scale(a.scale);
   p.scale_log2 = p.scale * kModLog2e;
   p.neg_q = a.scale < 0.f ? kIdescNegA : 0u;
-  p.cap = make_cap(p.scale, a.softcap);
+  p.cap = make_cap(p.scale, a.softcap, kF16);
   p.slopes = a.slopes;
   p.rel = a.rel;
   p.q_offset = a.q_offset;

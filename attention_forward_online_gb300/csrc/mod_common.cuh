@@ -102,9 +102,17 @@ struct CapArgs {
   float inv2;             // 1 / cap2^2
   float k[4];
   float q[3];             // the same of degree 2, for |y / cap| <= 0.2, that is up to s_max / 2
-  float s_free;           // up to here, s_max / 2 at most, logits are within 15 (base 2): 2^x needs no max
+  float s_free;           // up to here, s_max / 2 at most, logits are within free_logits: 2^x needs no max
 };
-inline CapArgs make_cap(float scale, float softcap) {
+// Logits (base 2) of either sign that a tile may have to be formed against
+// free_max or any greater max instead of its own, so that P stays below 2^15 and
+// keeps the type's precision: bf16 has the exponents for 2^-15, but fp16 is at its
+// smallest normal value 2^-14 with it.  There a tile's 128 P of 2^-7 or more sum
+// to at least 1, as they do against their own max, and what is below fp16's
+// smallest step beside them is as small a part of the row.
+__host__ __device__ constexpr float free_logits(bool fp16) { return fp16 ? 11.f : 15.f; }
+__host__ __device__ constexpr float free_max(bool fp16) { return fp16 ? -4.f : 0.f; }
+inline CapArgs make_cap(float scale, float softcap, bool fp16) {
   CapArgs c{};
   if (!(softcap > 0.f)) return c;
   const double a = static_cast<double>(scale) / softcap;  // the tanh is odd: either sign
@@ -119,7 +127,8 @@ inline CapArgs make_cap(float scale, float softcap) {
   c.s_max = !ok ? -1.f : (size < low ? 65536.f : static_cast<float>(0.4 / size));
   const double t2[3] = {0.9999998948, -0.3332859090, 0.1301540755};
   const double unit = (scale < 0 ? -scale : scale) * 1.4426950408889634;  // logit of a score of 1
-  c.s_free = static_cast<float>(15.0 / unit < 0.5 * c.s_max ? 15.0 / unit : 0.5 * c.s_max);
+  const double free = free_logits(fp16) / unit;
+  c.s_free = static_cast<float>(free < 0.5 * c.s_max ? free : 0.5 * c.s_max);
   double pw = a;
   for (int n = 0; n < 4; ++n, pw *= a * a) {
     c.k[n] = ok ? static_cast<float>(cap2 * t[n] * pw) : 0.f;

@@ -188,11 +188,11 @@ struct TileScore {
     constexpr bool kFree = kShort && !kMasked && MODE == kModCap;
     load_row<kFree>(s_addr, v, top);
     if constexpr (kFree) {
-      // Scores so small that 2^x is safe against any max up to 2^15 off: no
-      // max, and the accumulator's factor (1, but for a max below 0 so far)
+      // Scores so small that the tile's own max is not needed (free_logits), and
+      // the accumulator's factor (1, but for a max below free_max so far) comes
       // before anything else.
       if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= cap->s_free)) {
-        const float m_new = fmaxf(m, 0.f);
+        const float m_new = fmaxf(m, free_max(kF16));
         publish(alpha_bits(m, m_new));
         const float sum = exps<false, true, 2>(s_addr, v, k, bits_of, -m_new);
         l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
