@@ -24,7 +24,8 @@
 // warp whose 32 rows hold no token only keeps the barriers' count: a decode
 // step fills a few rows of the 128); 8-11 rescale O; 12 and 14 TMA producers of
 // Q and K, and of V (lane x loads box x of a tile, a box lying in one page);
-// 13 MMA issue.  Tensor memory: S0, S1 (P in 16 bits over them), O0, O1.
+// 13 MMA issue; 15 what masks leave.  Tensor memory: S0, S1 (P in 16 bits over
+// them), O0, O1.
 //
 // Measured (bf16; "of measured": of this GPU type's copy rate, 6.78 TB/s):
 //   B64 H32 kv8 T1 ctx 4096 .. 8192 d128   258 to 265 us, 6.1 to 6.25 TB/s, 90 to
@@ -40,6 +41,7 @@
 //     its scores to its output, which units of one CTA do not overlap
 #pragma once
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -76,7 +78,8 @@ enum : uint32_t {
   kSiteO = 90,
   kSiteOEmpty = 91,
   kSiteMerge = 92,
-  kSiteZero = 93
+  kSiteZero = 93,
+  kSiteSeen = 94
 };
 
 template <int HD, int MODE>
@@ -101,6 +104,16 @@ struct Walk {
   bool head_cut, tail_cut;  // misses the unit's first or last tiles
 };
 
+// The keys of a sequence that some draft sees: the context from `first` on
+// (first = ctx: none of it) and the drafts whose bit is set.  Masks need not be
+// trees: a draft may be on no line, or a window away from all that name it, and
+// where no draft has depth 0 the window's first keys are nobody's.
+constexpr int kSeenSlots = 4;  // segments that seen_role may be ahead
+struct Seen {
+  unsigned long long drafts;
+  int first;
+};
+
 struct __align__(16) Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
@@ -111,8 +124,10 @@ struct __align__(16) Bars {
   uint64_t o_empty;        // 256 arrivals: the accumulators have been read
   uint64_t merge;          // 256 arrivals: both states of the segment are stored
   uint64_t mma_drain;
+  uint64_t seen_full[kSeenSlots], seen_empty[kSeenSlots];  // 1 and 128 arrivals a segment, if there are masks
   uint32_t tmem_base;
   int abort_flag;
+  Seen seen[kSeenSlots];  // of the segment's sequence
   Walk start;  // of this CTA's share, before its first segment
   int warp_sum[16];
   // Within a segment alpha_bits of the accumulator's rows, [accumulator][row];
@@ -204,6 +219,41 @@ __device__ __forceinline__ unsigned long long mask_of(const Params& p, int b, in
 // A draft's place behind the context: how many other drafts lie on its line.
 __device__ __forceinline__ int depth_of(unsigned long long mask) {
   return mask ? __popcll(mask) - 1 : 0;
+}
+
+// The whole warp calls it.
+__device__ __forceinline__ Seen seen_of(const Params& p, int b, int ctx) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long m0 = lane < p.T ? mask_of(p, b, lane) : 0ull;
+  unsigned long long m1 = lane + 32 < p.T ? mask_of(p, b, lane + 32) : 0ull;
+  const int d0 = depth_of(m0), d1 = depth_of(m1);
+  // (a draft that sees any draft sees the context)
+  const int least = __reduce_min_sync(0xffffffffu, min(m0 ? d0 : INT_MAX, m1 ? d1 : INT_MAX));
+  if (p.window > 0 && p.T > p.window) {
+#pragma unroll 1
+    for (int u = 0; u < p.T; ++u) {
+      const int d = __shfl_sync(0xffffffffu, u < 32 ? d0 : d1, u & 31);
+      if (abs(d0 - d) >= p.window) m0 &= ~(1ull << u);
+      if (abs(d1 - d) >= p.window) m1 &= ~(1ull << u);
+    }
+  }
+  m0 |= m1;
+  const unsigned lo = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(m0));
+  const unsigned hi = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(m0 >> 32));
+  Seen s;
+  s.drafts = static_cast<unsigned long long>(hi) << 32 | lo;
+  s.first = least == INT_MAX ? ctx : (p.window > 0 ? min(max(0, ctx + least - p.window + 1), ctx) : 0);
+  return s;
+}
+__device__ __forceinline__ bool key_seen(const Seen& s, int ctx, int key) {
+  const int u = key - ctx;
+  return u < 0 ? key >= s.first : u < 64 && ((s.drafts >> u) & 1ull) != 0ull;
+}
+// Whether some draft sees one of the keys [key, key + n), n >= 1.
+__device__ __forceinline__ bool any_seen(const Seen& s, int ctx, int key, int n) {
+  if (key < ctx && s.first < ctx && key + n > s.first) return true;
+  const int from = max(key - ctx, 0), to = min(key + n - ctx, 64);
+  return from < to && ((s.drafts >> from) & (~0ull >> (64 - (to - from)))) != 0ull;
 }
 
 // Whether the slopes of a key head's query heads all go through the MMA step.
@@ -446,27 +496,21 @@ __device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uin
   const int quarter = warp & 3;
   const int row = quarter * 32 + lane;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-  uint32_t a_phase[2] = {0, 0}, vc = 0;  // vc: V tiles so far
+  uint32_t a_phase[2] = {0, 0}, vc = 0, seg = 0;  // vc: V tiles so far
   bool ok = true;
-  for (Walk w = bars->start; ok && walk_next(p, w);) {
-    // Drafts that some draft sees; the rows of V of the others, like those of
-    // keys before the window and behind the drafts, are zeroed below.
-    unsigned long long seen = 0ull;
-    int seen_for = -1;
+  for (Walk w = bars->start; ok && walk_next(p, w); ++seg) {
+    // The rows of V of keys that no draft sees are zeroed below.
     for (int i = 0; ok && i < w.n; ++i, ++vc) {
       const int t = i & 1;
       const int k0 = (w.tile0 + i) * BN;
       const int lo = first_key(p, w.ctx);
-      if (k0 < lo || k0 + BN > w.ctx) {
-        if (seen_for != w.b) {
-          for (int u = 0; u < p.T; ++u) seen |= mask_of(p, w.b, u);
-          seen_for = w.b;
-        }
-        ok = mbar_wait(&bars->v_full[vc % C::kVSlots], (vc / C::kVSlots) & 1u, wc, kSiteZero);
+      if (k0 < lo || k0 + BN > w.ctx || (p.mask && tile_masked(p, w.ctx, k0))) {
+        if (p.mask) ok = mbar_wait(&bars->seen_full[seg % kSeenSlots], seg / kSeenSlots & 1u, wc, kSiteSeen);
+        if (ok) ok = mbar_wait(&bars->v_full[vc % C::kVSlots], (vc / C::kVSlots) & 1u, wc, kSiteZero);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int u = k0 + row - w.ctx;
-        if (k0 + row < lo || (u >= 0 && (u >= p.T || !((seen >> u) & 1ull)))) {
+        // (a chain's drafts see themselves, and the first has depth 0)
+        if (!key_seen(p.mask ? bars->seen[seg % kSeenSlots] : Seen{draft_bits(p.T), lo}, w.ctx, k0 + row)) {
           uint8_t* v = sV + (vc % C::kVSlots) * C::kTileBytes + row * 128;
 #pragma unroll
           for (int cb = 0; cb < HD / 64; ++cb)
@@ -507,14 +551,50 @@ __device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uin
       tc_fence_before_sync();
       mbar_arrive(&bars->p_full[t]);
     }
+    if (p.mask && ok) {  // (waited for in every segment: the phases stay in step)
+      ok = warp_wait(&bars->seen_full[seg % kSeenSlots], seg / kSeenSlots & 1u, wc, kSiteSeen);
+      mbar_arrive(&bars->seen_empty[seg % kSeenSlots]);
+    }
+  }
+}
+
+// One warp, where there are masks: what the drafts of each segment's sequence see,
+// and the status for pages that do not exist but hold a key that some draft sees.
+// A warp of its own, some segments ahead: in the producers or the correction warps
+// this costs registers and code (one token over 700 keys, without masks, 12.5 ->
+// 13.2 us), and waiting for each segment's end it takes issue slots from the
+// softmax (8 trees of 27 drafts over 6000 keys 57.6 -> 60.4 us; without masks'
+// leavings, which let NaN from unseen keys through, 56).
+__device__ __forceinline__ void seen_role(const Params& p, Bars* bars, WaitCtl wc) {
+  if (!p.mask) return;
+  const int lane = threadIdx.x & 31;
+  uint32_t seg = 0;
+  bool ok = true;
+  for (Walk w = bars->start; ok && walk_next(p, w); ++seg) {
+    const Seen s = seen_of(p, w.b, w.ctx);
+    const uint32_t slot = seg % kSeenSlots;
+    if (seg >= kSeenSlots) ok = warp_wait(&bars->seen_empty[slot], (seg / kSeenSlots - 1) & 1u, wc, kSiteSeen);
+    if (!ok) break;
+    if (lane == 0) {
+      bars->seen[slot] = s;
+      mbar_arrive(&bars->seen_full[slot]);
+    }
+    __syncwarp();
+    const int last = min((w.tile0 + w.n) * BN, w.ctx + p.T) - 1;
+    for (int at = w.tile0 * BN / p.page + lane; at <= last / p.page; at += 32)
+      if (any_seen(s, w.ctx, at * p.page, p.page)) {
+        const int page = __ldg(p.table + static_cast<long long>(w.b) * p.max_pages + at);
+        if (page < 0 || page >= p.num_pages) atomicMax(p.status, kBadArg);
+      }
+    __syncwarp();
   }
 }
 
 // ------------------------------------------------------------------ producers
 // One warp loads Q and K, another V; lane x loads box x of each tile.  A box
-// that holds no visible key, or whose page number is not one of the pool's, is
-// read from behind the pool, which fills it with zeros; the latter also sets
-// the status.
+// before every window or behind the drafts, or whose page number is not one of
+// the pool's, is read from behind the pool, which fills it with zeros; the latter
+// also sets the status (with masks seen_role does, which knows what they leave).
 template <int HD, bool kF16, int MODE, bool kV>
 __device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmKV, const Params& p,
                                               Bars* bars, uint8_t* sQ, uint8_t* ring, uint8_t* slopes,
@@ -557,17 +637,15 @@ __device__ __forceinline__ void producer_role(const CUtensorMap* tmQ, const CUte
     for (int i = 0; ok && i < w.n; ++i) {
       const int s = static_cast<int>(n % kSlots);
       const uint32_t use = n / kSlots;
+      const int key = (w.tile0 + i) * BN + lane * p.box_rows;
       int page = p.num_pages, in_page = 0;
-      if (lane < boxes) {
-        const int key = (w.tile0 + i) * BN + lane * p.box_rows;
-        if (key < end && key + p.box_rows > lo) {
-          const int at = key / p.page;  // < max_pages: ctx + T fits the table
-          in_page = key - at * p.page;
-          page = __ldg(p.table + static_cast<long long>(w.b) * p.max_pages + at);
-          if (page < 0 || page >= p.num_pages) {
-            page = p.num_pages;
-            atomicMax(p.status, kBadArg);
-          }
+      if (lane < boxes && key < end && key + p.box_rows > lo) {
+        const int at = key / p.page;  // < max_pages: ctx + T fits the table
+        in_page = key - at * p.page;
+        page = __ldg(p.table + static_cast<long long>(w.b) * p.max_pages + at);
+        if (page < 0 || page >= p.num_pages) {
+          page = p.num_pages;
+          if (!p.mask) atomicMax(p.status, kBadArg);
         }
       }
       if (use > 0) ok = warp_wait(&empty[s], (use - 1) & 1u, wc, kV ? kSiteVEmpty : kSiteKEmpty);
@@ -756,6 +834,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->o_empty, 256);
     mbar_init(&bars->merge, 256);
     mbar_init(&bars->mma_drain, 1);
+    for (int s = 0; s < kSeenSlots; ++s) {
+      mbar_init(&bars->seen_full[s], 1);
+      mbar_init(&bars->seen_empty[s], 128);
+    }
     bars->abort_flag = 0;
     fence_barrier_init();
   }
@@ -801,6 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       producer_role<HD, kF16, MODE, true>(&tmQ, &tmV, p, bars, sQ, sV, slopes, wc);
     else if (warp == kMmaWarp)
       mma_role<HD, kF16, MODE>(p, bars, tmem, sQ, sK, sV, slopes, wc);
+    else
+      seen_role(p, bars, wc);
   }
 
   __syncwarp();
