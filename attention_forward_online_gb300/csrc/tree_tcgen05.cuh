@@ -216,10 +216,9 @@ __device__ __forceinline__ unsigned long long mask_of(const Params& p, int b, in
   return static_cast<unsigned long long>(__ldg(p.mask + static_cast<long long>(b) * p.T + t)) &
          draft_bits(p.T);
 }
-// A draft's place behind the context: how many other drafts lie on its line.
-__device__ __forceinline__ int depth_of(unsigned long long mask) {
-  return mask ? __popcll(mask) - 1 : 0;
-}
+// A draft's place behind the context (of a tree: how many other drafts lie on its
+// line).  A draft with an empty mask, which others may see, has -1.
+__device__ __forceinline__ int depth_of(unsigned long long mask) { return __popcll(mask) - 1; }
 
 // The whole warp calls it.
 __device__ __forceinline__ Seen seen_of(const Params& p, int b, int ctx) {
@@ -229,7 +228,7 @@ __device__ __forceinline__ Seen seen_of(const Params& p, int b, int ctx) {
   const int d0 = depth_of(m0), d1 = depth_of(m1);
   // (a draft that sees any draft sees the context)
   const int least = __reduce_min_sync(0xffffffffu, min(m0 ? d0 : INT_MAX, m1 ? d1 : INT_MAX));
-  if (p.window > 0 && p.T > p.window) {
+  if (p.window > 0 && p.T >= p.window) {
 #pragma unroll 1
     for (int u = 0; u < p.T; ++u) {
       const int d = __shfl_sync(0xffffffffu, u < 32 ? d0 : d1, u & 31);
@@ -328,7 +327,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
     // are a window away
     auto row_mask = [&](int b) {
       unsigned long long mask = live ? mask_of(p, b, tok) : 0ull;
-      if (p.window > 0 && p.T > p.window) {
+      if (p.window > 0 && p.T >= p.window) {  // (depths are -1 .. T - 1)
         const int depth = depth_of(mask);
         for (int u = 0; u < p.T; ++u)
           if (((mask >> u) & 1) && abs(depth - depth_of(mask_of(p, b, u))) >= p.window) mask &= ~(1ull << u);

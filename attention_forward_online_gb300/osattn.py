@@ -947,8 +947,8 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
     set iff draft t sees draft u (None: u <= t; 0: padding, O = 0, LSE = -inf).
 
     softcap and slopes (fp32 [H]) as in fwd_mod(), with a window keys at a
-    distance of at least `window` are hidden; a draft stands behind the
-    context by the number of other drafts it sees."""
+    distance of at least `window` are hidden; draft t stands at ctx_len +
+    (bits of its mask) - 1, which for a tree is its depth behind the context."""
     if q.dim() != 4 or k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("q must be [B, H, T, d], k_pages and v_pages [pages, Hkv, page_size, d]")
     B, H, T, d = q.shape

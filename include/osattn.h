@@ -579,9 +579,9 @@ int osattn_bwd_mod(const void* Q, const void* K, const void* V, const void* O, c
  * the whole context besides.
  *
  * Positions, for the window and the slopes: a cached key stands at its index,
- * draft t at ctx_len[b] + (bits of its mask) - 1.  With y the scaled score,
- * capped as in osattn_score, and dist = |position of the query less that of
- * the key|:
+ * draft t at ctx_len[b] + (bits of its mask) - 1 (padding too, for a draft that
+ * sees it).  With y the scaled score, capped as in osattn_score, and dist =
+ * |position of the query less that of the key|:
  *   y = y - slopes[h] * dist;  key visible only if dist < window (window > 0)
  * O and LSE as for osattn_fwd_mod, head h reading key head h / (H / Hkv).
  *
