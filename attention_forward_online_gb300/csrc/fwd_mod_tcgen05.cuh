@@ -254,9 +254,9 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap* tmO, const Param
     TileMask mk;
     if (masked) {
       mk.classify(bits_of);
-      ts.template tile<true, true>(s_addr, mk, bits_of, ts.by_place(), m, l, publish);
+      ts.template tile<true, true, false>(s_addr, mk, bits_of, ts.by_place(), m, l, publish);
     } else {
-      ts.template tile<false, true>(s_addr, mk, bits_of, ts.by_place(), m, l, publish);
+      ts.template tile<false, true, false>(s_addr, mk, bits_of, ts.by_place(), m, l, publish);
     }
     tmem_st_wait();
     tc_fence_before_sync();

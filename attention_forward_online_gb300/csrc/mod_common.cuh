@@ -83,9 +83,12 @@ __device__ __forceinline__ void fence_proxy_async() {
 
 // Capped scores: with E = e^{2 y / cap} and r = 1 / (1 + E),
 // tanh(y / cap) = 1 - 2 r, so cap tanh(y / cap) = cap - 2 cap r.  One ex2 and
-// one reciprocal; the error of r (about 2^-23 relative, r <= 1) moves the
-// logit by at most 2 cap 2^-23, 1e-5 at cap 50, while the one-instruction
-// tanh (relative error 2^-11) would move it by 0.02.  E = inf gives r = 0.
+// one reciprocal.  E is off by 2^-22 relative and the rounding of its exponent
+// (2^-24 of at most 30), which moves r by a fourth of that at most; 1 + E, the
+// reciprocal and, where four scores share one, four products add 2^-21 of r: in
+// all below 2^-20 of the cap (seen: 2^-22), whatever the score.  That is 5e-5 in
+// a logit at cap 50, where the one-instruction tanh (relative error 2^-11) would
+// move it by 0.02.  E = inf gives r = 0.
 // c1 = 2 scale log2(e) / cap.
 __device__ __forceinline__ float cap_r(float s, float c1) { return rcp_approx(1.f + ex2_approx(s * c1)); }
 
@@ -102,6 +105,7 @@ struct CapArgs {
   float inv2;             // 1 / cap2^2
   float k[4];
   float q[3];             // the same of degree 2, for |y / cap| <= 0.2, that is up to s_max / 2
+  bool large;             // the cap is above 64
   float s_free;           // up to here, s_max / 2 at most, logits are within free_logits: 2^x needs no max
 };
 // Logits (base 2) of either sign that a tile may have to be formed against
@@ -116,6 +120,7 @@ inline CapArgs make_cap(float scale, float softcap, bool fp16) {
   CapArgs c{};
   if (!(softcap > 0.f)) return c;
   const double a = static_cast<double>(scale) / softcap;  // the tanh is odd: either sign
+  c.large = softcap > 64.f;
   const double cap2 = static_cast<double>(softcap) * 1.4426950408889634;
   const double c1 = 2.0 * a * 1.4426950408889634;
   c.c1 = static_cast<float>(c1 > 3e38 ? 3e38 : c1 < -3e38 ? -3e38 : c1);

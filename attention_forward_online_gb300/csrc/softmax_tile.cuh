@@ -106,6 +106,8 @@ __device__ __forceinline__ float chunk_min(const Chunk& v) {
   return fminf(fmin3(a[0], a[1], a[2]), a[3]);
 }
 
+__device__ __forceinline__ float chunk_absmax(const Chunk& v) { return fmaxf(chunk_max(v), -chunk_min(v)); }
+
 // Bits [from, to) of 32, for any from and to.
 __device__ __forceinline__ uint32_t bit_range(int from, int to) {
   const int a = min(max(from, 0), 32), b = min(max(to, 0), 32);
@@ -180,13 +182,15 @@ struct TileScore {
   // kMasked: some rows of the warp may not see all of the tile.
   // kShort: with a shorter way for small capped scores (its code costs kernels
   // of few tiles 2 us).
-  template <bool kMasked, bool kShort, typename BitsOf, typename Gap, typename Publish>
-  __device__ __forceinline__ void tile(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
+  // kDirectOnly: without code for tiles whose logits have to be formed before
+  // their max; false for such a tile, with nothing done.
+  template <bool kMasked, bool kShort, bool kDirectOnly, typename BitsOf, typename Gap, typename Publish>
+  __device__ __forceinline__ bool tile(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
                                        float& m, float& l, Publish&& publish) const {
     Row v;
     float top[kChunks];
     constexpr bool kFree = kShort && !kMasked && MODE == kModCap;
-    load_row<kFree>(s_addr, v, top);
+    load_row<kFree || MODE == kModCapSlopes>(s_addr, v, top);
     if constexpr (kFree) {
       // Scores so small that the tile's own max is not needed (free_logits), and
       // the accumulator's factor (1, but for a max below free_max so far) comes
@@ -197,7 +201,7 @@ struct TileScore {
         const float sum = exps<false, true, 2>(s_addr, v, k, bits_of, -m_new);
         l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
         m = m_new;
-        return;
+        return true;
       }
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) top[ch] = chunk_max(v[ch]);
@@ -209,9 +213,14 @@ struct TileScore {
       for (int ch = 0; ch < kChunks; ++ch) {
         if ((k.partial >> ch) & 1u) {
           const uint32_t bits = bits_of(ch);
-          mask_chunk(v[ch], bits, kMinusInf);
-          top[ch] = chunk_max(v[ch]);
-          if constexpr (mode_cap(MODE)) mask_chunk(v[ch], bits, 0u);
+          if constexpr (MODE == kModCapSlopes) {
+            mask_chunk(v[ch], bits, 0u);
+            top[ch] = chunk_absmax(v[ch]);
+          } else {
+            mask_chunk(v[ch], bits, kMinusInf);
+            top[ch] = chunk_max(v[ch]);
+            if constexpr (mode_cap(MODE)) mask_chunk(v[ch], bits, 0u);
+          }
         }
         if ((k.none >> ch) & 1u) {
           top[ch] = -INFINITY;
@@ -232,8 +241,9 @@ struct TileScore {
     if constexpr (MODE == kModSlopes) direct = !both_sides;
     if constexpr (MODE == kModCapSlopes) direct = false;
     if constexpr (mode_rel(MODE)) direct = strip == nullptr;
+    if (kDirectOnly && !direct) return false;
     float m_new, sum;
-    if (direct) {
+    if (kDirectOnly || direct) {
       m_new = next_max(m, best_raw == -INFINITY ? -INFINITY : raw(best_raw) + off);
       publish(alpha_bits(m, m_new));
       // a row with no key so far has m_new = -inf and every x = -inf: against
@@ -247,7 +257,7 @@ struct TileScore {
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) {
         if (kMasked && ((k.none >> ch) & 1u)) continue;
-        logits(v[ch], ch, gap);
+        logits(v[ch], ch, gap, MODE == kModCapSlopes && small_scores(top[ch]));
         if (kMasked && mode_cap(MODE) && ((k.partial >> ch) & 1u)) mask_chunk(v[ch], bits_of(ch), kMinusInf);
         if (!bound) best = fmaxf(best, chunk_max(v[ch]));
       }
@@ -257,6 +267,7 @@ struct TileScore {
     }
     l = fmaf(l, m_new == m ? 1.f : ex2_approx(m - m_new), sum);
     m = m_new;
+    return true;
   }
 
   // The same for a masked tile by a rolled loop that reads each chunk from
@@ -264,7 +275,10 @@ struct TileScore {
   // meets once or twice, whose code then comes from far (a tree of 27 drafts
   // over 6000 keys: 50 us against 57; a prompt's many masked tiles would be 10
   // to 25 % slower).
-  template <typename BitsOf, typename Gap, typename Publish>
+  // kFine: with the cap's polynomial where a chunk's scores are small, for caps
+  // above 64: the other form is off by up to 2^-20 of the cap, 6e-5 at a cap of 64.
+  // (Its code costs: with it for all caps that tree, cap 30, takes 3 us more.)
+  template <bool kFine, typename BitsOf, typename Gap, typename Publish>
   __device__ __forceinline__ void tile_rolled(uint32_t s_addr, const TileMask& k, BitsOf&& bits_of, Gap&& gap,
                                               float& m, float& l, Publish&& publish) const {
     auto load = [&](int ch, Chunk& v) {
@@ -272,8 +286,12 @@ struct TileScore {
       tmem_ld_wait();
       reg_fence32(v);
       const uint32_t bits = bits_of(ch);
-      if constexpr (mode_cap(MODE)) mask_chunk(v, bits, 0u);
-      logits(v, ch, gap);
+      bool small = false;
+      if constexpr (mode_cap(MODE)) {
+        mask_chunk(v, bits, 0u);
+        if constexpr (kFine) small = small_scores(chunk_absmax(v));
+      }
+      logits(v, ch, gap, small);
       mask_chunk(v, bits, kMinusInf);
     };
     float best = -INFINITY;
@@ -314,10 +332,20 @@ struct TileScore {
     m = m_new;
   }
 
+  // Whether the cap's polynomial serves all of the warp's rows; size: the greatest
+  // magnitude of the row's scores.
+  __device__ __forceinline__ bool small_scores(float size) const {
+    return __all_sync(0xffffffffu, size <= cap->s_max);
+  }
+
   // x in place of the 32 scores of chunk ch, less the constant part of the bias.
+  // small: small_scores of the chunk.
   template <typename Gap>
-  __device__ __forceinline__ void logits(Chunk& v, int ch, Gap&& gap) const {
-    if constexpr (mode_cap(MODE)) {
+  __device__ __forceinline__ void logits(Chunk& v, int ch, Gap&& gap, bool small) const {
+    if (mode_cap(MODE) && small) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) set_pair(v, e, cap_pair<3>(pair_of(v, e), 0ull));
+    } else if constexpr (mode_cap(MODE)) {
       // cap2 - 2 cap2 / (1 + E): one reciprocal for four scores, 1 + E kept
       // below 2^30 so that four multiply without overflow (the tanh is 1 to
       // the last bit long before)
@@ -364,22 +392,26 @@ struct TileScore {
     }
   }
 
-  // x + n of two raw scores (direct tiles); n2: n twice, with off in it.
+  // cap2 tanh(s |scale| / cap) + n of two scores by the polynomial (n2: n twice).
   template <int kDegree>
-  __device__ __forceinline__ uint64_t direct_pair(uint64_t s, uint64_t n2) const {
-    if constexpr (MODE == kModCap && kDegree == 2) {
-      const uint64_t u = f2_mul(s, s);
+  __device__ __forceinline__ uint64_t cap_pair(uint64_t s, uint64_t n2) const {
+    const uint64_t u = f2_mul(s, s);
+    if constexpr (kDegree == 2) {
       const uint64_t k0 = f2_pack(cap->q[0], cap->q[0]), k1 = f2_pack(cap->q[1], cap->q[1]),
                      k2 = f2_pack(cap->q[2], cap->q[2]);
       return f2_fma(f2_fma(f2_fma(k2, u, k1), u, k0), s, n2);
-    } else if constexpr (MODE == kModCap) {
-      const uint64_t u = f2_mul(s, s);
+    } else {
       const uint64_t k0 = f2_pack(cap->k[0], cap->k[0]), k1 = f2_pack(cap->k[1], cap->k[1]),
                      k2 = f2_pack(cap->k[2], cap->k[2]), k3 = f2_pack(cap->k[3], cap->k[3]);
       return f2_fma(f2_fma(f2_fma(f2_fma(k3, u, k2), u, k1), u, k0), s, n2);
-    } else {
-      return f2_fma(s, f2_pack(c, c), n2);
     }
+  }
+
+  // x + n of two raw scores (direct tiles); n2: n twice, with off in it.
+  template <int kDegree>
+  __device__ __forceinline__ uint64_t direct_pair(uint64_t s, uint64_t n2) const {
+    if constexpr (MODE == kModCap) return cap_pair<kDegree>(s, n2);
+    else return f2_fma(s, f2_pack(c, c), n2);
   }
 
   // P in 16 bits over the first 64 columns of the row's scores, and the sum:

@@ -377,8 +377,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
         ts.both_sides = !linear || masked;
         ts.off = ts.both_sides ? 0.f : ts.slope2 * ts.d0;
       }
+      // Tiles that every row sees, where one pass does; the others by the rolled loop.
       TileMask mk;
-      if (masked) {
+      bool done = false;
+      if (!masked)
+        done = ts.template tile<false, false, MODE != kModCapSlopes>(s_addr, mk, [](int) { return 0xffffffffu; },
+                                                                     ts.by_place(), m, l, publish);
+      if (!done) {
         const unsigned long long mask = tail ? row_mask(at.b) : 0ull;
         // visible keys of a chunk: context keys [lo, ctx), then the mask
         auto bits_of = [&](int ch) {
@@ -408,9 +413,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Bars* bars, uint32
             return e < before ? first + static_cast<float>(e) : at;
           };
         };
-        ts.tile_rolled(s_addr, mk, bits_of, gap, m, l, publish);
-      } else {
-        ts.template tile<false, false>(s_addr, mk, [](int) { return 0xffffffffu; }, ts.by_place(), m, l, publish);
+        if (mode_cap(MODE) && p.cap.large)
+          ts.template tile_rolled<true>(s_addr, mk, bits_of, gap, m, l, publish);
+        else
+          ts.template tile_rolled<false>(s_addr, mk, bits_of, gap, m, l, publish);
       }
       tmem_st_wait();
       tc_fence_before_sync();

@@ -491,8 +491,9 @@ int osattn_mask_plan(void* plan, size_t plan_bytes, int B, int Nq, int Nkv, int 
  *   y = y + rel_table[rel_map[clamp(j - p, -R, R) + R]][h]  (rel_table), R = rel_range
  * slopes and rel_table exclude each other (OSATTN_ERR_INVALID_ARG); softcap
  * with rel_table is OSATTN_ERR_UNSUPPORTED.  Capped scores are computed to
- * about 2^-22 softcap, and to 2^-22 relative where all scores around them
- * (those of 32 rows and a tile of keys) are below 0.4 softcap.
+ * 2^-20 softcap, and to 2^-22 relative where all scores around them (those of
+ * 32 rows and a tile of keys) are below 0.4 softcap (osattn_tree_attn: with
+ * softcap above 64).
  */
 typedef struct osattn_score {
   float softcap;          /* 0: no cap; else 0.001 .. 10000 (others: OSATTN_ERR_INVALID_ARG) */
