@@ -183,7 +183,11 @@ __device__ __forceinline__ void mma_abt_id(uint32_t d_tmem, uint64_t a_desc, uin
 // so do all row groups where every query row is alike.
 constexpr int kSlopeQBytes = 128;       // alike query rows: one core matrix
 constexpr int kSlopeRowsBytes = 128 * 16;  // 128 different rows, of queries or keys
-constexpr float kSlopeMax = 16384.f;    // |slope / scale| beyond: score by score
+// Beyond either: score by score.  The sum s + (slope / scale) e is rounded to fp32
+// before the constant is taken off, an error of 2^-23 of 128 |slope| in the logit of
+// a key beside its query: 2e-5 at slope 1, where the common slopes end, but 1e-3 at
+// 32.  (The quotient's pieces have to fit fp16.)
+constexpr float kSlopeMax = 1.f, kSlopeScaledMax = 16384.f;
 
 // Descriptor of rows of 8 elements read twice; sbo: to the next 8 rows.
 __device__ __forceinline__ uint64_t sdesc_plain(uint32_t smem_addr, uint32_t sbo) {
@@ -197,7 +201,7 @@ __device__ __forceinline__ uint64_t slope_q_desc(uint32_t at) { return sdesc_pla
 __device__ __forceinline__ uint64_t slope_rows_desc(uint32_t at) { return sdesc_plain(at, 128); }
 
 __device__ __forceinline__ bool slope_linear(float slope, float scale) {
-  return fabsf(slope / scale) <= kSlopeMax;
+  return fabsf(slope) <= kSlopeMax && fabsf(slope / scale) <= kSlopeScaledMax;
 }
 
 template <bool kF16>

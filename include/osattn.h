@@ -493,7 +493,8 @@ int osattn_mask_plan(void* plan, size_t plan_bytes, int B, int Nq, int Nkv, int 
  * with rel_table is OSATTN_ERR_UNSUPPORTED.  Capped scores are computed to
  * 2^-20 softcap, and to 2^-22 relative where all scores around them (those of
  * 32 rows and a tile of keys) are below 0.4 softcap (osattn_tree_attn: with
- * softcap above 64).
+ * softcap above 64).  Slopes are applied in fp32, those up to 1 in magnitude
+ * with an error of up to 5e-5 of the slope in a logit.
  */
 typedef struct osattn_score {
   float softcap;          /* 0: no cap; else 0.001 .. 10000 (others: OSATTN_ERR_INVALID_ARG) */
