@@ -21,8 +21,8 @@
 //                added by atomics: results do not depend on the order of CTAs.
 //                Where key tiles are few, a cluster of 2, 4 or 8 CTAs shares
 //                one's (head, query tile) pairs and adds its fp32 sums through
-//                distributed shared memory in rank order (B1 H8 kv2 1078 d64
-//                capped: whole step 120 -> 73 us).
+//                distributed shared memory in rank order (dkdv_split.h; B1 H8 kv2
+//                1078 d64 capped, no mask: whole step 173 -> 84 us).
 //                With a learned bias also the sums of dY by distance, here and
 //                not in dq_kernel since there is shared memory to spare (there
 //                it cost a K slot, 0.35 us a tile at d = 128).
@@ -62,6 +62,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "dkdv_split.h"
 #include "mod_common.cuh"
 #include "mod_internal.h"
 #include "sm100_ptx.cuh"
@@ -1444,23 +1445,6 @@ __global__ void __launch_bounds__(1024) rel_reduce_kernel(const float* __restric
     if (lane == 0)
       out[static_cast<long long>(k) * H + h] = static_cast<uint16_t>(pack2<kF16>(v, 0.f) & 0xffffu);
   }
-}
-
-// CTAs that share a key tile's (head, query tile) pairs, of which it has at
-// most `pairs`, as a power of two: one that divides `of`, leaves a CTA two
-// pairs, and makes the kernel shortest if a CTA takes 1 / s of a tile's time
-// and a quarter of it besides, and the SMs take the CTAs in rounds.  Whole
-// steps, without / with: 18 key tiles, B1 H8 kv2 1078 d64, 120 / 73 us (8 CTAs
-// each); 24 tiles of a group of 4, B2 H8 kv2 1530 learned bias, 183 / 130 us (4);
-// but 96 tiles, B1 H4 2967 d128, 112 / 122 us with 4, so they stay whole.
-inline int dkdv_split(long long units, int num_sms, long long pairs, int of) {
-  int best = 0;
-  double cost = 0.0;
-  for (int n = 0; n == 0 || (n <= 3 && of % (1 << n) == 0 && (2 << n) <= pairs); ++n) {
-    const double c = static_cast<double>(((units << n) + num_sms - 1) / num_sms) * (1.0 / (1 << n) + 0.25);
-    if (n == 0 || c < cost) best = n, cost = c;
-  }
-  return best;
 }
 
 // The setmaxnreg split hands out exactly 384 x 168 registers; a build with
