@@ -764,8 +764,8 @@ def _mod_shapes(q, k, v):
     Hkv, Nkv = k.shape[1], k.shape[2]
     if k.shape != (B, Hkv, Nkv, d) or v.shape != k.shape:
         raise ValueError("k and v must be [B, Hkv, Nkv, d] matching q")
-    if Hkv < 1 or H % Hkv:
-        raise ValueError("the number of key/value heads must divide the number of query heads")
+    if H < 1 or Hkv < 1 or H % Hkv or d < 1:
+        raise ValueError("there must be heads, those of k and v dividing those of q, and d of at least 1")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must share one dtype")
     if not q.is_cuda:
@@ -889,6 +889,8 @@ def bwd_mod(q, k, v, o, lse, do, scale: float | None = None, plan=None, softcap:
     for t in (o, do):
         if t.shape != q.shape or t.dtype != q.dtype or t.get_device() != index:
             raise ValueError("o and do must be shaped, typed and placed like q")
+    if lse is None:
+        raise ValueError("lse must be the one that fwd_mod() returned")
     _lse(lse, (B, H, Nq), index, None)
     score, held = _score(q, plan, index, H, B, Nq, Nkv, softcap, slopes, rel_table, rel_map)
 
@@ -953,8 +955,8 @@ def tree_attn(q, k_pages, v_pages, page_table, ctx_len, tree_mask=None, scale: f
         raise ValueError("q must be [B, H, T, d], k_pages and v_pages [pages, Hkv, page_size, d]")
     B, H, T, d = q.shape
     pages, Hkv, page_size, dk = k_pages.shape
-    if dk != d or Hkv < 1 or H % Hkv:
-        raise ValueError("k_pages must have q's d and a number of heads that divides q's")
+    if dk != d or H < 1 or Hkv < 1 or H % Hkv or d < 1:
+        raise ValueError("k_pages must have q's d and a number of heads that divides q's, none of them 0")
     if k_pages.dtype != q.dtype or v_pages.dtype != q.dtype:
         raise TypeError("q, k_pages, v_pages must share one dtype")
     index = q.get_device()
