@@ -191,7 +191,7 @@ def _elsewhere_stream(stream, index):
     `index`."""
     if stream is None or stream.cuda_stream == _raw_stream(index):
         return False
-    if stream.device_index != index:
+    if getattr(stream, "device_index", index) != index:
         raise ValueError("stream is on another device than the tensors")
     return True
 
@@ -206,6 +206,8 @@ def _under(stream, index, call, *given):
     import torch
 
     caller = torch.cuda.current_stream(index)
+    if not hasattr(stream, "device_index"):  # another library's, known by its handle
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=index)
     with torch.cuda.stream(stream):
         results = call()
     for t in results if isinstance(results, tuple) else (results,):
