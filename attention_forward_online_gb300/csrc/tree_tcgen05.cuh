@@ -510,12 +510,17 @@ __device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uin
       const int k0 = (w.tile0 + i) * BN;
       const int lo = first_key(p, w.ctx);
       if (k0 < lo || k0 + BN > w.ctx || (p.mask && tile_masked(p, w.ctx, k0))) {
-        if (p.mask) ok = mbar_wait(&bars->seen_full[seg % kSeenSlots], seg / kSeenSlots & 1u, wc, kSiteSeen);
-        if (ok) ok = mbar_wait(&bars->v_full[vc % C::kVSlots], (vc / C::kVSlots) & 1u, wc, kSiteZero);
+        ok = mbar_wait(&bars->v_full[vc % C::kVSlots], (vc / C::kVSlots) & 1u, wc, kSiteZero);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         // (a chain's drafts see themselves, and the first has depth 0)
-        if (!key_seen(p.mask ? bars->seen[seg % kSeenSlots] : Seen{draft_bits(p.T), lo}, w.ctx, k0 + row)) {
+        bool hidden = k0 + row < lo || k0 + row >= w.ctx + p.T;
+        if (p.mask) {
+          ok = warp_wait(&bars->seen_full[seg % kSeenSlots], seg / kSeenSlots & 1u, wc, kSiteSeen);
+          if (!ok) break;
+          hidden = !key_seen(bars->seen[seg % kSeenSlots], w.ctx, k0 + row);
+        }
+        if (hidden) {
           uint8_t* v = sV + (vc % C::kVSlots) * C::kTileBytes + row * 128;
 #pragma unroll
           for (int cb = 0; cb < HD / 64; ++cb)
