@@ -47,13 +47,15 @@
 // What bounds it: the elementwise work, by issue and latency, as in the
 // forward pass: 1.2 us a 128 x 128 tile in dq_kernel and 1.8 in dkdv_kernel
 // at d = 128 without masks, where the 3 and 4 products take 0.75 and 1.0.
-// Measured (dq, dkdv), bf16:
-//   B2 H16 kv4 4096 d128 window 1024 cap 50    130, 177 us
-//   B1 H16 8192 d128 documents of about 700    113, 134 us
-//   B1 H16 4096 d128 learned bias, no mask     167, 228 us (1230 and 1210 TFLOP/s
-//     as executed; 870 together for the 5 products that the mathematics asks for)
-//   B8 H12 512 d64 learned bias                 28,  49 us;  table sums 5 us
+// Measured (dq, dkdv), bf16, kernel times:
+//   B2 H16 kv4 4096 d128 window 1024 cap 50    131, 177 us
+//   B1 H16 8192 d128 documents of about 700    114, 136 us
+//   B1 H16 4096 d128 learned bias, no mask     169, 232 us (1220 and 1190 TFLOP/s
+//     as executed; 860 together for the 5 products that the mathematics asks for)
+//   B8 H12 512 d64 learned bias                 28,  48 us;  table sums 5 us
 //   B4 H8 kv2 381 d64 fp16 prefix                8,  14 us
+//   B4 H16 2048 d128 causal: plain 116, 136; cap 135, 172; slopes 124, 156; cap and
+//     slopes 158, 207 us;  d64: 88, 101; 111, 139; 97, 120; 133, 170 us
 #pragma once
 
 #include <cmath>

@@ -25,6 +25,10 @@
 //
 // O leaves through the query tile's place in shared memory and TMA stores.
 //
+// P is rounded to 16 bits, the width of the MMA's operand, before P V; its sum and
+// everything else stay in fp32.  O is then off by about 1.4 times the rounding of
+// a right result (bf16, against 64 bits: 0.0023 to 0.0024 of its size, 0.0017).
+//
 // What bounds it: the softmax between a score tile's two products, by issue
 // and latency (two tiles a CTA hide each other's products, not all of each
 // other's softmax).  Per 128 x 128 tile the products take 512 cycles each at
@@ -34,12 +38,14 @@
 // 16-element MMA step and nothing per score; a learned bias one packed FMA's
 // operand from shared memory within its range and a constant beyond.
 //
-// Measured (bf16, causal unless noted; "of measured" is the copy and dense
-// bf16 matrix rate of this GPU type, 6.78 TB/s and 1940 TFLOP/s):
-//   B1 H32 kv8 8192 d128 cap 50       444 us, 1238 TFLOP/s, 64 % of measured
-//   B4 H16 2048 d128 plain / cap / slopes / both      70 / 101 / 82 / 141 us
-//   B4 H16 2048 d64  plain (no mask) / cap / slopes / both   93 / 91 / 71 / 123 us
-//   B4 H16 1501 d64 fp16 learned bias  52 us;  B1 H16 4096 d128, no mask, 115 us
+// Measured (bf16, causal unless noted; GPU time of the mask plan and this kernel
+// replayed as a graph, scores of standard deviation 2; "of measured" is the dense
+// bf16 matrix rate of this GPU type, 1940 TFLOP/s):
+//   B1 H32 kv8 8192 d128 cap 50       446 to 452 us, 1220 TFLOP/s, 63 % of measured
+//   B4 H16 2048 d128 plain / cap / slopes / both   74 / 98 / 82 / 133 us
+//   B4 H16 2048 d64  plain / cap / slopes / both   61 / 86 / 67 / 114 us
+//   the last without a mask, plain                 95 us
+//   B4 H16 1501 d64 fp16 learned bias  53 us;  B1 H16 4096 d128, no mask, 112 us
 // A unit of 256 rows costs 3 us before its first score and 2 us after its last
 // besides (about 5 steps of such a pair of tiles in all at d = 64).
 #pragma once

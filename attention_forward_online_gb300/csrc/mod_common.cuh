@@ -32,6 +32,8 @@ enum ScoreMode : int {
   kModRel = 4,
   kModRelWide = 5  // forward and dQ at d = 128: ranges above kSmallRel
 };
+// Up to this range the table fits beside five K/V stages at d = 128 (180 would);
+// 128 is where tables of bucketed distances commonly end.
 constexpr int kSmallRel = 128;
 __host__ __device__ constexpr bool mode_cap(int m) { return m == kModCap || m == kModCapSlopes; }
 __host__ __device__ constexpr bool mode_slopes(int m) { return m == kModSlopes || m == kModCapSlopes; }

@@ -272,9 +272,9 @@ struct TileScore {
 
   // The same for a masked tile by a rolled loop that reads each chunk from
   // tensor memory twice: a third of the instructions, for tiles that a CTA
-  // meets once or twice, whose code then comes from far (a tree of 27 drafts
-  // over 6000 keys: 50 us against 57; a prompt's many masked tiles would be 10
-  // to 25 % slower).
+  // meets once or twice, whose code then comes from far (8 trees of 27 drafts over
+  // 6000 keys: 58 us against 65; a prompt's many masked tiles would be 10 to 25 %
+  // slower).
   // kFine: with the cap's polynomial where a chunk's scores are small, for caps
   // above 64: the other form is off by up to 2^-20 of the cap, 6e-5 at a cap of 64.
   // (Its code costs: with it for all caps that tree, cap 30, takes 3 us more.)

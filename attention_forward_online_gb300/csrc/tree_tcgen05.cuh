@@ -27,17 +27,18 @@
 // 13 MMA issue; 15 what masks leave.  Tensor memory: S0, S1 (P in 16 bits over
 // them), O0, O1.
 //
-// Measured (bf16; "of measured": of this GPU type's copy rate, 6.78 TB/s):
-//   B64 H32 kv8 T1 ctx 4096 .. 8192 d128   258 to 265 us, 6.1 to 6.25 TB/s, 90 to
+// Measured (bf16; GPU time of both kernels replayed as a graph; "of measured": of
+// this GPU type's copy rate, 6.78 TB/s):
+//   B64 H32 kv8 T1 ctx 4096 .. 8192 d128   258 to 267 us, 6.05 to 6.25 TB/s, 89 to
 //     92 % of measured
-//   B8 H32 kv8 T27 ctx 3000 .. 6000 d128 cap 30, pages of 32    57 us, 39 %:
+//   B8 H32 kv8 T27 ctx 3000 .. 6000 d128 cap 30, pages of 32    58 us, 38 %:
 //     the first scores come after 9 us (every CTA's 6 slots fill together), the
 //     tiles at 5.3 TB/s after that, the last tile's softmax, the partial and the
 //     join take 12
-//   B2 H16 kv2 T64 ctx 50000 .. 100000 d64 fp16 slopes    87 us: 4 row tiles a
+//   B2 H16 kv2 T64 ctx 50000 .. 100000 d64 fp16 slopes    85 us: 4 row tiles a
 //     key head, bound by their softmax
-//   B1 H32 kv8 T1 ctx 700 d128   12 us, latency
-//   B300 H8 kv8 T1 ctx 300 d64  131 us: 8 us a unit of 3 tiles, the chain from
+//   B1 H32 kv8 T1 ctx 700 d128   12.5 us, latency
+//   B300 H8 kv8 T1 ctx 300 d64  132 us: 8 us a unit of 3 tiles, the chain from
 //     its scores to its output, which units of one CTA do not overlap
 #pragma once
 
@@ -573,8 +574,7 @@ __device__ __forceinline__ void correction_role(const Params& p, Bars* bars, uin
 // A warp of its own, some segments ahead: in the producers or the correction warps
 // this costs registers and code (one token over 700 keys, without masks, 12.5 ->
 // 13.2 us), and waiting for each segment's end it takes issue slots from the
-// softmax (8 trees of 27 drafts over 6000 keys 57.6 -> 60.4 us; without masks'
-// leavings, which let NaN from unseen keys through, 56).
+// softmax (8 trees of 27 drafts over 6000 keys 57.6 -> 60.4 us).
 __device__ __forceinline__ void seen_role(const Params& p, Bars* bars, WaitCtl wc) {
   if (!p.mask) return;
   const int lane = threadIdx.x & 31;

@@ -545,8 +545,10 @@ int osattn_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* 
  * get zeros, whatever Q, dO, K and V hold there (K and V under the rule of
  * osattn_fwd_mod; a non-finite Q or dO row that sees a key reaches dK and dV
  * of the whole 128-key tile).  dQ takes D = rowsum(dO O) with O as given, in 16
- * bits; without a cap dK and dRel take it corrected by the row's sum of dy.  No
- * atomics: the same call gives the same bits.
+ * bits; without a cap dK and dRel take it corrected by the row's sum of dy, which
+ * is 0 for the O and LSE of all keys that the row sees (an LSE over more keys
+ * than the call's would make them wrong).  No atomics: the same call gives the
+ * same bits.
  *
  *   dRel       device [rel_num, H], element type `dtype` (written), exactly
  *              when score->rel_table is given, else NULL
