@@ -25,7 +25,7 @@
 // magnitudes of 128; terms 2^-25 below the greatest of an addition are lost.)
 // The scale of a V block goes into the exponent, p s_v = 2^(x + log2 s_v - m), with m
 // the running max of that sum: blocks of any scales meet in one accumulator.  l takes
-// p, which is the weight over s_v.
+// p, which is the weight over s_v, times 2^-20 (see kSumUnit).
 //
 // As for 16-bit pages, one CTA per SM is persistent over its share of the list of key
 // tiles of all (sequence, key head, row tile) units (tree_walk.cuh); partials are
@@ -81,6 +81,10 @@ constexpr float kTop = 10.f;    // weights are formed as 2^10 times themselves,
 constexpr float kMost = 15.8f;  // and m moves before they pass e5m2's 57344 (2^15.8 = 57052)
 constexpr float kNoPage = -1.f;
 constexpr float kLeastScale = 7.8886090522101181e-31f;  // 2^-100
+// l is summed as 2^-20 weight / s_v: up to 2^(15.8 + 100 - 20) a key, so that 2^30 keys of the
+// least scale, a block of zeros', stay below 2^127.  (Without the 2^-20 some 4700 keys
+// passed it.)  At s_v = 2^112 a row's greatest key still adds 2^-122; fp32 loses bits from there on.
+constexpr float kSumLog2 = -20.f, kSumUnit = 9.5367431640625e-07f;
 
 enum : uint32_t {
   kSiteQ = 101,
@@ -431,7 +435,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Sh* sh, uint8_t* s
         vs = 1.f;
       }
       vs = vs < kLeastScale ? kLeastScale : vs;  // (values of a scale of 0 are 0, and their keys count all the same)
-      const float lv = seen ? lg2_approx(vs) : 0.f, inv = seen ? rcp_approx(vs) : 0.f;
+      const float lv = seen ? lg2_approx(vs) : 0.f, inv = seen ? kSumUnit * rcp_approx(vs) : 0.f;
       const uint64_t ks2 = f2_pack(ks, ks), lv2 = f2_pack(lv, lv), inv2 = f2_pack(inv, inv);
       const uint64_t finer2 = f2_pack(0.0625f, 0.0625f);
       [[maybe_unused]] const uint64_t before2 = f2_pack(before, before);
@@ -665,10 +669,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Sh* sh, uint8_t* s
         const float l1 = (sh->l[1][0][row] + sh->l[1][1][row]) + (sh->l[1][2][row] + sh->l[1][3][row]);
         const float L = fmaf(l0, f0, l1 * f1);
         const bool empty = L == 0.f || tab.sees[row] == 0;
-        const float rcp = empty ? 0.f : 1.f / L;
+        const float rcp = empty ? 0.f : kSumUnit / L;
         e.f[0] = f0 * rcp;
         e.f[1] = f1 * rcp;
-        e.lse = empty ? -INFINITY : (M + (log2f(L) - kTop)) * kLn2;
+        e.lse = empty ? -INFINITY : (M + (log2f(L) - (kTop + kSumLog2))) * kLn2;
         e.tok = (row0 + row) / p.group;
         e.h = w.hk * p.group + (row0 + row) - e.tok * p.group;
         if (quarter == 0) {

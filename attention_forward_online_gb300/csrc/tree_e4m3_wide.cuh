@@ -53,7 +53,7 @@ enum : uint32_t { kSiteReady = 121, kSitePrepare = 122 };
 
 // What the 8 keys of a chunk share.
 struct __align__(16) Chunk {
-  float ks, lv, inv, none;  // K's scale, log2 of V's and its reciprocal
+  float ks, lv, inv, none;  // K's scale, log2 of V's and kSumUnit over it
 };
 
 struct __align__(16) Shared {
@@ -387,7 +387,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, uint32
     const float f0 = s0.x == -INFINITY ? 0.f : ex2_approx(s0.x - M), f1 = s1.x == -INFINITY ? 0.f : ex2_approx(s1.x - M);
     const float L = fmaf(s0.y, f0, s1.y * f1);
     const bool empty = L == 0.f || !sees;
-    const float rcp = empty ? 0.f : 1.f / L, g0 = f0 * rcp, g1 = f1 * rcp;
+    const float rcp = empty ? 0.f : kSumUnit / L, g0 = f0 * rcp, g1 = f1 * rcp;
     const bool whole = !at.head_cut && !at.tail_cut;
     const long long part_row = (2 * static_cast<long long>(blockIdx.x) + (at.head_cut ? 0 : 1)) * p.tile_rows + row;
     constexpr int kHalf = HD / 2;
@@ -429,7 +429,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, uint32
     tc_fence_before_sync();
     mbar_arrive(&sh->o_empty);
     if (live && t == 0) {
-      const float lse = empty ? -INFINITY : (M + (log2f(L) - kTop)) * kLn2;
+      const float lse = empty ? -INFINITY : (M + (log2f(L) - (kTop + kSumLog2))) * kLn2;
       if (whole) p.LSE[(static_cast<long long>(at.b) * p.H + h) * p.T + tok] = lse;
       else p.lse_part[part_row] = lse;
     }
@@ -548,7 +548,7 @@ __device__ __forceinline__ void prepare_role(const Params& p, Shared* sh, uint8_
           vs = 1.f;
         }
         vs = vs < kLeastScale ? kLeastScale : vs;  // (values of a scale of 0 are 0, and their keys count all the same)
-        const Chunk of = any ? Chunk{ks, lg2_approx(vs), rcp_approx(vs), 0.f} : Chunk{0.f, 0.f, 0.f, 0.f};
+        const Chunk of = any ? Chunk{ks, lg2_approx(vs), kSumUnit * rcp_approx(vs), 0.f} : Chunk{0.f, 0.f, 0.f, 0.f};
         sh->chunk[slot][me] = of;
         float k_most = fabsf(of.ks), lv_most = of.lv;
 #pragma unroll

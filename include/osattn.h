@@ -637,7 +637,8 @@ int osattn_tree_attn(const void* Q, const void* K_pages, const void* V_pages,
  *              of the page, head and row axes in elements, multiples of 16
  *   K_scale, V_scale   device fp32 [num_pages, Hkv, page_size / scale_block]
  *              contiguous, finite where a draft sees a key, and V_scale not
- *              negative (below 2^-100 it counts as that)
+ *              negative (below 2^-100 it counts as that; above 2^112 the sums
+ *              of weights lose bits)
  *   scale_block   a divisor of page_size
  *   dtype      of Q and O: OSATTN_BF16 or OSATTN_FP16
  *   workspace  osattn_tree_e4m3_workspace_bytes(...) bytes
