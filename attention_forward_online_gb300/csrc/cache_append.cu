@@ -244,10 +244,12 @@ __device__ __forceinline__ void store_unit(const Params& p, const uint64_t* turn
       __syncwarp();
     }
     float scale = scale_of(amax);
-    const bool older = had > 0.f && had <= 3.402823466e38f;
-    if (older && had >= scale) scale = had;
-    if (older && had < scale) {
-      const float by = had / scale;
+    if (had >= scale && had <= 3.402823466e38f) {
+      scale = had;
+    } else if (ctx > x0) {
+      // (the older rows are `had` times their codes, zeros if it is 0; a negative one that the new
+      // scale does not reach, an infinite one or NaN leaves nothing of them but NaN)
+      const float by = fabsf(had) <= scale ? had / scale : __uint_as_float(0x7fc00000u);
       for (int r = row0 + tid / kSlots; r < row0 + ctx - x0; r += kTok) {
         uint4* q = reinterpret_cast<uint4*>(dst + r * p.page_s[which][2] + 16 * slot);
         uint4 w = *q;

@@ -713,8 +713,10 @@ int osattn_rotary(const void* Q, const void* K, void* Q_out, void* K_out, int B,
  * of its new rows at most 448 s (2^-100 for zeros), and values are rounded once,
  * from fp32; infinities become 448 s, NaN stays.  A block whose first rows are
  * older (places before ctx_len[b]) keeps its scale unless the new rows need a
- * greater one; then its older rows are brought to that, rounded once.  The scale
- * of a block without older rows is not read.
+ * greater one; then its older rows are brought to that, rounded once (to zeros
+ * from a scale of 0, with their signs from a negative one).  A scale there that is
+ * NaN, infinite, or negative and greater in magnitude than the new rows' leaves
+ * the older rows as NaN.  The scale of a block without older rows is not read.
  *
  * Nothing else in the pages is written.  A sequence whose n rows do not fit the
  * table, or a negative ctx_len, or a page outside [0, num_pages), leaves its

@@ -1,6 +1,9 @@
 """The older rows of a block that an append adds to (osattn_cache_append, e4m3 pages): as
 they were where the block keeps its scale, rounded once to a greater one, whether a warp
-(16 new tokens or fewer) or a thread block takes the unit."""
+(16 new tokens or fewer) or a thread block takes the unit, and for scales that
+say nothing."""
+import math
+
 import pytest
 import torch
 
@@ -66,3 +69,50 @@ def test_older_rows_stay_or_are_rounded_once(d, page, block, ctx, T, turned):
             kept, grown = kept + x[0], grown + x[1]
     assert kept and grown  # both happened
     untouched(c, raw, B, ctx, [T] * B)
+
+
+@pytest.mark.parametrize("T", [1, 17])
+def test_older_rows_of_a_scale_of_zero_are_zeros(T):
+    # as the attention call reads them, before and after
+    c = Cache(1, 2, 64, 64, 128, BF, 64)
+    k, v = (torch.ones(1, 2, T, 64, dtype=BF, device=DEV) for _ in range(2))
+    for x in (c.k, c.v):
+        raw = x.view(torch.uint8)
+        raw[(raw & 0x7f) == 0x7f] = 0x30
+    for s in (c.ks, c.vs):
+        s.zero_()
+    c.append(k, v, [40])
+    for x, s in ((c.k, c.ks), (c.v, c.vs)):
+        assert (c.factors(s, 0, 0, 1) == 2.0 ** -8).all()
+        assert not c.rows(x, 0, 0, 40).any()
+        assert (c.rows(x, 0, 40, 40 + T) == 256.0).all()
+
+
+@pytest.mark.parametrize("T", [1, 17])
+@pytest.mark.parametrize("exponent", [-20, -8])
+def test_older_rows_of_a_negative_scale_keep_their_signs(exponent, T):
+    c = Cache(1, 2, 64, 64, 128, BF, 64)
+    k, v = (torch.ones(1, 2, T, 64, dtype=BF, device=DEV) for _ in range(2))
+    for s in (c.ks, c.vs):
+        s.fill_(-2.0 ** exponent)
+    was = [c.rows(x, 0, 0, 40) for x in (c.k, c.v)]
+    c.append(k, v, [40])
+    for x, s, old in zip((c.k, c.v), (c.ks, c.vs), was):
+        assert (c.factors(s, 0, 0, 1) == 2.0 ** -8).all()
+        want, got = (-old * 2.0 ** (exponent + 8)).float().to(E4).double(), c.rows(x, 0, 0, 40)
+        assert ((got == want) | (got.isnan() & want.isnan())).all()
+
+
+@pytest.mark.parametrize("T", [1, 17])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, -1.0])
+def test_older_rows_without_a_scale_are_nan(bad, T):
+    # no scale that the new rows can have gives them their values back
+    c = Cache(1, 2, 128, 64, 128, FP, 64)
+    k, v = (torch.ones(1, 2, T, 128, dtype=FP, device=DEV) for _ in range(2))
+    for s in (c.ks, c.vs):
+        s.fill_(bad)
+    c.append(k, v, [40])
+    for x, s in ((c.k, c.ks), (c.v, c.vs)):
+        assert (c.factors(s, 0, 0, 1) == 2.0 ** -8).all()
+        assert c.rows(x, 0, 0, 40).isnan().all()
+        assert (c.rows(x, 0, 40, 40 + T) == 256.0).all()
