@@ -387,6 +387,8 @@ extern "C" int osattn_cache_append(const void* K, const void* V, const void* Q, 
       (Q && (api_strides(q_strides, H, T, d, dtype, qs) != OSATTN_OK ||
              api_strides(qo_strides, H, T, d, dtype, qos) != OSATTN_OK)))
     return OSATTN_ERR_INVALID_ARG;
+  if (Q && Q == Q_out && ((B > 1 && qs[0] != qos[0]) || (H > 1 && qs[1] != qos[1]) || (T > 1 && qs[2] != qos[2])))
+    return OSATTN_ERR_INVALID_ARG;  // (a row would be written before another thread has read it)
   ApiDevice dev;
   const int rc = api_device(&dev);
   if (rc != OSATTN_OK) return rc;

@@ -145,7 +145,8 @@ bool fill_rows(rotary::Rows* r, const void* in, void* out, int B, int heads, int
   long long i[3], o[3];
   if (!row_strides(is, B, heads, N, d, false, i) || !row_strides(os, B, heads, N, d, true, o)) return false;
   *r = rotary::Rows{in, out, i[0], i[1], i[2], o[0], o[1], o[2], heads};
-  return true;
+  // In place with other strides a row would be written before another thread has read it.
+  return in != out || (i[0] == o[0] && i[1] == o[1] && i[2] == o[2]);
 }
 
 }  // namespace osattn

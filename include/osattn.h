@@ -678,6 +678,7 @@ typedef struct osattn_rotation {
  *   Q, Q_out   device [B, H, N, d] with (b, h, row) element strides (NULL:
  *              contiguous); those of Q may be 0, those of Q_out at least 1 where
  *              the axis is longer than 1; Q_out may be Q with the same strides
+ *              (with others it is refused)
  *   K, K_out   device [B, Hkv, N, d] likewise; Hkv = 0: none
  *   positions  device int32 [N], or [B, N] with batch_positions, or NULL: row n
  *              stands at offset + n
@@ -701,7 +702,8 @@ int osattn_rotary(const void* Q, const void* K, void* Q_out, void* K_out, int B,
  *   K, V       device [B, Hkv, T, d], element type `dtype`, strides as for
  *              osattn_fwd_strided
  *   Q, Q_out   device [B, H, T, d] likewise, or both NULL; needs a rotation; all
- *              T rows are written.  Q_out may be Q
+ *              T rows are written.  Q_out may be Q with the same strides (with others
+ *              it is refused)
  *   positions  device int32 [B, T] for the rotation (a tree's drafts stand at
  *              their depths), or NULL: ctx_len[b] + t
  *   K_pages, V_pages, page_table   as for osattn_tree_attn, cache_dtype being
