@@ -127,8 +127,8 @@ cudaError_t launch(const TreeE4m3Args& a, const CUtensorMap& k, const CUtensorMa
   p.group = a.H / a.Hkv;
   p.T = a.T;
   p.rows = a.T * p.group;
-  // The form for few rows up to 16 of them (H32 kv8 d128, 16 rows: B8 ctx 6000 35 us, 49 in
-  // the other form, B64 ctx 4000 111 and 176); then the other, which reads a key once for 128
+  // The form for few rows up to 16 of them (H32 kv8 d128, 16 rows: B8 ctx 6000 36.5 us, 49
+  // in the other form, B64 ctx 4000 112 and 176); then the other, which reads a key once for 128
   // rows (20 rows: B64 ctx 4000 174 us, 193 as two tiles, B8 ctx 6000 48 and 47; B2 H16 kv2
   // ctx 100000 d64, 64 rows: 43, 72 as four tiles).
   const bool many = p.rows > kTreeE4m3FewRows && a.block % wide::kChunk == 0;

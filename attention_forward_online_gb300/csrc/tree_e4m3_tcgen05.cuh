@@ -16,10 +16,9 @@
 //   q 2^k = q0 + q1 / 16 (+ q2 / 256 for fp16) in e4m3, 2^k bringing a row to
 //     [128, 256): 8 (11) bits are 4 + 4 (+ 3), so all are kept, down to 2^-21 of the
 //     row's greatest element
-//   w = p s_v, rounded to fp16, = w0 + w1 + w2 in e5m2: 3 + 4 + 4 bits with the signs of
-//     the remainders, so fp16's 11 are kept; e5m2 is fp16's upper byte, and its range
-//     down to 2^-27 of the row's greatest weight needs no scales (e4m3 terms would stop
-//     at 2^-22 or, scaled, 2^-26, and cost conversions)
+//   w = p s_v, rounded to fp16, = w0 + w1 / 8 + w2 / 128 in e5m2: 3 + 4 + 4 bits with the signs
+//     of the remainders, so fp16's 11 are kept, down to 2^-34 of the row's greatest weight
+//     (unscaled terms would stop at 2^-27, e4m3 ones at 2^-22 or, scaled, 2^-26)
 // The products of a term have accumulators of their own, added up in fp32 when they
 // are read.  (Measured: the tensor cores add e4m3 products to 2^-21.5 of the sum of
 // magnitudes of 128; terms 2^-25 below the greatest of an addition are lost.)
@@ -43,8 +42,8 @@
 // of this GPU type's copy rate, 6.78 TB/s):
 //   B64 H32 kv8 T1 ctx 4096 .. 8192 d128, a token's heads side by side  137 to 139 us,
 //     5.8 TB/s, 86 % of measured (the same over 16-bit pages: 258 to 267 us)
-//   B64 H32 kv8 T1 ctx 4000 d128  96 us; T4 (16 rows) 111 us
-//   B8 H32 kv8 ctx 6000 d128  4 rows 29 us, 16 rows 35 us
+//   B64 H32 kv8 T1 ctx 4000 d128  96 us; T4 (16 rows) 112 us
+//   B8 H32 kv8 ctx 6000 d128  4 rows 29 us, 16 rows 36.5 us
 //   B1 H32 kv8 T1 d128  ctx 700 14.4 to 16 us, ctx 32000 25 us, ctx 100000 48 us
 //
 // Warps 0-3 and 4-7: softmax of the even and odd tiles; 8 and 9: TMA loads of the even and
@@ -79,6 +78,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTop = 10.f;    // weights are formed as 2^10 times themselves,
 constexpr float kMost = 15.8f;  // and m moves before they pass e5m2's 57344 (2^15.8 = 57052)
+constexpr float kFine1 = 8.f, kFine2 = 128.f;  // see weights_of
 constexpr float kNoPage = -1.f;
 constexpr float kLeastScale = 7.8886090522101181e-31f;  // 2^-100
 // l is summed as 2^-20 weight / s_v: up to 2^(15.8 + 100 - 20) a key, so that 2^30 keys of the
@@ -279,13 +279,37 @@ __device__ __forceinline__ void terms_of(__half2 x, uint16_t* term) {
   }
 }
 
+// Two halves as e5m2.
+__device__ __forceinline__ uint16_t e5m2_of(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  return r;
+}
+
 // Four non-negative fp16 values (lo: 0 and 1) as three e5m2 terms whose sum they are: a
 // term is the value's upper byte, rounded; the remainder is exact in fp16, and after two
 // terms there are 3 bits of it, or less than half of e5m2's least value.
+// kFine: the value is term[0] + term[1] 2^-3 + term[2] 2^-7, which fills e5m2's range from above
+// (remainders of values up to 2^15.8 are at most 2^12 and 2^8) and keeps all but 2^-24 of
+// values below its least step, too.  (Without the factors the part of 100000 keys 2^-26 below
+// the row's greatest was off by 40 %; B8 H32 kv8 ctx 6000 d128, 16 rows 35.1 us without, 36.5
+// with them, 4 rows 29 us either way.)
+template <bool kFine>
 __device__ __forceinline__ void weights_of(uint32_t lo, uint32_t hi, uint32_t* term) {
   __half2 x[2] = {*reinterpret_cast<__half2*>(&lo), *reinterpret_cast<__half2*>(&hi)};
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
+    if constexpr (kFine) {
+      if (i > 0) {
+        const __half2 finer = __float2half2_rn(i == 1 ? kFine1 : kFine2 / kFine1);
+        x[0] = __hmul2(x[0], finer);
+        x[1] = __hmul2(x[1], finer);
+      }
+      if (i == 2) {  // (a cvt: NaN has to stay)
+        term[2] = __byte_perm(e5m2_of(x[0]), e5m2_of(x[1]), 0x5410);
+        return;
+      }
+    }
     uint32_t e[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -531,8 +555,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Sh* sh, uint8_t* s
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             uint32_t term[2][3];
-            weights_of(h[4 * g], h[4 * g + 1], term[0]);
-            weights_of(h[4 * g + 2], h[4 * g + 3], term[1]);
+            weights_of<true>(h[4 * g], h[4 * g + 1], term[0]);
+            weights_of<true>(h[4 * g + 2], h[4 * g + 3], term[1]);
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
               const int col = out_col<NG>(g & ~1, c);
@@ -700,7 +724,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Sh* sh, uint8_t* s
         const typename Sh::End e = sh->end[t][quarter][4 * g + r];
         if (e.h < 0) continue;
         auto sum = [&](int s) {
-          return (__uint_as_float(a[s][r]) + __uint_as_float(a[s][4 + r])) + __uint_as_float(a[s][8 + r]);
+          return fmaf(__uint_as_float(a[s][8 + r]), 1.f / kFine2, fmaf(__uint_as_float(a[s][4 + r]), 1.f / kFine1, __uint_as_float(a[s][r])));
         };
         float o = sum(0) * e.f[0];
         if (w.n > 1) o = fmaf(sum(1), e.f[1], o);

@@ -12,7 +12,8 @@
 //   q 2^k = q0 in e4m3 + q1 (+ q2 for fp16) in e5m2, 2^k bringing a row to [128, 256):
 //     with the remainders' signs 4 + 4 (+ 3) bits, so elements down to 2^-13 of the
 //     row's greatest are exact, smaller ones to 2^-21 of it
-//   w = p s_v as in the first form: fp16, as three e5m2 terms
+//   w = p s_v in fp16, as three e5m2 terms of one sum: to half of e5m2's least step, 2^-27 of
+//     the row's greatest weight (the first form, with an accumulator a term, goes to 2^-34)
 //
 // What bounds it: the softmax (half of the issue slots, most of the rest of its time waiting
 // for what it has issued), and behind it the chain from one tile's weights over 18 to 24
@@ -348,7 +349,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, uint32
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t term[3];
-              weights_of(h2[2 * j], h2[2 * j + 1], term);
+              weights_of<false>(h2[2 * j], h2[2 * j + 1], term);
 #pragma unroll
               for (int x = 0; x < 3; ++x) out[8 * x + 2 * c + j] = term[x];
             }

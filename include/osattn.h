@@ -643,7 +643,10 @@ int osattn_tree_attn(const void* Q, const void* K_pages, const void* V_pages,
  *   dtype      of Q and O: OSATTN_BF16 or OSATTN_FP16
  *   workspace  osattn_tree_e4m3_workspace_bytes(...) bytes
  * Pages and scales may hold anything (NaN included) at positions that no draft
- * sees.
+ * sees.  Of the weights of V, probabilities times V_scale, those below 2^-34 of the
+ * greatest of a CTA's part of a row (2^-26 with more than 16 query rows T H / Hkv
+ * and blocks of 8 tokens or more) may count in LSE and not in O: with N keys there
+ * O is off by at most N times that of max |V|.
  */
 size_t osattn_tree_e4m3_workspace_bytes(int B, int H, int Hkv, int T, int d);
 int osattn_tree_attn_e4m3(const void* Q, const void* K_pages, const void* V_pages,
