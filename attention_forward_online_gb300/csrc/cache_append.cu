@@ -57,7 +57,6 @@ struct Params {
 };
 
 // The place of chunk `slot` (16 elements: two vectors of 8) of a row.
-template <int HD>
 __device__ __forceinline__ void slot_at(const Params& p, int slot, int& at0, int& at1) {
   at0 = 16 * slot;
   at1 = at0 + 8;
@@ -162,7 +161,7 @@ __device__ __forceinline__ void store_unit(const Params& p, const uint64_t* turn
   const uint16_t* in = static_cast<const uint16_t*>(p.in[which]) + b * p.in_s[which][0] + hk * p.in_s[which][1];
   const int slot = tid % kSlots;
   int at0, at1;
-  slot_at<HD>(p, slot, at0, at1);
+  slot_at(p, slot, at0, at1);
   auto fetch = [&](int x, Slot<E>& raw) {
     const uint16_t* row = in + (x - ctx) * p.in_s[which][2];
     raw.v0.load(row + at0);

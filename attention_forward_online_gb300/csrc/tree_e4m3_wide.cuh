@@ -54,7 +54,7 @@ enum : uint32_t { kSiteReady = 121, kSitePrepare = 122 };
 
 // What the 8 keys of a chunk share.
 struct __align__(16) Chunk {
-  float ks, lv, inv, none;  // K's scale, log2 of V's and kSumUnit over it
+  float ks, lv, inv;  // K's scale, log2 of V's and kSumUnit over it
 };
 
 struct __align__(16) Shared {
@@ -549,7 +549,7 @@ __device__ __forceinline__ void prepare_role(const Params& p, Shared* sh, uint8_
           vs = 1.f;
         }
         vs = vs < kLeastScale ? kLeastScale : vs;  // (values of a scale of 0 are 0, and their keys count all the same)
-        const Chunk of = any ? Chunk{ks, lg2_approx(vs), kSumUnit * rcp_approx(vs), 0.f} : Chunk{0.f, 0.f, 0.f, 0.f};
+        const Chunk of = any ? Chunk{ks, lg2_approx(vs), kSumUnit * rcp_approx(vs)} : Chunk{0.f, 0.f, 0.f};
         sh->chunk[slot][me] = of;
         float k_most = fabsf(of.ks), lv_most = of.lv;
 #pragma unroll
