@@ -30,7 +30,11 @@ namespace append {
 constexpr unsigned kBadArg = 1u;  // OSATTN_ERR_INVALID_ARG in the status word
 constexpr int kThreads = 256;
 constexpr int kLeastExp = -100;   // of the scale of a block of zeros
-constexpr int kHeld = 2;          // sweeps over a block whose values stay in registers (64 tokens of 128)
+// Sweeps over a block whose values stay in registers: 64 tokens of 128 elements in a thread
+// block, 8 in a warp; what lies beyond is read and turned twice.  (4 x 2048 whole tokens, H32 kv8 d128
+// into e4m3 pages: blocks of 64 43 us, 47 with one sweep held and 49 with four; of 128 43, 45 and 43;
+// 64 sequences of 16 tokens 14.4 us, 14.4 and 13.0.)
+constexpr int kHeld = 2;
 constexpr int kHalfChunk = 64;    // tokens of a 16-bit unit
 
 struct Params {
@@ -92,7 +96,8 @@ __device__ __forceinline__ void turn_slot(const Params& p, const uint64_t* turn,
     else rotary::turn_pairs<8>(y, false, c, s);
     return;
   }
-  // pairs that lie anywhere: each element with the other of its pair
+  // pairs that lie anywhere: each element with the other of its pair, and its own sine and
+  // cosine (4 x 2048 tokens, H32 kv8 d128, 24 elements turned: 121 us, where 16 or 32 take 43)
 #pragma unroll 1
   for (int i = 0; i < 16; ++i) {
     const int e = 16 * slot + i;
@@ -316,7 +321,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
 
 template <class E, int HD>
 cudaError_t launch(Params& p, bool e4m3, bool queries, int num_sms, cudaStream_t stream) {
-  // a warp for each unit where a sequence brings few rows, else a block
+  // A warp for each unit where a sequence brings few rows, else a block (H32 kv8 d128 into e4m3
+  // pages: 64 sequences of 1 row 6.2 us as warps, 10.3 as blocks, of 16 14.4 and 16.4, of 32 24.6 and
+  // 18.5; 8 sequences of 16 10.3 and 6.2, of 8 6.2 either way).
   const bool warps = p.T <= 16;
   const int group = warps ? 32 : kThreads;
   const long long units = 2ll * p.B * p.blocks * p.Hkv;

@@ -40,7 +40,7 @@
 // large, before that by the chain of two launches, page numbers, tiles and the join.
 // Measured (bf16, blocks of 64, GPU time of both kernels replayed as a graph; "of measured":
 // of this GPU type's copy rate, 6.78 TB/s):
-//   B64 H32 kv8 T1 ctx 4096 .. 8192 d128, a token's heads side by side  137 to 139 us,
+//   B64 H32 kv8 T1 ctx 4096 .. 8192 d128, a token's heads side by side  137 to 140 us,
 //     5.8 TB/s, 86 % of measured (the same over 16-bit pages: 258 to 267 us)
 //   B64 H32 kv8 T1 ctx 4000 d128  96 us; T4 (16 rows) 112 us
 //   B8 H32 kv8 ctx 6000 d128  4 rows 29 us, 16 rows 36.5 us

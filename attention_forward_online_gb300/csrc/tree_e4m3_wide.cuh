@@ -21,10 +21,10 @@
 // over a tile is a loop of 32 keys: unrolled over all 128, with m decided from weights at
 // hand, it waited for instructions (B2 T64 below: 177 us).
 // Measured (GPU time of both kernels replayed as a graph):
-//   B8 H32 kv8 T27 ctx 3000 .. 6000 d128 cap 30 bf16, blocks of 32  61.5 us, as much as over
-//     16-bit pages (58)
+//   B8 H32 kv8 T27 ctx 3000 .. 6000 d128 cap 30 bf16, blocks of 32  60 to 62 us (16-bit
+//     pages: 58)
 //   B2 H16 kv2 T64 ctx 50000 .. 100000 d64 fp16 slopes  115 us, 2600 cycles a tile (16-bit
-//     pages: 85 us)
+//     pages: 85 us): who drafts wide trees over long contexts keeps 16-bit pages
 //   B8 H32 kv8 ctx 6000 d128 bf16  20 rows 47 us, 64 rows 50 us, 128 rows 60 us
 //   B64 H32 kv8 ctx 4000 d128 bf16  20 rows 176 us, 64 rows 184 us, 128 rows 207 us
 //

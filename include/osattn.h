@@ -628,7 +628,10 @@ int osattn_tree_attn(const void* Q, const void* K_pages, const void* V_pages,
 
 /*
  * osattn_tree_attn_e4m3 - osattn_tree_attn over pages of e4m3 values, one fp32
- * scale for each block of scale_block tokens of a page and key head: the key at
+ * scale for each block of scale_block tokens of a page and key head.  A step of few
+ * query rows a key head takes half the time of 16-bit pages over long contexts;
+ * trees of 17 rows and more take up to a third longer than there, for half the
+ * memory.  The key at
  * row r of a page is K_scale[page][head][r / scale_block] times the values of
  * K_pages there, and likewise V.  Everything else is as for osattn_tree_attn:
  * masks, positions, window, cap, slopes, shared heads, pages that do not exist.
@@ -646,7 +649,7 @@ int osattn_tree_attn(const void* Q, const void* K_pages, const void* V_pages,
  * sees.  Of the weights of V, probabilities times V_scale, those below 2^-34 of the
  * greatest of a CTA's part of a row (2^-26 with more than 16 query rows T H / Hkv
  * and blocks of 8 tokens or more) may count in LSE and not in O: with N keys there
- * O is off by at most N times that of max |V|.
+ * O is off by at most N times that of max |V|.  Those below 2^-136 count in neither.
  */
 size_t osattn_tree_e4m3_workspace_bytes(int B, int H, int Hkv, int T, int d);
 int osattn_tree_attn_e4m3(const void* Q, const void* K_pages, const void* V_pages,
